@@ -10,6 +10,7 @@ Build the library first with ``python -m invariant_token_log_fp32_amd.build``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -21,6 +22,7 @@ __all__ = [
     "support_state_fields", "l2norm", "l2norm_zero", "l2norm_accumulate", "l2norm_finalize", "NORM_BIN_WORDS",
     "linear", "linear_logp", "linear_logp_workspace_bytes", "linear_logp_summaries", "linear_logp_merge",
     "logp_nucleus_noalloc", "NOALLOC_MAX_ROWS", "RlkError", "N_SHARDS",
+    "mx4_bytes", "mx4_quantize", "mx4_linear", "mx4_linear_workspace_bytes",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -29,6 +31,8 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("RLK_LIBRARY") or os.path.join(_PKG, "librlk_logp.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "rlk_logp.h")
 HEADER_PATHS = [HEADER_PATH] + [os.path.join(os.path.dirname(_PKG), "include", n) for n in ("rlk_norm.h", "rlk_linear.h")]
+# The serving operators' headers (rollout and drafting).
+SERVING_HEADER_PATHS = [os.path.join(os.path.dirname(_PKG), "include", n) for n in ("rlk_mx4.h",)]
 N_SHARDS = 8
 NORM_BIN_WORDS = 264  # uint64 words of rlk_norm_bins
 NOALLOC_MAX_ROWS = 32768  # RLK_NOALLOC_MAX_ROWS
@@ -109,6 +113,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rlk_linear_logp_merge.restype = i32
     lib.rlk_linear_logp_summary_bytes.argtypes = [i64, lay]
     lib.rlk_linear_logp_summary_bytes.restype = sz
+    lib.rlk_mx4_codes_bytes.argtypes = [i64, i64]
+    lib.rlk_mx4_codes_bytes.restype = sz
+    lib.rlk_mx4_scales_bytes.argtypes = [i64, i64]
+    lib.rlk_mx4_scales_bytes.restype = sz
+    lib.rlk_mx4_quantize.argtypes = [vp, i64, i64, i64, vp, sz, vp, sz, vp, i64, vp]
+    lib.rlk_mx4_quantize.restype = i32
+    lib.rlk_mx4_linear.argtypes = [vp, i64, i64, i64, vp, vp, lay, vp, vp, sz, vp]
+    lib.rlk_mx4_linear.restype = i32
+    lib.rlk_mx4_linear_workspace_bytes.argtypes = [i64, i64]
+    lib.rlk_mx4_linear_workspace_bytes.restype = sz
     _lib = lib
     return lib
 
@@ -616,3 +630,101 @@ def linear_logp_merge(summaries, temperature, target, *, n_rows: int, groups: in
     if st != RLK_OK:
         raise RlkError(st, "rlk_linear_logp_merge")
     return (out, lse_out) if return_lse else out
+
+
+# ---------------------------------------------------------------------------
+# microscaled 4-bit quantisation and LM-head linear (include/rlk_mx4.h)
+# ---------------------------------------------------------------------------
+
+def _on_device(device):
+    """The context a launch needs: the tensors' device made current, when it is not."""
+    torch = _torch()
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _bytes_tensor(value, need, device, name):
+    """A caller-supplied uint8 tensor of at least ``need`` bytes, checked, or a new one."""
+    torch = _torch()
+    if value is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if value.dtype != torch.uint8 or value.device != device or not value.is_contiguous() or value.numel() < need:
+        raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {need} bytes on {device}")
+    return value
+
+
+def mx4_bytes(n_rows: int, d: int) -> Tuple[int, int]:
+    """Bytes of the codes and of the scales of an n_rows x d matrix (rlk_mx4_codes_bytes, rlk_mx4_scales_bytes)."""
+    lib = load_library()
+    return int(lib.rlk_mx4_codes_bytes(int(n_rows), int(d))), int(lib.rlk_mx4_scales_bytes(int(n_rows), int(d)))
+
+
+def mx4_quantize(x, *, codes=None, scales=None, values_out=None, return_values: bool = False, stream=None):
+    """Microscaled 4-bit form of the rows of ``x`` (rlk_mx4_quantize): blocks of
+    32 BF16 values that share a power of two, in the layout that mx4_linear
+    reads. ``x`` is a [n_rows, d] device tensor of BF16 bits, d a multiple of
+    32, row stride a multiple of 8. Returns (codes, scales), uint8 tensors, or
+    with ``return_values`` (codes, scales, values) where ``values`` is the
+    bfloat16 [n_rows, d] matrix that they stand for (``values_out`` may be ``x``)."""
+    torch = _torch()
+    ldx = _bf16_matrix(x, "x")
+    n, d = x.shape
+    dev = x.device
+    lib = load_library()
+    need_c, need_s = int(lib.rlk_mx4_codes_bytes(n, d)), int(lib.rlk_mx4_scales_bytes(n, d))
+    codes = _bytes_tensor(codes, need_c, dev, "codes")
+    scales = _bytes_tensor(scales, need_s, dev, "scales")
+    if return_values and values_out is None:
+        values_out = torch.empty((n, d), dtype=torch.bfloat16, device=dev)
+    ldv = 0
+    if values_out is not None:
+        ldv = _bf16_matrix(values_out, "values_out")
+        if values_out.device != dev or tuple(values_out.shape) != (n, d):
+            raise ValueError(f"values_out must hold {n} rows of {d} BF16 values on {dev}")
+    with _on_device(dev):
+        st = lib.rlk_mx4_quantize(x.data_ptr(), n, d, ldx, codes.data_ptr(), codes.numel(), scales.data_ptr(),
+                                  scales.numel(), values_out.data_ptr() if values_out is not None else None, ldv,
+                                  _stream_handle(stream, dev))
+    if st != RLK_OK:
+        raise RlkError(st, "rlk_mx4_quantize")
+    return (codes, scales, values_out) if return_values else (codes, scales)
+
+
+def mx4_linear_workspace_bytes(n_rows: int, d_model: int) -> int:
+    return int(load_library().rlk_mx4_linear_workspace_bytes(int(n_rows), int(d_model)))
+
+
+def mx4_linear(hidden, weight_codes, weight_scales, *, vocab_real: int, vocab_padded: int, out=None, workspace=None,
+               stream=None):
+    """BF16 logits [n_rows, vocab_padded] of the LM head with both operands in 4
+    bits, pads -inf (rlk_mx4_linear). ``hidden`` is BF16 [n_rows, d_model],
+    quantised by the call; ``weight_codes`` and ``weight_scales`` come from
+    mx4_quantize on the [vocab_real, d_model] projection."""
+    torch = _torch()
+    ldh = _bf16_matrix(hidden, "hidden")
+    n, d = hidden.shape
+    dev = hidden.device
+    lib = load_library()
+    for value, need, name in ((weight_codes, int(lib.rlk_mx4_codes_bytes(int(vocab_real), d)), "weight_codes"),
+                              (weight_scales, int(lib.rlk_mx4_scales_bytes(int(vocab_real), d)), "weight_scales")):
+        if value is None:
+            raise ValueError(f"{name} is missing")
+        _bytes_tensor(value, need, dev, name)
+    if out is None:
+        out = torch.empty((n, vocab_padded), dtype=torch.bfloat16, device=dev)
+    ldo = _check_logits(out)
+    if out.device != dev or out.shape[0] != n or out.shape[1] < vocab_padded or (ldo % 8) != 0:
+        raise ValueError(f"out must hold {n} rows of at least {vocab_padded} BF16 columns, row stride a multiple "
+                         f"of 8, on {dev}")
+    lay = make_layout(vocab_padded, vocab_real, ldo)
+    need = int(lib.rlk_mx4_linear_workspace_bytes(n, d))
+    workspace, ws_bytes = _workspace(workspace, need, dev)
+    with _on_device(dev):
+        st = lib.rlk_mx4_linear(hidden.data_ptr(), n, d, ldh, weight_codes.data_ptr(), weight_scales.data_ptr(),
+                                ctypes.byref(lay), out.data_ptr(),
+                                workspace.data_ptr() if workspace is not None else None, ws_bytes,
+                                _stream_handle(stream, dev))
+    if st != RLK_OK:
+        raise RlkError(st, "rlk_mx4_linear")
+    return out

@@ -50,6 +50,7 @@
 
 #include <atomic>
 
+#include "bf16_store.hpp"
 #include "logp_device.hpp"
 #include "rlk_linear.h"
 #include "rlk_logp.h"
@@ -323,60 +324,6 @@ __device__ __forceinline__ float round_bf16(float v) {
   return __uint_as_float(static_cast<uint32_t>(__builtin_bit_cast(uint16_t, b)) << 16);
 }
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
-// Two fp32 values rounded to BF16 (nearest even) in one 32-bit word, low first.
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const bf16x2 v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
-  return __builtin_bit_cast(uint32_t, v);
-}
-
-// 8 BF16 logits (4 packed pairs) at column c of a row; pad columns -inf.
-__device__ __forceinline__ void store8(const Geo& g, uint16_t* __restrict__ dst, int64_t c, uint32_t w0, uint32_t w1,
-                                      uint32_t w2, uint32_t w3) {
-  if (c + 8 > g.vocab_real) {
-    const uint32_t w[4] = {w0, w1, w2, w3};
-    uint32_t o[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t lo = (c + 2 * k < g.vocab_real) ? (w[k] & 0xFFFFu) : 0xFF80u;
-      const uint32_t hi = (c + 2 * k + 1 < g.vocab_real) ? (w[k] & 0xFFFF0000u) : 0xFF800000u;
-      o[k] = lo | hi;
-    }
-    w0 = o[0];
-    w1 = o[1];
-    w2 = o[2];
-    w3 = o[3];
-  }
-  *reinterpret_cast<u32x4*>(dst) = u32x4{w0, w1, w2, w3};
-}
-
-// The 16 BF16 logits of block (i, j) that lane l stores, as 8 packed words:
-// lane l holds, for q = 0..3, columns 8q + 4h .. +3 (h = l/32) of row l%32;
-// one exchange with lane l^32 gives it the 16 columns 16h .. +15.
-__device__ __forceinline__ void block_words(const Acc& v, int h, uint32_t (&w)[8]) {
-  // columns 8q + 4h + (0, 1) and (2, 3) of this lane, q = 0..3
-  const uint32_t p00 = pack_bf16(v[0], v[1]), p01 = pack_bf16(v[2], v[3]);
-  const uint32_t p10 = pack_bf16(v[4], v[5]), p11 = pack_bf16(v[6], v[7]);
-  const uint32_t p20 = pack_bf16(v[8], v[9]), p21 = pack_bf16(v[10], v[11]);
-  const uint32_t p30 = pack_bf16(v[12], v[13]), p31 = pack_bf16(v[14], v[15]);
-  // h = 0 keeps q = 0, 1 and takes the partner's; h = 1 keeps q = 2, 3
-  const uint32_t g00 = static_cast<uint32_t>(__shfl_xor(static_cast<int>(h ? p00 : p20), 32));
-  const uint32_t g01 = static_cast<uint32_t>(__shfl_xor(static_cast<int>(h ? p01 : p21), 32));
-  const uint32_t g10 = static_cast<uint32_t>(__shfl_xor(static_cast<int>(h ? p10 : p30), 32));
-  const uint32_t g11 = static_cast<uint32_t>(__shfl_xor(static_cast<int>(h ? p11 : p31), 32));
-  const uint32_t a0 = h ? p20 : p00, a1 = h ? p21 : p01;
-  const uint32_t b0 = h ? p30 : p10, b1 = h ? p31 : p11;
-  w[0] = h ? g00 : a0;
-  w[1] = h ? g01 : a1;
-  w[2] = h ? a0 : g00;
-  w[3] = h ? a1 : g01;
-  w[4] = h ? g10 : b0;
-  w[5] = h ? g11 : b1;
-  w[6] = h ? b0 : g10;
-  w[7] = h ? b1 : g11;
-}
-
 // Stores the tile's BF16 logits from the accumulators; pads -inf.
 __device__ __forceinline__ void tile_store(const Geo& g, int64_t row0, int64_t col0, const Acc (&acc)[kMB][kNB],
                                            uint16_t* __restrict__ out, int64_t ldo) {
@@ -394,7 +341,7 @@ __device__ __forceinline__ void tile_store(const Geo& g, int64_t row0, int64_t c
 #pragma unroll
       for (int j = 0; j < kNB; ++j) {
         uint32_t w[8];
-        block_words(acc[i][j], h, w);
+        rlk::block_words(acc[i][j], h, w);
         // ordinary stores: L2 merges the 16-byte pieces of a row into whole lines
         // (with the non-temporal hint they reach HBM as partial lines, 15% slower)
         if (gr < g.n_rows) {
@@ -411,11 +358,11 @@ __device__ __forceinline__ void tile_store(const Geo& g, int64_t row0, int64_t c
 #pragma unroll
     for (int j = 0; j < kNB; ++j) {
       uint32_t w[8];
-      block_words(acc[i][j], h, w);
+      rlk::block_words(acc[i][j], h, w);
       const int64_t gc = cw + j * 32;
       if (gr >= g.n_rows || gc >= g.vocab_padded) continue;
-      store8(g, out + gr * ldo + gc, gc, w[0], w[1], w[2], w[3]);
-      store8(g, out + gr * ldo + gc + 8, gc + 8, w[4], w[5], w[6], w[7]);
+      rlk::store8(g.vocab_real, out + gr * ldo + gc, gc, w[0], w[1], w[2], w[3]);
+      rlk::store8(g.vocab_real, out + gr * ldo + gc + 8, gc + 8, w[4], w[5], w[6], w[7]);
     }
   }
 }
