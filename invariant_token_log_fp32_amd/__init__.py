@@ -23,6 +23,7 @@ __all__ = [
     "linear", "linear_logp", "linear_logp_workspace_bytes", "linear_logp_summaries", "linear_logp_merge",
     "logp_nucleus_noalloc", "NOALLOC_MAX_ROWS", "RlkError", "N_SHARDS",
     "mx4_bytes", "mx4_quantize", "mx4_linear", "mx4_linear_workspace_bytes",
+    "draft_verify", "draft_workspace_bytes",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -32,7 +33,7 @@ LIB_PATH = os.environ.get("RLK_LIBRARY") or os.path.join(_PKG, "librlk_logp.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "rlk_logp.h")
 HEADER_PATHS = [HEADER_PATH] + [os.path.join(os.path.dirname(_PKG), "include", n) for n in ("rlk_norm.h", "rlk_linear.h")]
 # The serving operators' headers (rollout and drafting).
-SERVING_HEADER_PATHS = [os.path.join(os.path.dirname(_PKG), "include", n) for n in ("rlk_mx4.h",)]
+SERVING_HEADER_PATHS = [os.path.join(os.path.dirname(_PKG), "include", n) for n in ("rlk_mx4.h", "rlk_draft.h")]
 N_SHARDS = 8
 NORM_BIN_WORDS = 264  # uint64 words of rlk_norm_bins
 NOALLOC_MAX_ROWS = 32768  # RLK_NOALLOC_MAX_ROWS
@@ -59,6 +60,21 @@ class VocabLayout(ctypes.Structure):
         ("row_stride", ctypes.c_int64),
         ("n_shards", ctypes.c_int32),
         ("groups", ctypes.c_int32),
+    ]
+
+
+class ScoredRows(ctypes.Structure):
+    """Mirror of ``rlk_scored_rows``."""
+
+    _fields_ = [
+        ("logits", ctypes.c_void_p),
+        ("n_rows", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("temperature", ctypes.c_void_p),
+        ("policy_logp", ctypes.c_void_p),
+        ("ref_logp", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p),
+        ("support", ctypes.c_void_p),
     ]
 
 
@@ -123,6 +139,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rlk_mx4_linear.restype = i32
     lib.rlk_mx4_linear_workspace_bytes.argtypes = [i64, i64]
     lib.rlk_mx4_linear_workspace_bytes.restype = sz
+    rows = ctypes.POINTER(ScoredRows)
+    lib.rlk_draft_verify.argtypes = [rows, rows, lay, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.rlk_draft_verify.restype = i32
+    lib.rlk_draft_workspace_bytes.argtypes = [i64, lay]
+    lib.rlk_draft_workspace_bytes.restype = sz
     _lib = lib
     return lib
 
@@ -728,3 +749,101 @@ def mx4_linear(hidden, weight_codes, weight_scales, *, vocab_real: int, vocab_pa
     if st != RLK_OK:
         raise RlkError(st, "rlk_mx4_linear")
     return out
+
+
+# ---------------------------------------------------------------------------
+# verification of drafted tokens (include/rlk_draft.h)
+# ---------------------------------------------------------------------------
+
+def draft_workspace_bytes(n_seq: int, vocab_padded: int, vocab_real: int) -> int:
+    lay = make_layout(vocab_padded, vocab_real, vocab_padded)
+    return int(load_library().rlk_draft_workspace_bytes(int(n_seq), ctypes.byref(lay)))
+
+
+def _given(value, shape, dtype, device, name):
+    """A required input tensor, checked."""
+    torch = _torch()
+    if not isinstance(value, torch.Tensor) or value.dtype != dtype or value.device != device or \
+            tuple(value.shape) != tuple(shape) or not value.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return value
+
+
+def draft_verify(logits, draft_token, draft_start, accept_u, sample_u, *, temperature, policy_logp, ref_logp, lse,
+                 support_state, vocab_real: int, vocab_padded: Optional[int] = None, draft_logits=None,
+                 draft_temperature=None, draft_policy_logp=None, draft_support_state=None, token_out=None,
+                 accepted_out=None, policy_out=None, ref_out=None, workspace=None, stream=None):
+    """Accept or refuse drafted tokens and draw one more per sequence (rlk_draft_verify).
+
+    ``logits`` are the target's rows, sequence after sequence, K + 1 for a
+    sequence of K drafted tokens; ``policy_logp``, ``ref_logp``, ``lse`` and
+    ``support_state`` are what logp_nucleus(..., return_state=True) gave for
+    them with the drafted tokens as targets (any real column in the last row of
+    a sequence). ``draft_start`` int64 [n_seq + 1] are the running lengths of
+    the drafts, ``draft_token`` int64 [n_draft] and ``accept_u`` float64
+    [n_draft] lie sequence after sequence, ``sample_u`` is float64 [n_seq].
+    ``draft_logits`` [n_draft rows] with its own temperature, policy logprobs
+    and support records is the drafter's side; without it every drafted token
+    is a point mass. With n_draft 0 the call draws one token per row.
+    Returns (tokens int64 [n_rows], accepted int32 [n_seq], policy, reference
+    float32 [n_rows]); new outputs hold -1, -1, 0, 0 in rows of no sequence."""
+    torch = _torch()
+    stride = _check_logits(logits)
+    n = logits.shape[0]
+    dev = logits.device
+    vp = int(vocab_padded if vocab_padded is not None else logits.shape[1])
+    if logits.shape[1] < vp:
+        raise ValueError(f"logits must have at least {vp} columns")
+    n_seq, n_draft = draft_start.numel() - 1, draft_token.numel()
+    if n_seq < 0:
+        raise ValueError("draft_start must hold n_seq + 1 offsets")
+    _given(draft_start, (n_seq + 1,), torch.int64, dev, "draft_start")
+    _given(draft_token, (n_draft,), torch.int64, dev, "draft_token")
+    _given(accept_u, (n_draft,), torch.float64, dev, "accept_u")
+    _given(sample_u, (n_seq,), torch.float64, dev, "sample_u")
+    if n < n_draft + n_seq:
+        raise ValueError(f"logits must hold a row for each of {n_draft} drafted tokens and {n_seq} sequences")
+    temperature = _per_row(temperature, n, torch.float32, dev, "temperature")
+    for value, name in ((policy_logp, "policy_logp"), (ref_logp, "ref_logp"), (lse, "lse")):
+        _given(value, (n,), torch.float32, dev, name)
+    _given(support_state, (n, 4), torch.int32, dev, "support_state")
+    target = ScoredRows(logits.data_ptr(), n, stride, temperature.data_ptr(), policy_logp.data_ptr(),
+                        ref_logp.data_ptr(), lse.data_ptr(), support_state.data_ptr())
+    draft = None
+    if draft_logits is not None:
+        dstride = _check_logits(draft_logits)
+        m = draft_logits.shape[0]
+        if draft_logits.device != dev or m < n_draft or draft_logits.shape[1] < vp:
+            raise ValueError(f"draft_logits must hold {n_draft} rows of at least {vp} columns on {dev}")
+        if not isinstance(draft_temperature, (int, float)):
+            _given(draft_temperature, (m,), torch.float32, dev, "draft_temperature")
+        draft_temperature = _per_row(draft_temperature, m, torch.float32, dev, "draft_temperature")
+        _given(draft_policy_logp, (m,), torch.float32, dev, "draft_policy_logp")
+        _given(draft_support_state, (m, 4), torch.int32, dev, "draft_support_state")
+        draft = ScoredRows(draft_logits.data_ptr(), m, dstride, draft_temperature.data_ptr(),
+                           draft_policy_logp.data_ptr(), None, None, draft_support_state.data_ptr())
+    if token_out is None:
+        token_out = torch.full((n,), -1, dtype=torch.int64, device=dev)
+    if accepted_out is None:
+        accepted_out = torch.full((n_seq,), -1, dtype=torch.int32, device=dev)
+    if policy_out is None:
+        policy_out = torch.zeros(n, dtype=torch.float32, device=dev)
+    if ref_out is None:
+        ref_out = torch.zeros(n, dtype=torch.float32, device=dev)
+    _out(token_out, (n,), torch.int64, dev, "token_out")
+    _out(accepted_out, (n_seq,), torch.int32, dev, "accepted_out")
+    _out(policy_out, (n,), torch.float32, dev, "policy_out")
+    _out(ref_out, (n,), torch.float32, dev, "ref_out")
+    lay = make_layout(vp, vocab_real, vp)
+    lib = load_library()
+    need = int(lib.rlk_draft_workspace_bytes(n_seq, ctypes.byref(lay)))
+    workspace, ws_bytes = _workspace(workspace, need, dev)
+    with _on_device(dev):
+        st = lib.rlk_draft_verify(
+            ctypes.byref(target), ctypes.byref(draft) if draft is not None else None, ctypes.byref(lay), n_seq,
+            n_draft, draft_start.data_ptr(), draft_token.data_ptr(), accept_u.data_ptr(), sample_u.data_ptr(),
+            token_out.data_ptr(), accepted_out.data_ptr(), policy_out.data_ptr(), ref_out.data_ptr(),
+            workspace.data_ptr() if workspace is not None else None, ws_bytes, _stream_handle(stream, dev))
+    if st != RLK_OK:
+        raise RlkError(st, "rlk_draft_verify")
+    return token_out, accepted_out, policy_out, ref_out

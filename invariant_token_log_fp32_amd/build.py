@@ -2,8 +2,9 @@
 
 Produces ``librlk_logp.so`` next to this file from ``csrc/rlk_logp.hip``
 (token logprobs, their backward), ``csrc/rlk_norm.hip`` (gradient L2 norm),
-``csrc/rlk_linear.hip`` (LM-head linear, fused linear + logprob) and
-``csrc/rlk_mx4.hip`` (4-bit microscaled quantisation and LM-head linear):
+``csrc/rlk_linear.hip`` (LM-head linear, fused linear + logprob),
+``csrc/rlk_mx4.hip`` (4-bit microscaled quantisation and LM-head linear) and
+``csrc/rlk_draft.hip`` (verification of drafted tokens):
     python -m invariant_token_log_fp32_amd.build
 """
 from __future__ import annotations
@@ -15,7 +16,8 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRCS = [os.path.join(PKG, "csrc", n) for n in ("rlk_logp.hip", "rlk_norm.hip", "rlk_linear.hip", "rlk_mx4.hip")]
+SRCS = [os.path.join(PKG, "csrc", n) for n in ("rlk_logp.hip", "rlk_norm.hip", "rlk_linear.hip", "rlk_mx4.hip",
+                                              "rlk_draft.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "librlk_logp.so")
 ARCH = "gfx950"
