@@ -15,6 +15,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "bf16_store.hpp"
 #include "logp_device.hpp"
 #include "rlk_logp.h"
@@ -172,6 +174,7 @@ __device__ __forceinline__ f32x16 mma(const i32x4& w, const i32x4& h, const f32x
 
 constexpr int kRowsThreads = 256;
 constexpr int kRowsCols = 64;  // columns of a wave
+constexpr int64_t kRowsMost = 128;  // rows up to which k_mx4_rows runs
 
 __global__ __launch_bounds__(kRowsThreads) void k_mx4_rows(Geo g, int64_t col_tiles, int64_t n_work,
                                                            uint16_t* __restrict__ out) {
@@ -230,9 +233,338 @@ __global__ __launch_bounds__(kRowsThreads) void k_mx4_rows(Geo g, int64_t col_ti
   }
 }
 
+// ---------------------------------------------------------------------------
+// product, many rows: 256 x 256 tiles
+// ---------------------------------------------------------------------------
+
+constexpr int BM = 256;                   // rows of a workgroup's tile
+constexpr int BN = 256;                   // vocabulary columns of it
+constexpr int kTilesThreads = 256;        // 4 waves, 2 x 2, each 128 x 128
+constexpr int kPanelTiles = BM / kTileRows;      // 8 packed tiles of either operand
+constexpr int kMB = 4;                    // 32 x 32 blocks of a wave, either way
+constexpr int kNB = 4;
+constexpr int kSteps = kScaleK / kStepK;  // 4 instructions deep: one stage, one word of scales
+constexpr int kPanelBytes = kPanelTiles * kSteps * kStepBytes;   // 32 KB of codes a stage
+constexpr int kPanelScales = kPanelTiles * kScaleBytes;          // 2 KB of scales a stage
+constexpr int kStageBytes = 2 * kPanelBytes + 2 * kPanelScales;  // both operands: 68 KB
+constexpr int kOffScales = 2 * kPanelBytes;
+constexpr int kXcds = 8;
+constexpr int kGM = 4;                    // tiles of a group that shares an XCD's L2
+constexpr int kGN = 8;
+constexpr int kRsrcWord3 = 0x00020000;    // raw buffer, 32-bit data format, no swizzle
+constexpr int kNoLoad = 0x40000000;       // an offset behind the end of every resource
+static_assert(BM == BN, "one panel shape for both operands");
+
+typedef __attribute__((address_space(3))) void* LdsPtr;
+typedef i32x4 Frag;
+
+struct TileGeo {
+  Geo g;
+  int64_t m_tiles;
+  int64_t n_tiles;
+  int64_t m_groups;
+  int64_t n_groups;
+  int64_t h_end;     // packed tiles of either operand
+  int64_t w_end;
+};
+
+// Tile of virtual workgroup v, or false when v has none. Workgroup b runs on
+// XCD b % 8; an XCD takes groups of kGM x kGN tiles, one for each of its 32
+// compute units, that stream the same panels through its L2.
+__device__ __forceinline__ bool tile_of(const TileGeo& g, int64_t v, int64_t& m_t, int64_t& n_t) {
+  const int64_t slot = v / kXcds;
+  const int64_t k = (slot / (kGM * kGN)) * kXcds + v % kXcds;
+  const int64_t local = slot % (kGM * kGN);
+  if (k >= g.m_groups * g.n_groups) return false;
+  m_t = (k % g.m_groups) * kGM + local % kGM;
+  n_t = (k / g.m_groups) * kGN + local / kGM;
+  return m_t < g.m_tiles && n_t < g.n_tiles;
+}
+
+__host__ __device__ __forceinline__ int64_t virtual_blocks(const TileGeo& g) {
+  const int64_t groups = g.m_groups * g.n_groups;
+  return ((groups + kXcds - 1) / kXcds) * kXcds * kGM * kGN;
+}
+
+__device__ __forceinline__ bool next_tile(const TileGeo& g, int64_t n_virtual, int64_t& v, int64_t& m_t, int64_t& n_t) {
+  while (v < n_virtual) {
+    if (tile_of(g, v, m_t, n_t)) return true;
+    v += gridDim.x;
+  }
+  return false;
+}
+
+// One operand's 8 packed tiles as buffer resources. Wave w loads tiles 2w and
+// 2w + 1; a tile behind the operand's end is replaced by its last one (its
+// rows or columns are not stored), so every load is in range.
+struct Panel {
+  __amdgpu_buffer_rsrc_t codes;
+  __amdgpu_buffer_rsrc_t scales;
+  int tile[2];       // of this wave's loads, counted from the panel's first tile
+};
+
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6); }
+
+__device__ __forceinline__ Panel make_panel(const uint8_t* codes, const uint8_t* scales, int64_t tile0, int64_t end,
+                                            int steps4) {
+  Panel p;
+  const int64_t first = tile0 < end ? tile0 : end - 1;
+  const int n = static_cast<int>(end - first < kPanelTiles ? end - first : kPanelTiles);
+  p.codes = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(codes + first * steps4 * (kSteps * kStepBytes)), 0,
+                                              n * steps4 * (kSteps * kStepBytes), kRsrcWord3);
+  p.scales = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(scales + first * steps4 * kScaleBytes), 0,
+                                               n * steps4 * kScaleBytes, kRsrcWord3);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = 2 * wave_id() + i;
+    p.tile[i] = t < n ? t : n - 1;
+  }
+  return p;
+}
+
+// Load i (0..7) of this wave's 8 KB of a panel's stage kt: step i % 4 of its
+// tile i / 4, lane after lane as it lies in memory. kt < 0: an offset behind
+// the resource's end, which fetches nothing (zeros), without a branch.
+__device__ __forceinline__ void load_codes(const Panel& p, int steps4, int kt, uint8_t* __restrict__ stage, int i) {
+  const int lane = threadIdx.x & 63;
+  const int at = (p.tile[i >> 2] * steps4 + (kt < 0 ? 0 : kt)) * (kSteps * kStepBytes) + (i & 3) * kStepBytes;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(p.codes, (LdsPtr)(stage + (8 * wave_id() + i) * kStepBytes), 16,
+                                           lane * 16 + (kt < 0 ? kNoLoad : 0), at, 0, 0);
+}
+
+// Load i (0..1): the scales of its tile i.
+__device__ __forceinline__ void load_scales(const Panel& p, int steps4, int kt, uint8_t* __restrict__ stage, int i) {
+  const int lane = threadIdx.x & 63;
+  const int at = (p.tile[i] * steps4 + (kt < 0 ? 0 : kt)) * kScaleBytes;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(p.scales, (LdsPtr)(stage + (2 * wave_id() + i) * kScaleBytes), 4,
+                                           lane * 4 + (kt < 0 ? kNoLoad : 0), at, 0, 0);
+}
+
+struct Tile {
+  Panel h;
+  Panel w;
+};
+
+__device__ __forceinline__ Tile make_tile(const TileGeo& g, int64_t m_t, int64_t n_t) {
+  Tile t;
+  t.h = make_panel(g.g.hc, g.g.hs, m_t * kPanelTiles, g.h_end, g.g.steps4);
+  t.w = make_panel(g.g.wc, g.g.ws, n_t * kPanelTiles, g.w_end, g.g.steps4);
+  return t;
+}
+
+// LDS of a stage: the hidden states' codes, the projection's, then their scales.
+__device__ __forceinline__ void load_stage(const Tile& t, int steps4, int kt, uint8_t* __restrict__ stage) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) load_codes(t.h, steps4, kt, stage, i);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) load_codes(t.w, steps4, kt, stage + kPanelBytes, i);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) load_scales(t.h, steps4, kt, stage + kOffScales, i);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) load_scales(t.w, steps4, kt, stage + kOffScales + kPanelScales, i);
+}
+
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Fragment of step kk of a wave's tile i (its 32 rows, 64 deep).
+__device__ __forceinline__ Frag frag(const uint8_t* __restrict__ codes, int first, int i, int kk) {
+  const int lane = threadIdx.x & 63;
+  return *reinterpret_cast<const Frag*>(codes + ((first + i) * kSteps + kk) * kStepBytes + lane * 16);
+}
+
+__device__ __forceinline__ int scale_word(const uint8_t* __restrict__ scales, int first, int i) {
+  const int lane = threadIdx.x & 63;
+  return *reinterpret_cast<const int*>(scales + (first + i) * kScaleBytes + lane * 4);
+}
+
+struct Scales {
+  int h[kMB];
+  int w[kNB];
+};
+
+// One step: 16 instructions, each followed by its share of the reads for the
+// step after next (8 fragments), of the next stage's scales (steps 2 and 3)
+// and of the loads of the stage after next (steps 2 and 3).
+template <int kk>
+__device__ __forceinline__ void mma_step(const Frag (&a)[kMB], const Frag (&b)[kNB], const Scales& sc,
+                                         f32x16 (&acc)[kMB][kNB], const uint8_t* __restrict__ from, int fm, int fn,
+                                         Frag (&na)[kMB], Frag (&nb)[kNB], Scales& next, const Tile& t, int steps4,
+                                         int kt, uint8_t* __restrict__ to) {
+  constexpr int nk = (kk + 2) % kSteps;
+#pragma unroll
+  for (int s = 0; s < kMB * kNB; ++s) {
+    const int i = s / kNB, j = s % kNB;
+    acc[i][j] = mma<kk>(b[j], a[i], acc[i][j], sc.w[j], sc.h[i]);
+    if (s < kMB)
+      na[s] = frag(from, fm, s, nk);
+    else if (s < kMB + kNB)
+      nb[s - kMB] = frag(from + kPanelBytes, fn, s - kMB, nk);
+    else if (kk == 2 && s < kMB + kNB + kMB)
+      next.h[s - kMB - kNB] = scale_word(from + kOffScales, fm, s - kMB - kNB);
+    else if (kk == 3 && s < kMB + kNB + kNB)
+      next.w[s - kMB - kNB] = scale_word(from + kOffScales + kPanelScales, fn, s - kMB - kNB);
+    if (kk == 2 && (s & 1) == 0) load_codes(t.h, steps4, kt, to, s >> 1);
+    if (kk == 3 && (s & 1) == 0) load_codes(t.w, steps4, kt, to + kPanelBytes, s >> 1);
+    if (kk == 2 && (s == 13 || s == 15)) load_scales(t.h, steps4, kt, to + kOffScales, s == 15);
+    if (kk == 3 && (s == 13 || s == 15)) load_scales(t.w, steps4, kt, to + kOffScales + kPanelScales, s == 15);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+struct Ahead {
+  Frag a[kSteps][kMB];
+  Frag b[kSteps][kNB];
+  Scales sc;
+};
+
+// The fragments of steps 0 and 1 and the scales of a landed stage.
+__device__ __forceinline__ void read_first(const uint8_t* __restrict__ stage, int fm, int fn, Ahead& f) {
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+    for (int i = 0; i < kMB; ++i) f.a[kk][i] = frag(stage, fm, i, kk);
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) f.b[kk][j] = frag(stage + kPanelBytes, fn, j, kk);
+  }
+#pragma unroll
+  for (int i = 0; i < kMB; ++i) f.sc.h[i] = scale_word(stage + kOffScales, fm, i);
+#pragma unroll
+  for (int j = 0; j < kNB; ++j) f.sc.w[j] = scale_word(stage + kOffScales + kPanelScales, fn, j);
+}
+
+// Products of one tile. Stage kt lives in LDS buffer (kt + par) & 1. The
+// barrier behind step 1 waits for the next stage's loads and for every wave's
+// reads of this stage's buffer; steps 2 and 3 load into that buffer the stage
+// two ahead, of this tile or of the next one (tn; its stages 0 and 1 then are
+// in flight or landed on return, and its first fragments read).
+__device__ __forceinline__ void tile_products(const TileGeo& g, const Tile& t, const Tile& tn, bool next, int par,
+                                              uint8_t* __restrict__ smem, f32x16 (&acc)[kMB][kNB], Ahead& f) {
+  const int wave = threadIdx.x >> 6;
+  const int fm = (wave & 1) * kMB;
+  const int fn = (wave >> 1) * kNB;
+#pragma unroll
+  for (int i = 0; i < kMB; ++i)
+#pragma unroll
+    for (int j = 0; j < kNB; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+  const int n = g.g.steps4;
+  const bool ahead = next && n >= 2;
+  for (int kt = 0; kt < n; ++kt) {
+    uint8_t* cur = smem + ((kt + par) & 1) * kStageBytes;
+    uint8_t* nxt = smem + ((kt + par + 1) & 1) * kStageBytes;
+    Scales sn;
+    mma_step<0>(f.a[0], f.b[0], f.sc, acc, cur, fm, fn, f.a[2], f.b[2], sn, t, n, -1, cur);
+    mma_step<1>(f.a[1], f.b[1], f.sc, acc, cur, fm, fn, f.a[3], f.b[3], sn, t, n, -1, cur);
+    stage_barrier();
+    const bool mine = kt + 2 < n;
+    Tile q;
+    q.h = mine ? t.h : tn.h;
+    q.w = mine ? t.w : tn.w;
+    const int k2 = mine ? kt + 2 : (ahead ? kt + 2 - n : -1);
+    mma_step<2>(f.a[2], f.b[2], f.sc, acc, nxt, fm, fn, f.a[0], f.b[0], sn, q, n, k2, cur);
+    mma_step<3>(f.a[3], f.b[3], f.sc, acc, nxt, fm, fn, f.a[1], f.b[1], sn, q, n, k2, cur);
+    f.sc = sn;
+  }
+}
+
+// Stores a wave's 128 x 128 logits; pads -inf.
+__device__ __forceinline__ void tile_store(const Geo& g, int64_t row0, int64_t col0, const f32x16 (&acc)[kMB][kNB],
+                                           uint16_t* __restrict__ out) {
+  const int lane = threadIdx.x & 63;
+  const int h = lane >> 5;
+  const bool all_real = col0 + kNB * 32 <= g.vocab_real;  // uniform
+#pragma unroll
+  for (int i = 0; i < kMB; ++i) {
+    const int64_t row = row0 + i * 32 + (lane & 31);
+    uint16_t* dst = out + row * g.ldo;
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) {
+      uint32_t w[8];
+      rlk::block_words(acc[i][j], h, w);
+      const int64_t c = col0 + j * 32 + 16 * h;
+      if (row >= g.n_rows) continue;
+      if (all_real) {
+        *reinterpret_cast<u32x4*>(dst + c) = u32x4{w[0], w[1], w[2], w[3]};
+        *reinterpret_cast<u32x4*>(dst + c + 8) = u32x4{w[4], w[5], w[6], w[7]};
+      } else if (c < g.vocab_padded) {
+        rlk::store8(g.vocab_real, dst + c, c, w[0], w[1], w[2], w[3]);
+        rlk::store8(g.vocab_real, dst + c + 8, c + 8, w[4], w[5], w[6], w[7]);
+      }
+    }
+  }
+}
+
+__global__ __launch_bounds__(kTilesThreads) void k_mx4_tiles(TileGeo g, uint16_t* __restrict__ out) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * kStageBytes];
+  const int64_t n_virtual = virtual_blocks(g);
+  const int n = g.g.steps4;
+  int64_t v = blockIdx.x, m_t = 0, n_t = 0;
+  if (!next_tile(g, n_virtual, v, m_t, n_t)) return;  // uniform across the workgroup
+  const int wave = threadIdx.x >> 6;
+  const int fm = (wave & 1) * kMB;
+  const int fn = (wave >> 1) * kNB;
+  Tile t = make_tile(g, m_t, n_t);
+  int par = 0;
+  Ahead f;
+  load_stage(t, n, 0, smem);
+  load_stage(t, n, n > 1 ? 1 : -1, smem + kStageBytes);
+  stage_barrier();
+  read_first(smem, fm, fn, f);
+  int64_t v2 = v + gridDim.x, m2 = 0, n2 = 0;
+  bool more = next_tile(g, n_virtual, v2, m2, n2);
+  Tile tn = more ? make_tile(g, m2, n2) : t;
+  while (true) {
+    f32x16 acc[kMB][kNB];
+    tile_products(g, t, tn, more, par, smem, acc, f);
+    tile_store(g.g, m_t * BM + fm * 32, n_t * BN + fn * 32, acc, out);
+    if (!more) break;
+    par = (par + n) & 1;
+    m_t = m2;
+    n_t = n2;
+    t = tn;
+    v2 += gridDim.x;
+    more = next_tile(g, n_virtual, v2, m2, n2);
+    tn = more ? make_tile(g, m2, n2) : t;
+    if (n == 1) {
+      // a one-stage tile could not load the next one in its loop; every wave
+      // is past the barrier behind its step 1, so the other buffer is free
+      load_stage(t, n, 0, smem + par * kStageBytes);
+      stage_barrier();
+      read_first(smem + par * kStageBytes, fm, fn, f);
+    }
+  }
+}
+
 static bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 static int32_t launched() { return hipGetLastError() == hipSuccess ? RLK_OK : RLK_ERR_HIP; }
+
+// Compute units of the current device (cached per device; 0 if unknown).
+static int cu_count() {
+  static std::atomic<int> cache[64];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 0;
+  if (dev < 64) {
+    const int c = cache[dev].load(std::memory_order_relaxed);
+    if (c > 0) return c;
+  }
+  int n = 0;
+  if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) return 0;
+  if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// One workgroup per compute unit (its LDS fills one), each looping over its
+// tiles; a multiple of 8, so a workgroup's tiles keep their XCD.
+static unsigned grid_for(const TileGeo& g) {
+  const int64_t v = virtual_blocks(g);
+  int64_t cap = cu_count();
+  cap = cap > 0 ? (cap + kXcds - 1) / kXcds * kXcds : 256;
+  return static_cast<unsigned>(v < cap ? v : cap);
+}
 
 static int32_t launch_quantize(const uint16_t* x, int64_t n_rows, int64_t d, int64_t ldx, uint8_t* codes,
                                uint8_t* scales, uint16_t* values, int64_t ldv, hipStream_t stream) {
@@ -322,6 +654,18 @@ int32_t rlk_mx4_linear(const uint16_t* hidden, int64_t n_rows, int64_t d_model, 
   g.vocab_padded = layout->vocab_padded;
   g.ldo = layout->row_stride;
   g.steps4 = static_cast<int>(scale_steps(d_model));
+  if (n_rows > kRowsMost) {
+    TileGeo t;
+    t.g = g;
+    t.m_tiles = (n_rows + BM - 1) / BM;
+    t.n_tiles = (layout->vocab_padded + BN - 1) / BN;
+    t.m_groups = (t.m_tiles + kGM - 1) / kGM;
+    t.n_groups = (t.n_tiles + kGN - 1) / kGN;
+    t.h_end = row_tiles(n_rows);
+    t.w_end = row_tiles(layout->vocab_real);
+    k_mx4_tiles<<<dim3(grid_for(t)), dim3(kTilesThreads), 0, stream>>>(t, logits_out);
+    return launched();
+  }
   const int64_t col_tiles = layout->vocab_padded / kRowsCols;
   const int64_t n_work = col_tiles * row_tiles(n_rows);
   const int64_t blocks = (n_work + kRowsThreads / 64 - 1) / (kRowsThreads / 64);
