@@ -41,29 +41,29 @@ __device__ __forceinline__ void store8(int64_t vocab_real, uint16_t* __restrict_
 }
 
 // The 16 BF16 logits of block (i, j) that lane l stores, as 8 packed words:
-// lane l holds, for q = 0..3, columns 8q + 4h .. +3 (h = l/32) of row l%32;
-// one exchange with lane l^32 gives it the 16 columns 16h .. +15.
-__device__ __forceinline__ void block_words(const f32x16& v, int h, uint32_t (&w)[8]) {
-  // columns 8q + 4h + (0, 1) and (2, 3) of this lane, q = 0..3
-  const uint32_t p00 = pack_bf16(v[0], v[1]), p01 = pack_bf16(v[2], v[3]);
-  const uint32_t p10 = pack_bf16(v[4], v[5]), p11 = pack_bf16(v[6], v[7]);
-  const uint32_t p20 = pack_bf16(v[8], v[9]), p21 = pack_bf16(v[10], v[11]);
-  const uint32_t p30 = pack_bf16(v[12], v[13]), p31 = pack_bf16(v[14], v[15]);
-  // h = 0 keeps q = 0, 1 and takes the partner's; h = 1 keeps q = 2, 3
-  const uint32_t g00 = static_cast<uint32_t>(__shfl_xor(static_cast<int>(h ? p00 : p20), 32));
-  const uint32_t g01 = static_cast<uint32_t>(__shfl_xor(static_cast<int>(h ? p01 : p21), 32));
-  const uint32_t g10 = static_cast<uint32_t>(__shfl_xor(static_cast<int>(h ? p10 : p30), 32));
-  const uint32_t g11 = static_cast<uint32_t>(__shfl_xor(static_cast<int>(h ? p11 : p31), 32));
-  const uint32_t a0 = h ? p20 : p00, a1 = h ? p21 : p01;
-  const uint32_t b0 = h ? p30 : p10, b1 = h ? p31 : p11;
-  w[0] = h ? g00 : a0;
-  w[1] = h ? g01 : a1;
-  w[2] = h ? a0 : g00;
-  w[3] = h ? a1 : g01;
-  w[4] = h ? g10 : b0;
-  w[5] = h ? g11 : b1;
-  w[6] = h ? b0 : g10;
-  w[7] = h ? b1 : g11;
+// lane l holds, for q = 0..3, columns 8q + 4h .. +3 (h = l/32) of row l%32; one
+// exchange with lane l^32 gives it the 16 columns 16h .. +15. The exchange of a
+// lower half's word for an upper half's is one instruction.
+__device__ __forceinline__ void swap_halves(uint32_t& low, uint32_t& high) {
+  // lanes 32..63 of `low` with lanes 0..31 of `high`
+  const auto r = __builtin_amdgcn_permlane32_swap(low, high, false, false);
+  low = r[0];
+  high = r[1];
+}
+
+__device__ __forceinline__ void block_words(const f32x16& v, uint32_t (&w)[8]) {
+  w[0] = pack_bf16(v[0], v[1]);    // q = 0: stays in h = 0, to the partner in h = 1
+  w[1] = pack_bf16(v[2], v[3]);
+  w[2] = pack_bf16(v[8], v[9]);    // q = 2
+  w[3] = pack_bf16(v[10], v[11]);
+  w[4] = pack_bf16(v[4], v[5]);    // q = 1
+  w[5] = pack_bf16(v[6], v[7]);
+  w[6] = pack_bf16(v[12], v[13]);  // q = 3
+  w[7] = pack_bf16(v[14], v[15]);
+  swap_halves(w[0], w[2]);
+  swap_halves(w[1], w[3]);
+  swap_halves(w[4], w[6]);
+  swap_halves(w[5], w[7]);
 }
 
 }  // namespace rlk

@@ -341,7 +341,7 @@ __device__ __forceinline__ void tile_store(const Geo& g, int64_t row0, int64_t c
 #pragma unroll
       for (int j = 0; j < kNB; ++j) {
         uint32_t w[8];
-        rlk::block_words(acc[i][j], h, w);
+        rlk::block_words(acc[i][j], w);
         // ordinary stores: L2 merges the 16-byte pieces of a row into whole lines
         // (with the non-temporal hint they reach HBM as partial lines, 15% slower)
         if (gr < g.n_rows) {
@@ -358,7 +358,7 @@ __device__ __forceinline__ void tile_store(const Geo& g, int64_t row0, int64_t c
 #pragma unroll
     for (int j = 0; j < kNB; ++j) {
       uint32_t w[8];
-      rlk::block_words(acc[i][j], h, w);
+      rlk::block_words(acc[i][j], w);
       const int64_t gc = cw + j * 32;
       if (gr >= g.n_rows || gc >= g.vocab_padded) continue;
       rlk::store8(g.vocab_real, out + gr * ldo + gc, gc, w[0], w[1], w[2], w[3]);

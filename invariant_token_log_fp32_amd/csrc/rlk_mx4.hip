@@ -224,7 +224,7 @@ __global__ __launch_bounds__(kRowsThreads) void k_mx4_rows(Geo g, int64_t col_ti
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     uint32_t w[8];
-    rlk::block_words(acc[j], h, w);
+    rlk::block_words(acc[j], w);
     const int64_t c = (2 * ct + j) * kTileRows + 16 * h;
     if (row < g.n_rows && c < g.vocab_padded) {
       rlk::store8(g.vocab_real, out + row * g.ldo + c, c, w[0], w[1], w[2], w[3]);
@@ -243,14 +243,16 @@ constexpr int kTilesThreads = 256;        // 4 waves, 2 x 2, each 128 x 128
 constexpr int kPanelTiles = BM / kTileRows;      // 8 packed tiles of either operand
 constexpr int kMB = 4;                    // 32 x 32 blocks of a wave, either way
 constexpr int kNB = 4;
-constexpr int kSteps = kScaleK / kStepK;  // 4 instructions deep: one stage, one word of scales
-constexpr int kPanelBytes = kPanelTiles * kSteps * kStepBytes;   // 32 KB of codes a stage
-constexpr int kPanelScales = kPanelTiles * kScaleBytes;          // 2 KB of scales a stage
-constexpr int kStageBytes = 2 * kPanelBytes + 2 * kPanelScales;  // both operands: 68 KB
-constexpr int kOffScales = 2 * kPanelBytes;
+constexpr int kSteps = kScaleK / kStepK;  // 4 instructions deep: one word of scales
+constexpr int kHalfSteps = kSteps / 2;    // steps of a half stage (128 values of d)
+constexpr int kHalfPanel = kPanelTiles * kHalfSteps * kStepBytes;  // 16 KB of codes of one operand
+constexpr int kHalfBytes = 2 * kHalfPanel;                         // both operands
+constexpr int kPanelScales = kPanelTiles * kScaleBytes;            // 2 KB of scales of one operand and stage
+constexpr int kOffScales = 4 * kHalfBytes;                         // four half stages of codes, then two of scales
+constexpr int kStageScales = 2 * kPanelScales;
+constexpr int kSmemBytes = kOffScales + 2 * kStageScales;          // 136 KB
 constexpr int kXcds = 8;
-constexpr int kGM = 4;                    // tiles of a group that shares an XCD's L2
-constexpr int kGN = 8;
+constexpr int kGroup = 32;                // tiles of a group: an XCD's compute units
 constexpr int kRsrcWord3 = 0x00020000;    // raw buffer, 32-bit data format, no swizzle
 constexpr int kNoLoad = 0x40000000;       // an offset behind the end of every resource
 static_assert(BM == BN, "one panel shape for both operands");
@@ -260,33 +262,34 @@ typedef i32x4 Frag;
 
 struct TileGeo {
   Geo g;
-  int64_t m_tiles;
-  int64_t n_tiles;
-  int64_t m_groups;
-  int64_t n_groups;
+  int m_tiles;
+  int n_tiles;
+  int gm;            // a group is gm x gn tiles
+  int gn;
+  int m_groups;
+  int groups;
   int64_t h_end;     // packed tiles of either operand
   int64_t w_end;
 };
 
 // Tile of virtual workgroup v, or false when v has none. Workgroup b runs on
-// XCD b % 8; an XCD takes groups of kGM x kGN tiles, one for each of its 32
-// compute units, that stream the same panels through its L2.
-__device__ __forceinline__ bool tile_of(const TileGeo& g, int64_t v, int64_t& m_t, int64_t& n_t) {
-  const int64_t slot = v / kXcds;
-  const int64_t k = (slot / (kGM * kGN)) * kXcds + v % kXcds;
-  const int64_t local = slot % (kGM * kGN);
-  if (k >= g.m_groups * g.n_groups) return false;
-  m_t = (k % g.m_groups) * kGM + local % kGM;
-  n_t = (k / g.m_groups) * kGN + local / kGM;
-  return m_t < g.m_tiles && n_t < g.n_tiles;
+// XCD b % 8; an XCD takes groups of gm x gn tiles, one for each of its compute
+// units, that stream the same panels through its L2.
+__device__ __forceinline__ bool tile_of(const TileGeo& g, int v, int& m_t, int& n_t) {
+  const int slot = v / kXcds;
+  const int k = (slot / kGroup) * kXcds + v % kXcds;
+  const int local = slot % kGroup;
+  if (k >= g.groups) return false;
+  m_t = (k % g.m_groups) * g.gm + local % g.gm;
+  n_t = (k / g.m_groups) * g.gn + local / g.gm;
+  return local < g.gm * g.gn && m_t < g.m_tiles && n_t < g.n_tiles;
 }
 
-__host__ __device__ __forceinline__ int64_t virtual_blocks(const TileGeo& g) {
-  const int64_t groups = g.m_groups * g.n_groups;
-  return ((groups + kXcds - 1) / kXcds) * kXcds * kGM * kGN;
+__host__ __device__ __forceinline__ int virtual_blocks(const TileGeo& g) {
+  return ((g.groups + kXcds - 1) / kXcds) * kXcds * kGroup;
 }
 
-__device__ __forceinline__ bool next_tile(const TileGeo& g, int64_t n_virtual, int64_t& v, int64_t& m_t, int64_t& n_t) {
+__device__ __forceinline__ bool next_tile(const TileGeo& g, int n_virtual, int& v, int& m_t, int& n_t) {
   while (v < n_virtual) {
     if (tile_of(g, v, m_t, n_t)) return true;
     v += gridDim.x;
@@ -301,6 +304,7 @@ struct Panel {
   __amdgpu_buffer_rsrc_t codes;
   __amdgpu_buffer_rsrc_t scales;
   int tile[2];       // of this wave's loads, counted from the panel's first tile
+  int n;             // tiles that exist
 };
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6); }
@@ -314,6 +318,7 @@ __device__ __forceinline__ Panel make_panel(const uint8_t* codes, const uint8_t*
                                               n * steps4 * (kSteps * kStepBytes), kRsrcWord3);
   p.scales = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(scales + first * steps4 * kScaleBytes), 0,
                                                n * steps4 * kScaleBytes, kRsrcWord3);
+  p.n = n;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = 2 * wave_id() + i;
@@ -322,56 +327,79 @@ __device__ __forceinline__ Panel make_panel(const uint8_t* codes, const uint8_t*
   return p;
 }
 
-// Load i (0..7) of this wave's 8 KB of a panel's stage kt: step i % 4 of its
-// tile i / 4, lane after lane as it lies in memory. kt < 0: an offset behind
-// the resource's end, which fetches nothing (zeros), without a branch.
-__device__ __forceinline__ void load_codes(const Panel& p, int steps4, int kt, uint8_t* __restrict__ stage, int i) {
+// Load i (0..3) of this wave's 4 KB of one operand's half stage: step i % 2 of
+// its tile i / 2, lane after lane as it lies in memory. `half` counts half
+// stages along d; below 0: an offset behind the resource's end, which fetches
+// nothing (zeros), without a branch.
+__device__ __forceinline__ void load_codes(const Panel& p, int steps4, int half, uint8_t* __restrict__ panel, int i) {
   const int lane = threadIdx.x & 63;
-  const int at = (p.tile[i >> 2] * steps4 + (kt < 0 ? 0 : kt)) * (kSteps * kStepBytes) + (i & 3) * kStepBytes;
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(p.codes, (LdsPtr)(stage + (8 * wave_id() + i) * kStepBytes), 16,
-                                           lane * 16 + (kt < 0 ? kNoLoad : 0), at, 0, 0);
-}
-
-// Load i (0..1): the scales of its tile i.
-__device__ __forceinline__ void load_scales(const Panel& p, int steps4, int kt, uint8_t* __restrict__ stage, int i) {
-  const int lane = threadIdx.x & 63;
-  const int at = (p.tile[i] * steps4 + (kt < 0 ? 0 : kt)) * kScaleBytes;
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(p.scales, (LdsPtr)(stage + (2 * wave_id() + i) * kScaleBytes), 4,
-                                           lane * 4 + (kt < 0 ? kNoLoad : 0), at, 0, 0);
+  const int at = (p.tile[i >> 1] * (2 * steps4) + (half < 0 ? 0 : half)) * (kHalfSteps * kStepBytes) + (i & 1) * kStepBytes;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(p.codes, (LdsPtr)(panel + (4 * wave_id() + i) * kStepBytes), 16,
+                                           lane * 16 + (half < 0 ? kNoLoad : 0), at, 0, 0);
 }
 
 struct Tile {
   Panel h;
   Panel w;
+  int scale_off;     // this lane's tile in its wave's load of scales, in bytes
 };
+
+// The scales of a stage, four tiles of one panel in a wave's one load, 16 lanes
+// a tile: waves 0 and 1 take the hidden states' panel, 2 and 3 the projection's.
+__device__ __forceinline__ void load_scales(const Tile& t, int steps4, int kt, uint8_t* __restrict__ scales) {
+  const int lane = threadIdx.x & 63;
+  const int w = wave_id();
+  const int off = t.scale_off + (lane & 15) * 16 + (kt < 0 ? kNoLoad : 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(w < 2 ? t.h.scales : t.w.scales, (LdsPtr)(scales + w * 4 * kScaleBytes), 16,
+                                           off, (kt < 0 ? 0 : kt) * kScaleBytes, 0, 0);
+}
 
 __device__ __forceinline__ Tile make_tile(const TileGeo& g, int64_t m_t, int64_t n_t) {
   Tile t;
   t.h = make_panel(g.g.hc, g.g.hs, m_t * kPanelTiles, g.h_end, g.g.steps4);
   t.w = make_panel(g.g.wc, g.g.ws, n_t * kPanelTiles, g.w_end, g.g.steps4);
+  const int lane = threadIdx.x & 63;
+  const int n = wave_id() < 2 ? t.h.n : t.w.n;
+  const int tile = (wave_id() & 1) * 4 + (lane >> 4);
+  t.scale_off = (tile < n ? tile : n - 1) * g.g.steps4 * kScaleBytes;
   return t;
 }
 
-// LDS of a stage: the hidden states' codes, the projection's, then their scales.
-__device__ __forceinline__ void load_stage(const Tile& t, int steps4, int kt, uint8_t* __restrict__ stage) {
+// Half stage `half` (of stage half / 2) into its LDS buffer; the first half of
+// a stage brings the stage's scales.
+__device__ __forceinline__ void load_half(const Tile& t, int steps4, int half, int buf, uint8_t* __restrict__ smem) {
+  if ((buf & 1) == 0)
+    load_scales(t, steps4, half < 0 ? -1 : half >> 1, smem + kOffScales + (buf >> 1) * kStageScales);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) load_codes(t.h, steps4, kt, stage, i);
+  for (int i = 0; i < 4; ++i) load_codes(t.h, steps4, half, smem + buf * kHalfBytes, i);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) load_codes(t.w, steps4, kt, stage + kPanelBytes, i);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) load_scales(t.h, steps4, kt, stage + kOffScales, i);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) load_scales(t.w, steps4, kt, stage + kOffScales + kPanelScales, i);
+  for (int i = 0; i < 4; ++i) load_codes(t.w, steps4, half, smem + buf * kHalfBytes + kHalfPanel, i);
 }
 
-__device__ __forceinline__ void stage_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// Loads that a wave has in flight behind those that a half stage waits for: two
+// half stages, one of them with its stage's scales, and, where the last tile's
+// 32 stores were issued since, those.
+constexpr int kInFlight = 2 * 8 + 1;
+constexpr int kStores = 2 * kMB * kNB;
+static_assert(kInFlight + kStores <= 63, "the counter holds 6 bits");
+
+// Waits until all but the newest n of this wave's loads and stores are done
+// (they complete in order) and its LDS reads are, then for the workgroup.
+template <int n>
+__device__ __forceinline__ void half_barrier() {
+  static_assert(n == 0 || n == kInFlight || n == kInFlight + kStores, "one of the three counts");
+  if constexpr (n == 0)
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else if constexpr (n == kInFlight)
+    asm volatile("s_waitcnt vmcnt(17) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else
+    asm volatile("s_waitcnt vmcnt(49) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// Fragment of step kk of a wave's tile i (its 32 rows, 64 deep).
-__device__ __forceinline__ Frag frag(const uint8_t* __restrict__ codes, int first, int i, int kk) {
+// Fragment of step kk (0, 1) of a half stage of a wave's tile i (32 rows, 64 deep).
+__device__ __forceinline__ Frag frag(const uint8_t* __restrict__ panel, int first, int i, int kk) {
   const int lane = threadIdx.x & 63;
-  return *reinterpret_cast<const Frag*>(codes + ((first + i) * kSteps + kk) * kStepBytes + lane * 16);
+  return *reinterpret_cast<const Frag*>(panel + ((first + i) * kHalfSteps + kk) * kStepBytes + lane * 16);
 }
 
 __device__ __forceinline__ int scale_word(const uint8_t* __restrict__ scales, int first, int i) {
@@ -384,64 +412,76 @@ struct Scales {
   int w[kNB];
 };
 
+struct Ahead {      // of the half stage to come: its fragments, and its stage's scales
+  Frag a[kHalfSteps][kMB];
+  Frag b[kHalfSteps][kNB];
+  Scales sc;
+};
+
 // One step: 16 instructions, each followed by its share of the reads for the
-// step after next (8 fragments), of the next stage's scales (steps 2 and 3)
-// and of the loads of the stage after next (steps 2 and 3).
+// same step of the next half stage (8 fragments; with kk 1 and 2 of a stage's
+// second half also the next stage's 8 words of scales) and of the loads of the
+// half stage four ahead (8, and a stage's scales).
 template <int kk>
 __device__ __forceinline__ void mma_step(const Frag (&a)[kMB], const Frag (&b)[kNB], const Scales& sc,
-                                         f32x16 (&acc)[kMB][kNB], const uint8_t* __restrict__ from, int fm, int fn,
-                                         Frag (&na)[kMB], Frag (&nb)[kNB], Scales& next, const Tile& t, int steps4,
-                                         int kt, uint8_t* __restrict__ to) {
-  constexpr int nk = (kk + 2) % kSteps;
+                                         f32x16 (&acc)[kMB][kNB], const uint8_t* __restrict__ from,
+                                         const uint8_t* __restrict__ scales, int fm, int fn, Frag (&na)[kMB],
+                                         Frag (&nb)[kNB], Scales& next, const Tile& t, int steps4, int half, int buf,
+                                         uint8_t* __restrict__ smem) {
+  constexpr int step = kk % kHalfSteps;
 #pragma unroll
   for (int s = 0; s < kMB * kNB; ++s) {
     const int i = s / kNB, j = s % kNB;
     acc[i][j] = mma<kk>(b[j], a[i], acc[i][j], sc.w[j], sc.h[i]);
     if (s < kMB)
-      na[s] = frag(from, fm, s, nk);
+      na[s] = frag(from, fm, s, step);
     else if (s < kMB + kNB)
-      nb[s - kMB] = frag(from + kPanelBytes, fn, s - kMB, nk);
+      nb[s - kMB] = frag(from + kHalfPanel, fn, s - kMB, step);
     else if (kk == 2 && s < kMB + kNB + kMB)
-      next.h[s - kMB - kNB] = scale_word(from + kOffScales, fm, s - kMB - kNB);
-    else if (kk == 3 && s < kMB + kNB + kNB)
-      next.w[s - kMB - kNB] = scale_word(from + kOffScales + kPanelScales, fn, s - kMB - kNB);
-    if (kk == 2 && (s & 1) == 0) load_codes(t.h, steps4, kt, to, s >> 1);
-    if (kk == 3 && (s & 1) == 0) load_codes(t.w, steps4, kt, to + kPanelBytes, s >> 1);
-    if (kk == 2 && (s == 13 || s == 15)) load_scales(t.h, steps4, kt, to + kOffScales, s == 15);
-    if (kk == 3 && (s == 13 || s == 15)) load_scales(t.w, steps4, kt, to + kOffScales + kPanelScales, s == 15);
+      next.h[s - kMB - kNB] = scale_word(scales, fm, s - kMB - kNB);
+    else if (kk == 2)
+      next.w[s - 2 * kMB - kNB] = scale_word(scales + kPanelScales, fn, s - 2 * kMB - kNB);
+    if (kk == 0 && s == 1)
+      load_scales(t, steps4, half < 0 ? -1 : half >> 1, smem + kOffScales + (buf >> 1) * kStageScales);
+    if ((s & 3) == 2) {
+      if (step == 0)
+        load_codes(t.h, steps4, half, smem + buf * kHalfBytes, s >> 2);
+      else
+        load_codes(t.w, steps4, half, smem + buf * kHalfBytes + kHalfPanel, s >> 2);
+    }
     __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-struct Ahead {
-  Frag a[kSteps][kMB];
-  Frag b[kSteps][kNB];
-  Scales sc;
-};
-
-// The fragments of steps 0 and 1 and the scales of a landed stage.
-__device__ __forceinline__ void read_first(const uint8_t* __restrict__ stage, int fm, int fn, Ahead& f) {
+// The fragments of a landed half stage and its stage's scales.
+__device__ __forceinline__ void read_first(const uint8_t* __restrict__ smem, int buf, int fm, int fn, Ahead& f) {
+  const uint8_t* panel = smem + buf * kHalfBytes;
+  const uint8_t* scales = smem + kOffScales + (buf >> 1) * kStageScales;
 #pragma unroll
-  for (int kk = 0; kk < 2; ++kk) {
+  for (int kk = 0; kk < kHalfSteps; ++kk) {
 #pragma unroll
-    for (int i = 0; i < kMB; ++i) f.a[kk][i] = frag(stage, fm, i, kk);
+    for (int i = 0; i < kMB; ++i) f.a[kk][i] = frag(panel, fm, i, kk);
 #pragma unroll
-    for (int j = 0; j < kNB; ++j) f.b[kk][j] = frag(stage + kPanelBytes, fn, j, kk);
+    for (int j = 0; j < kNB; ++j) f.b[kk][j] = frag(panel + kHalfPanel, fn, j, kk);
   }
 #pragma unroll
-  for (int i = 0; i < kMB; ++i) f.sc.h[i] = scale_word(stage + kOffScales, fm, i);
+  for (int i = 0; i < kMB; ++i) f.sc.h[i] = scale_word(scales, fm, i);
 #pragma unroll
-  for (int j = 0; j < kNB; ++j) f.sc.w[j] = scale_word(stage + kOffScales + kPanelScales, fn, j);
+  for (int j = 0; j < kNB; ++j) f.sc.w[j] = scale_word(scales + kPanelScales, fn, j);
 }
 
-// Products of one tile. Stage kt lives in LDS buffer (kt + par) & 1. The
-// barrier behind step 1 waits for the next stage's loads and for every wave's
-// reads of this stage's buffer; steps 2 and 3 load into that buffer the stage
-// two ahead, of this tile or of the next one (tn; its stages 0 and 1 then are
-// in flight or landed on return, and its first fragments read).
+// Products of one tile. Half stage x of the tile lives in LDS buffer (2 par +
+// x) % 4. While it is multiplied, the fragments of half stage x + 1 are read;
+// the barrier before it waits for x + 1 to land in LDS and for every wave's
+// reads of x's buffer (made one half stage before), so that buffer takes half
+// stage x + 4: three half stages, about 3000 cycles, cover a load. Behind the
+// tile's end x + 1 and x + 4 are the next tile's (tn), whose half stages 0 to 3
+// are in flight or landed on return and whose first fragments are read.
+// stored: the wave's last 32 stores may still be in flight.
 __device__ __forceinline__ void tile_products(const TileGeo& g, const Tile& t, const Tile& tn, bool next, int par,
-                                              uint8_t* __restrict__ smem, f32x16 (&acc)[kMB][kNB], Ahead& f) {
-  const int wave = threadIdx.x >> 6;
+                                              bool stored, uint8_t* __restrict__ smem, f32x16 (&acc)[kMB][kNB],
+                                              Ahead& f) {
+  const int wave = wave_id();
   const int fm = (wave & 1) * kMB;
   const int fn = (wave >> 1) * kNB;
 #pragma unroll
@@ -453,29 +493,54 @@ __device__ __forceinline__ void tile_products(const TileGeo& g, const Tile& t, c
   const int n = g.g.steps4;
   const bool ahead = next && n >= 2;
   for (int kt = 0; kt < n; ++kt) {
-    uint8_t* cur = smem + ((kt + par) & 1) * kStageBytes;
-    uint8_t* nxt = smem + ((kt + par + 1) & 1) * kStageBytes;
-    Scales sn;
-    mma_step<0>(f.a[0], f.b[0], f.sc, acc, cur, fm, fn, f.a[2], f.b[2], sn, t, n, -1, cur);
-    mma_step<1>(f.a[1], f.b[1], f.sc, acc, cur, fm, fn, f.a[3], f.b[3], sn, t, n, -1, cur);
-    stage_barrier();
+    const int buf = 2 * ((kt + par) & 1);       // of this stage's first half; the next stage's are the other two
     const bool mine = kt + 2 < n;
     Tile q;
     q.h = mine ? t.h : tn.h;
     q.w = mine ? t.w : tn.w;
-    const int k2 = mine ? kt + 2 : (ahead ? kt + 2 - n : -1);
-    mma_step<2>(f.a[2], f.b[2], f.sc, acc, nxt, fm, fn, f.a[0], f.b[0], sn, q, n, k2, cur);
-    mma_step<3>(f.a[3], f.b[3], f.sc, acc, nxt, fm, fn, f.a[1], f.b[1], sn, q, n, k2, cur);
-    f.sc = sn;
+    q.scale_off = mine ? t.scale_off : tn.scale_off;
+    const int k2 = mine ? 2 * (kt + 2) : (ahead ? 2 * (kt + 2 - n) : -2);
+    Ahead o;
+    const uint8_t* second = smem + (buf + 1) * kHalfBytes;
+    if (stored && kt < 2)
+      half_barrier<kInFlight + kStores>();
+    else
+      half_barrier<kInFlight>();
+    mma_step<0>(f.a[0], f.b[0], f.sc, acc, second, nullptr, fm, fn, o.a[0], o.b[0], o.sc, q, n, k2, buf, smem);
+    mma_step<1>(f.a[1], f.b[1], f.sc, acc, second, nullptr, fm, fn, o.a[1], o.b[1], o.sc, q, n, k2, buf, smem);
+    const uint8_t* third = smem + (buf ^ 2) * kHalfBytes;
+    const uint8_t* scales = smem + kOffScales + ((buf ^ 2) >> 1) * kStageScales;
+    if (stored && kt == 0)
+      half_barrier<kInFlight + kStores>();
+    else
+      half_barrier<kInFlight>();
+    mma_step<2>(o.a[0], o.b[0], f.sc, acc, third, scales, fm, fn, f.a[0], f.b[0], o.sc, q, n, k2 + 1, buf + 1, smem);
+    mma_step<3>(o.a[1], o.b[1], f.sc, acc, third, scales, fm, fn, f.a[1], f.b[1], o.sc, q, n, k2 + 1, buf + 1, smem);
+    f.sc = o.sc;
   }
 }
 
-// Stores a wave's 128 x 128 logits; pads -inf.
-__device__ __forceinline__ void tile_store(const Geo& g, int64_t row0, int64_t col0, const f32x16 (&acc)[kMB][kNB],
+// Stores a wave's 128 x 128 logits; pads -inf. A part inside the matrix takes
+// kStores stores in every lane and returns true (uniform across the wave); at
+// an edge all stores are done on return.
+__device__ __forceinline__ bool tile_store(const Geo& g, int64_t row0, int64_t col0, const f32x16 (&acc)[kMB][kNB],
                                            uint16_t* __restrict__ out) {
   const int lane = threadIdx.x & 63;
   const int h = lane >> 5;
-  const bool all_real = col0 + kNB * 32 <= g.vocab_real;  // uniform
+  if (row0 + kMB * 32 <= g.n_rows && col0 + kNB * 32 <= g.vocab_real) {
+#pragma unroll
+    for (int i = 0; i < kMB; ++i) {
+      u32x4* dst = reinterpret_cast<u32x4*>(out + (row0 + i * 32 + (lane & 31)) * g.ldo + col0 + 16 * h);
+#pragma unroll
+      for (int j = 0; j < kNB; ++j) {
+        uint32_t w[8];
+        rlk::block_words(acc[i][j], w);
+        dst[4 * j] = u32x4{w[0], w[1], w[2], w[3]};
+        dst[4 * j + 1] = u32x4{w[4], w[5], w[6], w[7]};
+      }
+    }
+    return true;
+  }
 #pragma unroll
   for (int i = 0; i < kMB; ++i) {
     const int64_t row = row0 + i * 32 + (lane & 31);
@@ -483,44 +548,46 @@ __device__ __forceinline__ void tile_store(const Geo& g, int64_t row0, int64_t c
 #pragma unroll
     for (int j = 0; j < kNB; ++j) {
       uint32_t w[8];
-      rlk::block_words(acc[i][j], h, w);
+      rlk::block_words(acc[i][j], w);
       const int64_t c = col0 + j * 32 + 16 * h;
-      if (row >= g.n_rows) continue;
-      if (all_real) {
-        *reinterpret_cast<u32x4*>(dst + c) = u32x4{w[0], w[1], w[2], w[3]};
-        *reinterpret_cast<u32x4*>(dst + c + 8) = u32x4{w[4], w[5], w[6], w[7]};
-      } else if (c < g.vocab_padded) {
+      if (row < g.n_rows && c < g.vocab_padded) {
         rlk::store8(g.vocab_real, dst + c, c, w[0], w[1], w[2], w[3]);
         rlk::store8(g.vocab_real, dst + c + 8, c + 8, w[4], w[5], w[6], w[7]);
       }
     }
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  return false;
 }
 
 __global__ __launch_bounds__(kTilesThreads) void k_mx4_tiles(TileGeo g, uint16_t* __restrict__ out) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * kStageBytes];
-  const int64_t n_virtual = virtual_blocks(g);
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kSmemBytes];
+  const int n_virtual = virtual_blocks(g);
   const int n = g.g.steps4;
-  int64_t v = blockIdx.x, m_t = 0, n_t = 0;
+  int v = blockIdx.x, m_t = 0, n_t = 0;
   if (!next_tile(g, n_virtual, v, m_t, n_t)) return;  // uniform across the workgroup
-  const int wave = threadIdx.x >> 6;
+  const int wave = wave_id();
   const int fm = (wave & 1) * kMB;
   const int fn = (wave >> 1) * kNB;
   Tile t = make_tile(g, m_t, n_t);
   int par = 0;
+  bool stored = false;
   Ahead f;
-  load_stage(t, n, 0, smem);
-  load_stage(t, n, n > 1 ? 1 : -1, smem + kStageBytes);
-  stage_barrier();
-  read_first(smem, fm, fn, f);
-  int64_t v2 = v + gridDim.x, m2 = 0, n2 = 0;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) load_half(t, n, n > 1 || x < 2 ? x : -2, x, smem);
+  half_barrier<0>();
+  read_first(smem, 0, fm, fn, f);
+  int v2 = v + gridDim.x, m2 = 0, n2 = 0;
   bool more = next_tile(g, n_virtual, v2, m2, n2);
   Tile tn = more ? make_tile(g, m2, n2) : t;
   while (true) {
     f32x16 acc[kMB][kNB];
-    tile_products(g, t, tn, more, par, smem, acc, f);
-    tile_store(g.g, m_t * BM + fm * 32, n_t * BN + fn * 32, acc, out);
-    if (!more) break;
+    tile_products(g, t, tn, more, par, stored, smem, acc, f);
+    stored = tile_store(g.g, static_cast<int64_t>(m_t) * BM + fm * 32, static_cast<int64_t>(n_t) * BN + fn * 32, acc, out);
+    if (!more) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS is in flight when the workgroup ends
+      break;
+    }
     par = (par + n) & 1;
     m_t = m2;
     n_t = n2;
@@ -529,11 +596,15 @@ __global__ __launch_bounds__(kTilesThreads) void k_mx4_tiles(TileGeo g, uint16_t
     more = next_tile(g, n_virtual, v2, m2, n2);
     tn = more ? make_tile(g, m2, n2) : t;
     if (n == 1) {
-      // a one-stage tile could not load the next one in its loop; every wave
-      // is past the barrier behind its step 1, so the other buffer is free
-      load_stage(t, n, 0, smem + par * kStageBytes);
-      stage_barrier();
-      read_first(smem + par * kStageBytes, fm, fn, f);
+      // a tile of one stage could not load the next one in its loop: the other
+      // stage's buffers, which every wave has left (they were read behind the
+      // last barrier, as fragments that are replaced here)
+      half_barrier<0>();
+#pragma unroll
+      for (int x = 0; x < 2; ++x) load_half(t, n, x, 2 * par + x, smem);
+      half_barrier<0>();
+      stored = false;
+      read_first(smem, 2 * par, fm, fn, f);
     }
   }
 }
@@ -560,7 +631,7 @@ static int cu_count() {
 // One workgroup per compute unit (its LDS fills one), each looping over its
 // tiles; a multiple of 8, so a workgroup's tiles keep their XCD.
 static unsigned grid_for(const TileGeo& g) {
-  const int64_t v = virtual_blocks(g);
+  const int64_t v = virtual_blocks(g);  // below 2^30
   int64_t cap = cu_count();
   cap = cap > 0 ? (cap + kXcds - 1) / kXcds * kXcds : 256;
   return static_cast<unsigned>(v < cap ? v : cap);
@@ -657,10 +728,15 @@ int32_t rlk_mx4_linear(const uint16_t* hidden, int64_t n_rows, int64_t d_model, 
   if (n_rows > kRowsMost) {
     TileGeo t;
     t.g = g;
-    t.m_tiles = (n_rows + BM - 1) / BM;
-    t.n_tiles = (layout->vocab_padded + BN - 1) / BN;
-    t.m_groups = (t.m_tiles + kGM - 1) / kGM;
-    t.n_groups = (t.n_tiles + kGN - 1) / kGN;
+    t.m_tiles = static_cast<int>((n_rows + BM - 1) / BM);                       // at most 2^14
+    t.n_tiles = static_cast<int>((layout->vocab_padded + BN - 1) / BN);         // at most 2^22
+    // groups of at most 4 rows of tiles, as even as they go, and as wide as 32 compute units allow
+    t.m_groups = (t.m_tiles + 3) / 4;
+    t.gm = (t.m_tiles + t.m_groups - 1) / t.m_groups;
+    t.gn = kGroup / t.gm;
+    const int64_t groups = static_cast<int64_t>(t.m_groups) * ((t.n_tiles + t.gn - 1) / t.gn);
+    if (groups > (int64_t(1) << 25)) return RLK_ERR_SHAPE;
+    t.groups = static_cast<int>(groups);
     t.h_end = row_tiles(n_rows);
     t.w_end = row_tiles(layout->vocab_real);
     k_mx4_tiles<<<dim3(grid_for(t)), dim3(kTilesThreads), 0, stream>>>(t, logits_out);
