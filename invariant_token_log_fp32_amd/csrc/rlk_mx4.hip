@@ -422,7 +422,9 @@ struct Ahead {      // of the half stage to come: its fragments, and its stage's
 // same step of the next half stage (8 fragments; with kk 1 and 2 of a stage's
 // second half also the next stage's 8 words of scales) and of the loads of the
 // half stage four ahead (8, and a stage's scales).
-template <int kk>
+// kFirst: the tile's first step, whose accumulators are the instruction's
+// constant 0 (256 registers need no clearing).
+template <int kk, bool kFirst>
 __device__ __forceinline__ void mma_step(const Frag (&a)[kMB], const Frag (&b)[kNB], const Scales& sc,
                                          f32x16 (&acc)[kMB][kNB], const uint8_t* __restrict__ from,
                                          const uint8_t* __restrict__ scales, int fm, int fn, Frag (&na)[kMB],
@@ -432,7 +434,12 @@ __device__ __forceinline__ void mma_step(const Frag (&a)[kMB], const Frag (&b)[k
 #pragma unroll
   for (int s = 0; s < kMB * kNB; ++s) {
     const int i = s / kNB, j = s % kNB;
-    acc[i][j] = mma<kk>(b[j], a[i], acc[i][j], sc.w[j], sc.h[i]);
+    if constexpr (kFirst) {
+      const f32x16 zero = {};
+      acc[i][j] = mma<kk>(b[j], a[i], zero, sc.w[j], sc.h[i]);
+    } else {
+      acc[i][j] = mma<kk>(b[j], a[i], acc[i][j], sc.w[j], sc.h[i]);
+    }
     if (s < kMB)
       na[s] = frag(from, fm, s, step);
     else if (s < kMB + kNB)
@@ -478,65 +485,85 @@ __device__ __forceinline__ void read_first(const uint8_t* __restrict__ smem, int
 // tile's end x + 1 and x + 4 are the next tile's (tn), whose half stages 0 to 3
 // are in flight or landed on return and whose first fragments are read.
 // stored: the wave's last 32 stores may still be in flight.
+template <bool kFirst>
+__device__ __forceinline__ void stage_products(const Tile& t, const Tile& tn, bool ahead, int n, int kt, int par,
+                                               bool stored, uint8_t* __restrict__ smem, int fm, int fn,
+                                               f32x16 (&acc)[kMB][kNB], Ahead& f) {
+  const int buf = 2 * ((kt + par) & 1);       // of this stage's first half; the next stage's are the other two
+  const bool mine = kt + 2 < n;
+  Tile q;
+  q.h = mine ? t.h : tn.h;
+  q.w = mine ? t.w : tn.w;
+  q.scale_off = mine ? t.scale_off : tn.scale_off;
+  const int k2 = mine ? 2 * (kt + 2) : (ahead ? 2 * (kt + 2 - n) : -2);
+  Ahead o;
+  const uint8_t* second = smem + (buf + 1) * kHalfBytes;
+  if (stored && kt < 2)
+    half_barrier<kInFlight + kStores>();
+  else
+    half_barrier<kInFlight>();
+  mma_step<0, kFirst>(f.a[0], f.b[0], f.sc, acc, second, nullptr, fm, fn, o.a[0], o.b[0], o.sc, q, n, k2, buf, smem);
+  mma_step<1, false>(f.a[1], f.b[1], f.sc, acc, second, nullptr, fm, fn, o.a[1], o.b[1], o.sc, q, n, k2, buf, smem);
+  const uint8_t* third = smem + (buf ^ 2) * kHalfBytes;
+  const uint8_t* scales = smem + kOffScales + ((buf ^ 2) >> 1) * kStageScales;
+  if (kFirst && stored)
+    half_barrier<kInFlight + kStores>();
+  else
+    half_barrier<kInFlight>();
+  mma_step<2, false>(o.a[0], o.b[0], f.sc, acc, third, scales, fm, fn, f.a[0], f.b[0], o.sc, q, n, k2 + 1, buf + 1, smem);
+  mma_step<3, false>(o.a[1], o.b[1], f.sc, acc, third, scales, fm, fn, f.a[1], f.b[1], o.sc, q, n, k2 + 1, buf + 1, smem);
+  f.sc = o.sc;
+}
+
 __device__ __forceinline__ void tile_products(const TileGeo& g, const Tile& t, const Tile& tn, bool next, int par,
-                                              bool stored, uint8_t* __restrict__ smem, f32x16 (&acc)[kMB][kNB],
-                                              Ahead& f) {
-  const int wave = wave_id();
-  const int fm = (wave & 1) * kMB;
-  const int fn = (wave >> 1) * kNB;
-#pragma unroll
-  for (int i = 0; i < kMB; ++i)
-#pragma unroll
-    for (int j = 0; j < kNB; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+                                              bool stored, uint8_t* __restrict__ smem, int fm, int fn,
+                                              f32x16 (&acc)[kMB][kNB], Ahead& f) {
   const int n = g.g.steps4;
   const bool ahead = next && n >= 2;
-  for (int kt = 0; kt < n; ++kt) {
-    const int buf = 2 * ((kt + par) & 1);       // of this stage's first half; the next stage's are the other two
-    const bool mine = kt + 2 < n;
-    Tile q;
-    q.h = mine ? t.h : tn.h;
-    q.w = mine ? t.w : tn.w;
-    q.scale_off = mine ? t.scale_off : tn.scale_off;
-    const int k2 = mine ? 2 * (kt + 2) : (ahead ? 2 * (kt + 2 - n) : -2);
-    Ahead o;
-    const uint8_t* second = smem + (buf + 1) * kHalfBytes;
-    if (stored && kt < 2)
-      half_barrier<kInFlight + kStores>();
-    else
-      half_barrier<kInFlight>();
-    mma_step<0>(f.a[0], f.b[0], f.sc, acc, second, nullptr, fm, fn, o.a[0], o.b[0], o.sc, q, n, k2, buf, smem);
-    mma_step<1>(f.a[1], f.b[1], f.sc, acc, second, nullptr, fm, fn, o.a[1], o.b[1], o.sc, q, n, k2, buf, smem);
-    const uint8_t* third = smem + (buf ^ 2) * kHalfBytes;
-    const uint8_t* scales = smem + kOffScales + ((buf ^ 2) >> 1) * kStageScales;
-    if (stored && kt == 0)
-      half_barrier<kInFlight + kStores>();
-    else
-      half_barrier<kInFlight>();
-    mma_step<2>(o.a[0], o.b[0], f.sc, acc, third, scales, fm, fn, f.a[0], f.b[0], o.sc, q, n, k2 + 1, buf + 1, smem);
-    mma_step<3>(o.a[1], o.b[1], f.sc, acc, third, scales, fm, fn, f.a[1], f.b[1], o.sc, q, n, k2 + 1, buf + 1, smem);
-    f.sc = o.sc;
-  }
+  stage_products<true>(t, tn, ahead, n, 0, par, stored, smem, fm, fn, acc, f);
+  for (int kt = 1; kt < n; ++kt) stage_products<false>(t, tn, ahead, n, kt, par, stored, smem, fm, fn, acc, f);
+}
+
+// Lane l's value where bit b of l is clear, else lane l ^ (1 << b)'s `other`.
+template <int b>
+__device__ __forceinline__ u32x4 keep_or_take(const u32x4& mine, const u32x4& other, bool take) {
+  constexpr int perm = b == 0 ? 0xB1 : 0x4E;  // quads: lanes 1 0 3 2, lanes 2 3 0 1
+  const u32x4 o = {quad_perm<perm>(other.x), quad_perm<perm>(other.y), quad_perm<perm>(other.z), quad_perm<perm>(other.w)};
+  return u32x4{take ? o.x : mine.x, take ? o.y : mine.y, take ? o.z : mine.z, take ? o.w : mine.w};
 }
 
 // Stores a wave's 128 x 128 logits; pads -inf. A part inside the matrix takes
 // kStores stores in every lane and returns true (uniform across the wave); at
-// an edge all stores are done on return.
+// an edge all stores are done on return. Inside, lanes of a quad exchange
+// 16-byte pieces first (bit 0 of the lane for the piece, bit 1 for the block of
+// 32 columns), so that 8 lanes write a row's 128 bytes with one instruction: as
+// the accumulators lie, every lane of a store writes another row, which took
+// 11,300 cycles a tile.
 __device__ __forceinline__ bool tile_store(const Geo& g, int64_t row0, int64_t col0, const f32x16 (&acc)[kMB][kNB],
                                            uint16_t* __restrict__ out) {
   const int lane = threadIdx.x & 63;
   const int h = lane >> 5;
   if (row0 + kMB * 32 <= g.n_rows && col0 + kNB * 32 <= g.vocab_real) {
+    const bool b0 = (lane & 1) != 0, b1 = (lane & 2) != 0;
+    uint16_t* base = out + (row0 + (lane & 28)) * g.ldo + col0 + 32 * (b1 ? 1 : 0) + 16 * h + 8 * (b0 ? 1 : 0);
 #pragma unroll
     for (int i = 0; i < kMB; ++i) {
-      u32x4* dst = reinterpret_cast<u32x4*>(out + (row0 + i * 32 + (lane & 31)) * g.ldo + col0 + 16 * h);
 #pragma unroll
-      for (int j = 0; j < kNB; ++j) {
-        uint32_t w[8];
-        rlk::block_words(acc[i][j], w);
-        dst[4 * j] = u32x4{w[0], w[1], w[2], w[3]};
-        dst[4 * j + 1] = u32x4{w[4], w[5], w[6], w[7]};
+      for (int j = 0; j < kNB; j += 2) {
+        u32x4 even[2], odd[2];  // rows of even and of odd number, of block j + k: piece b0
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t w[8];
+          rlk::block_words(acc[i][j + k], w);
+          const u32x4 p0 = {w[0], w[1], w[2], w[3]}, p1 = {w[4], w[5], w[6], w[7]};
+          even[k] = keep_or_take<0>(p0, p1, b0);
+          odd[k] = keep_or_take<0>(p1, p0, !b0);
+        }
+        uint16_t* dst = base + static_cast<int64_t>(i * 32) * g.ldo + j * 32;
+        *reinterpret_cast<u32x4*>(dst) = keep_or_take<1>(even[0], even[1], b1);
+        *reinterpret_cast<u32x4*>(dst + g.ldo) = keep_or_take<1>(odd[0], odd[1], b1);
+        *reinterpret_cast<u32x4*>(dst + 2 * g.ldo) = keep_or_take<1>(even[1], even[0], !b1);
+        *reinterpret_cast<u32x4*>(dst + 3 * g.ldo) = keep_or_take<1>(odd[1], odd[0], !b1);
       }
     }
     return true;
@@ -582,7 +609,7 @@ __global__ __launch_bounds__(kTilesThreads) void k_mx4_tiles(TileGeo g, uint16_t
   Tile tn = more ? make_tile(g, m2, n2) : t;
   while (true) {
     f32x16 acc[kMB][kNB];
-    tile_products(g, t, tn, more, par, stored, smem, acc, f);
+    tile_products(g, t, tn, more, par, stored, smem, fm, fn, acc, f);
     stored = tile_store(g.g, static_cast<int64_t>(m_t) * BM + fm * 32, static_cast<int64_t>(n_t) * BN + fn * 32, acc, out);
     if (!more) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS is in flight when the workgroup ends
