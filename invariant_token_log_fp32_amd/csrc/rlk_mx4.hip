@@ -15,8 +15,6 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "bf16_store.hpp"
 #include "logp_device.hpp"
 #include "rlk_logp.h"
@@ -252,7 +250,7 @@ constexpr int kOffScales = 4 * kHalfBytes;                         // four half 
 constexpr int kStageScales = 2 * kPanelScales;
 constexpr int kSmemBytes = kOffScales + 2 * kStageScales;          // 136 KB
 constexpr int kXcds = 8;
-constexpr int kGroup = 32;                // tiles of a group: an XCD's compute units
+constexpr int kGroup = 32;                // tiles that an XCD's compute units take together
 constexpr int kRsrcWord3 = 0x00020000;    // raw buffer, 32-bit data format, no swizzle
 constexpr int kNoLoad = 0x40000000;       // an offset behind the end of every resource
 static_assert(BM == BN, "one panel shape for both operands");
@@ -264,116 +262,119 @@ struct TileGeo {
   Geo g;
   int m_tiles;
   int n_tiles;
-  int gm;            // a group is gm x gn tiles
-  int gn;
-  int m_groups;
-  int groups;
+  int band;          // rows of tiles in a band (the last may have fewer)
+  int chunk;         // columns of tiles in a chunk (8; with one band all of them)
   int64_t h_end;     // packed tiles of either operand
   int64_t w_end;
 };
 
-// Tile of virtual workgroup v, or false when v has none. Workgroup b runs on
-// XCD b % 8; an XCD takes groups of gm x gn tiles, one for each of its compute
-// units, that stream the same panels through its L2.
-__device__ __forceinline__ bool tile_of(const TileGeo& g, int v, int& m_t, int& n_t) {
-  const int slot = v / kXcds;
-  const int k = (slot / kGroup) * kXcds + v % kXcds;
-  const int local = slot % kGroup;
-  if (k >= g.groups) return false;
-  m_t = (k % g.m_groups) * g.gm + local % g.gm;
-  n_t = (k / g.m_groups) * g.gn + local / g.gm;
-  return local < g.gm * g.gn && m_t < g.m_tiles && n_t < g.n_tiles;
-}
+// The tiles of a workgroup. In order: chunks of columns of tiles, in a chunk
+// bands of up to 4 rows, in a band rows fastest. Workgroup b runs on XCD b % 8,
+// and an XCD's 32 workgroups take 32 neighbours of that order at a time (4 x 8
+// tiles), which stream the same 12 panels through its L2, while the XCDs
+// together go over one part of the projection for all rows. 256 tiles a round,
+// no gaps. (Band after band, each over the whole projection: 2.51 instead of
+// 2.44 ms for 8192 rows of the 151936 x 4096 head.)
+struct Walk {
+  int left;          // place in the chunk
+  int col0;          // the chunk's first column of tiles
+  int m_t, n_t;      // the tile
 
-__host__ __device__ __forceinline__ int virtual_blocks(const TileGeo& g) {
-  return ((g.groups + kXcds - 1) / kXcds) * kXcds * kGroup;
-}
-
-__device__ __forceinline__ bool next_tile(const TileGeo& g, int n_virtual, int& v, int& m_t, int& n_t) {
-  while (v < n_virtual) {
-    if (tile_of(g, v, m_t, n_t)) return true;
-    v += gridDim.x;
+  __device__ __forceinline__ explicit Walk(const TileGeo& g) {
+    left = (blockIdx.x % kXcds) * kGroup + blockIdx.x / kXcds;
+    col0 = 0;
   }
-  return false;
-}
 
-// One operand's 8 packed tiles as buffer resources. Wave w loads tiles 2w and
-// 2w + 1; a tile behind the operand's end is replaced by its last one (its
-// rows or columns are not stored), so every load is in range.
-struct Panel {
-  __amdgpu_buffer_rsrc_t codes;
-  __amdgpu_buffer_rsrc_t scales;
-  int tile[2];       // of this wave's loads, counted from the panel's first tile
-  int n;             // tiles that exist
+  __device__ __forceinline__ void step() { left += kXcds * kGroup; }
+
+  __device__ __forceinline__ bool find(const TileGeo& g) {
+    while (col0 < g.n_tiles) {
+      const int width = g.n_tiles - col0 < g.chunk ? g.n_tiles - col0 : g.chunk;
+      if (left < g.m_tiles * width) {
+        const int row0 = left / (g.band * width) * g.band;
+        const int rest = left - row0 * width;
+        const int rows = g.m_tiles - row0 < g.band ? g.m_tiles - row0 : g.band;
+        m_t = row0 + rest % rows;
+        n_t = col0 + rest / rows;
+        return true;
+      }
+      left -= g.m_tiles * width;
+      col0 += g.chunk;
+    }
+    return false;
+  }
 };
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6); }
 
-__device__ __forceinline__ Panel make_panel(const uint8_t* codes, const uint8_t* scales, int64_t tile0, int64_t end,
-                                            int steps4) {
-  Panel p;
-  const int64_t first = tile0 < end ? tile0 : end - 1;
-  const int n = static_cast<int>(end - first < kPanelTiles ? end - first : kPanelTiles);
-  p.codes = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(codes + first * steps4 * (kSteps * kStepBytes)), 0,
-                                              n * steps4 * (kSteps * kStepBytes), kRsrcWord3);
-  p.scales = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(scales + first * steps4 * kScaleBytes), 0,
-                                               n * steps4 * kScaleBytes, kRsrcWord3);
-  p.n = n;
+// What this wave loads of a tile: packed tiles 2w and 2w + 1 of either operand's
+// 8, and the scales of four (waves 0 and 1 the hidden states', 2 and 3 the
+// projection's). A tile behind the operand's end is replaced by its last one
+// (its rows or columns are not stored), so every load is in range.
+struct Tile {
+  const uint8_t* h;      // the panels' first tiles
+  const uint8_t* w;
+  const uint8_t* scales; // of this wave's scales
+  int h_at[2];           // byte offsets of this wave's tiles in them
+  int w_at[2];
+  int scales_at;         // and of this lane's (16 lanes a tile)
+};
+
+__device__ __forceinline__ Tile make_tile(const TileGeo& g, const Walk& at) {
+  const int lane = threadIdx.x & 63;
+  const int w = wave_id();
+  const int codes = g.g.steps4 * (kSteps * kStepBytes), scales = g.g.steps4 * kScaleBytes;  // of a packed tile
+  const int64_t h0 = static_cast<int64_t>(at.m_t) * kPanelTiles;
+  int64_t w0 = static_cast<int64_t>(at.n_t) * kPanelTiles;
+  if (w0 >= g.w_end) w0 = g.w_end - 1;  // pad columns alone
+  const int64_t hl = g.h_end - h0, wl = g.w_end - w0;
+  const int hn = static_cast<int>(hl < kPanelTiles ? hl : kPanelTiles) - 1;  // last tile of the panels
+  const int wn = static_cast<int>(wl < kPanelTiles ? wl : kPanelTiles) - 1;
+  Tile t;
+  t.h = g.g.hc + h0 * codes;
+  t.w = g.g.wc + w0 * codes;
+  t.scales = w < 2 ? g.g.hs + h0 * scales : g.g.ws + w0 * scales;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int t = 2 * wave_id() + i;
-    p.tile[i] = t < n ? t : n - 1;
+    t.h_at[i] = (2 * w + i < hn ? 2 * w + i : hn) * codes;
+    t.w_at[i] = (2 * w + i < wn ? 2 * w + i : wn) * codes;
   }
-  return p;
+  const int mine = (w & 1) * 4 + (lane >> 4), last = w < 2 ? hn : wn;
+  t.scales_at = (mine < last ? mine : last) * scales + (lane & 15) * 16;
+  return t;
+}
+
+// Every offset into a panel is below 2^23, kNoLoad is behind the resource's end.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t panel_rsrc(const uint8_t* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, kNoLoad, kRsrcWord3);
 }
 
 // Load i (0..3) of this wave's 4 KB of one operand's half stage: step i % 2 of
 // its tile i / 2, lane after lane as it lies in memory. `half` counts half
 // stages along d; below 0: an offset behind the resource's end, which fetches
 // nothing (zeros), without a branch.
-__device__ __forceinline__ void load_codes(const Panel& p, int steps4, int half, uint8_t* __restrict__ panel, int i) {
+__device__ __forceinline__ void load_codes(const uint8_t* p, const int (&at)[2], int half, uint8_t* __restrict__ panel,
+                                           int i) {
   const int lane = threadIdx.x & 63;
-  const int at = (p.tile[i >> 1] * (2 * steps4) + (half < 0 ? 0 : half)) * (kHalfSteps * kStepBytes) + (i & 1) * kStepBytes;
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(p.codes, (LdsPtr)(panel + (4 * wave_id() + i) * kStepBytes), 16,
-                                           lane * 16 + (half < 0 ? kNoLoad : 0), at, 0, 0);
+  const int off = at[i >> 1] + (half < 0 ? 0 : half) * (kHalfSteps * kStepBytes) + (i & 1) * kStepBytes;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(panel_rsrc(p), (LdsPtr)(panel + (4 * wave_id() + i) * kStepBytes), 16,
+                                           lane * 16 + (half < 0 ? kNoLoad : 0), off, 0, 0);
 }
 
-struct Tile {
-  Panel h;
-  Panel w;
-  int scale_off;     // this lane's tile in its wave's load of scales, in bytes
-};
-
-// The scales of a stage, four tiles of one panel in a wave's one load, 16 lanes
-// a tile: waves 0 and 1 take the hidden states' panel, 2 and 3 the projection's.
-__device__ __forceinline__ void load_scales(const Tile& t, int steps4, int kt, uint8_t* __restrict__ scales) {
-  const int lane = threadIdx.x & 63;
-  const int w = wave_id();
-  const int off = t.scale_off + (lane & 15) * 16 + (kt < 0 ? kNoLoad : 0);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(w < 2 ? t.h.scales : t.w.scales, (LdsPtr)(scales + w * 4 * kScaleBytes), 16,
-                                           off, (kt < 0 ? 0 : kt) * kScaleBytes, 0, 0);
-}
-
-__device__ __forceinline__ Tile make_tile(const TileGeo& g, int64_t m_t, int64_t n_t) {
-  Tile t;
-  t.h = make_panel(g.g.hc, g.g.hs, m_t * kPanelTiles, g.h_end, g.g.steps4);
-  t.w = make_panel(g.g.wc, g.g.ws, n_t * kPanelTiles, g.w_end, g.g.steps4);
-  const int lane = threadIdx.x & 63;
-  const int n = wave_id() < 2 ? t.h.n : t.w.n;
-  const int tile = (wave_id() & 1) * 4 + (lane >> 4);
-  t.scale_off = (tile < n ? tile : n - 1) * g.g.steps4 * kScaleBytes;
-  return t;
+// The scales of a stage, four tiles of one panel in a wave's one load.
+__device__ __forceinline__ void load_scales(const Tile& t, int kt, uint8_t* __restrict__ scales) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(panel_rsrc(t.scales), (LdsPtr)(scales + wave_id() * 4 * kScaleBytes), 16,
+                                           t.scales_at + (kt < 0 ? kNoLoad : 0), (kt < 0 ? 0 : kt) * kScaleBytes, 0, 0);
 }
 
 // Half stage `half` (of stage half / 2) into its LDS buffer; the first half of
 // a stage brings the stage's scales.
-__device__ __forceinline__ void load_half(const Tile& t, int steps4, int half, int buf, uint8_t* __restrict__ smem) {
-  if ((buf & 1) == 0)
-    load_scales(t, steps4, half < 0 ? -1 : half >> 1, smem + kOffScales + (buf >> 1) * kStageScales);
+__device__ __forceinline__ void load_half(const Tile& t, int half, int buf, uint8_t* __restrict__ smem) {
+  if ((buf & 1) == 0) load_scales(t, half < 0 ? -1 : half >> 1, smem + kOffScales + (buf >> 1) * kStageScales);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) load_codes(t.h, steps4, half, smem + buf * kHalfBytes, i);
+  for (int i = 0; i < 4; ++i) load_codes(t.h, t.h_at, half, smem + buf * kHalfBytes, i);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) load_codes(t.w, steps4, half, smem + buf * kHalfBytes + kHalfPanel, i);
+  for (int i = 0; i < 4; ++i) load_codes(t.w, t.w_at, half, smem + buf * kHalfBytes + kHalfPanel, i);
 }
 
 // Loads that a wave has in flight behind those that a half stage waits for: two
@@ -428,7 +429,7 @@ template <int kk, bool kFirst>
 __device__ __forceinline__ void mma_step(const Frag (&a)[kMB], const Frag (&b)[kNB], const Scales& sc,
                                          f32x16 (&acc)[kMB][kNB], const uint8_t* __restrict__ from,
                                          const uint8_t* __restrict__ scales, int fm, int fn, Frag (&na)[kMB],
-                                         Frag (&nb)[kNB], Scales& next, const Tile& t, int steps4, int half, int buf,
+                                         Frag (&nb)[kNB], Scales& next, const Tile& t, int half, int buf,
                                          uint8_t* __restrict__ smem) {
   constexpr int step = kk % kHalfSteps;
 #pragma unroll
@@ -449,12 +450,12 @@ __device__ __forceinline__ void mma_step(const Frag (&a)[kMB], const Frag (&b)[k
     else if (kk == 2)
       next.w[s - 2 * kMB - kNB] = scale_word(scales + kPanelScales, fn, s - 2 * kMB - kNB);
     if (kk == 0 && s == 1)
-      load_scales(t, steps4, half < 0 ? -1 : half >> 1, smem + kOffScales + (buf >> 1) * kStageScales);
+      load_scales(t, half < 0 ? -1 : half >> 1, smem + kOffScales + (buf >> 1) * kStageScales);
     if ((s & 3) == 2) {
       if (step == 0)
-        load_codes(t.h, steps4, half, smem + buf * kHalfBytes, s >> 2);
+        load_codes(t.h, t.h_at, half, smem + buf * kHalfBytes, s >> 2);
       else
-        load_codes(t.w, steps4, half, smem + buf * kHalfBytes + kHalfPanel, s >> 2);
+        load_codes(t.w, t.w_at, half, smem + buf * kHalfBytes + kHalfPanel, s >> 2);
     }
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -491,10 +492,7 @@ __device__ __forceinline__ void stage_products(const Tile& t, const Tile& tn, bo
                                                f32x16 (&acc)[kMB][kNB], Ahead& f) {
   const int buf = 2 * ((kt + par) & 1);       // of this stage's first half; the next stage's are the other two
   const bool mine = kt + 2 < n;
-  Tile q;
-  q.h = mine ? t.h : tn.h;
-  q.w = mine ? t.w : tn.w;
-  q.scale_off = mine ? t.scale_off : tn.scale_off;
+  const Tile q = mine ? t : tn;
   const int k2 = mine ? 2 * (kt + 2) : (ahead ? 2 * (kt + 2 - n) : -2);
   Ahead o;
   const uint8_t* second = smem + (buf + 1) * kHalfBytes;
@@ -502,16 +500,16 @@ __device__ __forceinline__ void stage_products(const Tile& t, const Tile& tn, bo
     half_barrier<kInFlight + kStores>();
   else
     half_barrier<kInFlight>();
-  mma_step<0, kFirst>(f.a[0], f.b[0], f.sc, acc, second, nullptr, fm, fn, o.a[0], o.b[0], o.sc, q, n, k2, buf, smem);
-  mma_step<1, false>(f.a[1], f.b[1], f.sc, acc, second, nullptr, fm, fn, o.a[1], o.b[1], o.sc, q, n, k2, buf, smem);
+  mma_step<0, kFirst>(f.a[0], f.b[0], f.sc, acc, second, nullptr, fm, fn, o.a[0], o.b[0], o.sc, q, k2, buf, smem);
+  mma_step<1, false>(f.a[1], f.b[1], f.sc, acc, second, nullptr, fm, fn, o.a[1], o.b[1], o.sc, q, k2, buf, smem);
   const uint8_t* third = smem + (buf ^ 2) * kHalfBytes;
   const uint8_t* scales = smem + kOffScales + ((buf ^ 2) >> 1) * kStageScales;
   if (kFirst && stored)
     half_barrier<kInFlight + kStores>();
   else
     half_barrier<kInFlight>();
-  mma_step<2, false>(o.a[0], o.b[0], f.sc, acc, third, scales, fm, fn, f.a[0], f.b[0], o.sc, q, n, k2 + 1, buf + 1, smem);
-  mma_step<3, false>(o.a[1], o.b[1], f.sc, acc, third, scales, fm, fn, f.a[1], f.b[1], o.sc, q, n, k2 + 1, buf + 1, smem);
+  mma_step<2, false>(o.a[0], o.b[0], f.sc, acc, third, scales, fm, fn, f.a[0], f.b[0], o.sc, q, k2 + 1, buf + 1, smem);
+  mma_step<3, false>(o.a[1], o.b[1], f.sc, acc, third, scales, fm, fn, f.a[1], f.b[1], o.sc, q, k2 + 1, buf + 1, smem);
   f.sc = o.sc;
 }
 
@@ -524,12 +522,34 @@ __device__ __forceinline__ void tile_products(const TileGeo& g, const Tile& t, c
   for (int kt = 1; kt < n; ++kt) stage_products<false>(t, tn, ahead, n, kt, par, stored, smem, fm, fn, acc, f);
 }
 
-// Lane l's value where bit b of l is clear, else lane l ^ (1 << b)'s `other`.
+// `mine` in the lanes of `keep`, else the `other` of lane l ^ (1 << b): one
+// select with its operand taken across the quad (written out, because the
+// compiler leaves the exchange and the select apart, twice the instructions;
+// the nop covers the distance that an exchange needs from its operand's write).
 template <int b>
-__device__ __forceinline__ u32x4 keep_or_take(const u32x4& mine, const u32x4& other, bool take) {
-  constexpr int perm = b == 0 ? 0xB1 : 0x4E;  // quads: lanes 1 0 3 2, lanes 2 3 0 1
-  const u32x4 o = {quad_perm<perm>(other.x), quad_perm<perm>(other.y), quad_perm<perm>(other.z), quad_perm<perm>(other.w)};
-  return u32x4{take ? o.x : mine.x, take ? o.y : mine.y, take ? o.z : mine.z, take ? o.w : mine.w};
+__device__ __forceinline__ u32x4 keep_or_take(const u32x4& mine, const u32x4& other, uint64_t keep) {
+  uint32_t x, y, z, w;
+  if constexpr (b == 0)
+    asm("s_mov_b64 vcc, %[keep]\n\ts_nop 1\n\t"
+        "v_cndmask_b32_dpp %[x], %[ox], %[mx], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %[y], %[oy], %[my], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %[z], %[oz], %[mz], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %[w], %[ow], %[mw], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf"
+        : [x] "=&v"(x), [y] "=&v"(y), [z] "=&v"(z), [w] "=&v"(w)
+        : [keep] "s"(keep), [mx] "v"(mine.x), [my] "v"(mine.y), [mz] "v"(mine.z), [mw] "v"(mine.w), [ox] "v"(other.x),
+          [oy] "v"(other.y), [oz] "v"(other.z), [ow] "v"(other.w)
+        : "vcc");
+  else
+    asm("s_mov_b64 vcc, %[keep]\n\ts_nop 1\n\t"
+        "v_cndmask_b32_dpp %[x], %[ox], %[mx], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %[y], %[oy], %[my], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %[z], %[oz], %[mz], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %[w], %[ow], %[mw], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf"
+        : [x] "=&v"(x), [y] "=&v"(y), [z] "=&v"(z), [w] "=&v"(w)
+        : [keep] "s"(keep), [mx] "v"(mine.x), [my] "v"(mine.y), [mz] "v"(mine.z), [mw] "v"(mine.w), [ox] "v"(other.x),
+          [oy] "v"(other.y), [oz] "v"(other.z), [ow] "v"(other.w)
+        : "vcc");
+  return u32x4{x, y, z, w};
 }
 
 // Stores a wave's 128 x 128 logits; pads -inf. A part inside the matrix takes
@@ -544,6 +564,7 @@ __device__ __forceinline__ bool tile_store(const Geo& g, int64_t row0, int64_t c
   const int lane = threadIdx.x & 63;
   const int h = lane >> 5;
   if (row0 + kMB * 32 <= g.n_rows && col0 + kNB * 32 <= g.vocab_real) {
+    constexpr uint64_t kClear0 = 0x5555555555555555ull, kClear1 = 0x3333333333333333ull;  // lanes with the bit clear
     const bool b0 = (lane & 1) != 0, b1 = (lane & 2) != 0;
     uint16_t* base = out + (row0 + (lane & 28)) * g.ldo + col0 + 32 * (b1 ? 1 : 0) + 16 * h + 8 * (b0 ? 1 : 0);
 #pragma unroll
@@ -556,14 +577,14 @@ __device__ __forceinline__ bool tile_store(const Geo& g, int64_t row0, int64_t c
           uint32_t w[8];
           rlk::block_words(acc[i][j + k], w);
           const u32x4 p0 = {w[0], w[1], w[2], w[3]}, p1 = {w[4], w[5], w[6], w[7]};
-          even[k] = keep_or_take<0>(p0, p1, b0);
-          odd[k] = keep_or_take<0>(p1, p0, !b0);
+          even[k] = keep_or_take<0>(p0, p1, kClear0);
+          odd[k] = keep_or_take<0>(p1, p0, ~kClear0);
         }
         uint16_t* dst = base + static_cast<int64_t>(i * 32) * g.ldo + j * 32;
-        *reinterpret_cast<u32x4*>(dst) = keep_or_take<1>(even[0], even[1], b1);
-        *reinterpret_cast<u32x4*>(dst + g.ldo) = keep_or_take<1>(odd[0], odd[1], b1);
-        *reinterpret_cast<u32x4*>(dst + 2 * g.ldo) = keep_or_take<1>(even[1], even[0], !b1);
-        *reinterpret_cast<u32x4*>(dst + 3 * g.ldo) = keep_or_take<1>(odd[1], odd[0], !b1);
+        *reinterpret_cast<u32x4*>(dst) = keep_or_take<1>(even[0], even[1], kClear1);
+        *reinterpret_cast<u32x4*>(dst + g.ldo) = keep_or_take<1>(odd[0], odd[1], kClear1);
+        *reinterpret_cast<u32x4*>(dst + 2 * g.ldo) = keep_or_take<1>(even[1], even[0], ~kClear1);
+        *reinterpret_cast<u32x4*>(dst + 3 * g.ldo) = keep_or_take<1>(odd[1], odd[0], ~kClear1);
       }
     }
     return true;
@@ -589,24 +610,24 @@ __device__ __forceinline__ bool tile_store(const Geo& g, int64_t row0, int64_t c
 
 __global__ __launch_bounds__(kTilesThreads) void k_mx4_tiles(TileGeo g, uint16_t* __restrict__ out) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[kSmemBytes];
-  const int n_virtual = virtual_blocks(g);
   const int n = g.g.steps4;
-  int v = blockIdx.x, m_t = 0, n_t = 0;
-  if (!next_tile(g, n_virtual, v, m_t, n_t)) return;  // uniform across the workgroup
+  Walk at(g);
+  if (!at.find(g)) return;  // uniform across the workgroup
   const int wave = wave_id();
   const int fm = (wave & 1) * kMB;
   const int fn = (wave >> 1) * kNB;
-  Tile t = make_tile(g, m_t, n_t);
+  Tile t = make_tile(g, at);
   int par = 0;
   bool stored = false;
   Ahead f;
 #pragma unroll
-  for (int x = 0; x < 4; ++x) load_half(t, n, n > 1 || x < 2 ? x : -2, x, smem);
+  for (int x = 0; x < 4; ++x) load_half(t, n > 1 || x < 2 ? x : -2, x, smem);
   half_barrier<0>();
   read_first(smem, 0, fm, fn, f);
-  int v2 = v + gridDim.x, m2 = 0, n2 = 0;
-  bool more = next_tile(g, n_virtual, v2, m2, n2);
-  Tile tn = more ? make_tile(g, m2, n2) : t;
+  int m_t = at.m_t, n_t = at.n_t;
+  at.step();
+  bool more = at.find(g);
+  Tile tn = more ? make_tile(g, at) : t;
   while (true) {
     f32x16 acc[kMB][kNB];
     tile_products(g, t, tn, more, par, stored, smem, fm, fn, acc, f);
@@ -616,19 +637,19 @@ __global__ __launch_bounds__(kTilesThreads) void k_mx4_tiles(TileGeo g, uint16_t
       break;
     }
     par = (par + n) & 1;
-    m_t = m2;
-    n_t = n2;
+    m_t = at.m_t;
+    n_t = at.n_t;
     t = tn;
-    v2 += gridDim.x;
-    more = next_tile(g, n_virtual, v2, m2, n2);
-    tn = more ? make_tile(g, m2, n2) : t;
+    at.step();
+    more = at.find(g);
+    tn = more ? make_tile(g, at) : t;
     if (n == 1) {
       // a tile of one stage could not load the next one in its loop: the other
       // stage's buffers, which every wave has left (they were read behind the
       // last barrier, as fragments that are replaced here)
       half_barrier<0>();
 #pragma unroll
-      for (int x = 0; x < 2; ++x) load_half(t, n, x, 2 * par + x, smem);
+      for (int x = 0; x < 2; ++x) load_half(t, x, 2 * par + x, smem);
       half_barrier<0>();
       stored = false;
       read_first(smem, 2 * par, fm, fn, f);
@@ -639,30 +660,6 @@ __global__ __launch_bounds__(kTilesThreads) void k_mx4_tiles(TileGeo g, uint16_t
 static bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 static int32_t launched() { return hipGetLastError() == hipSuccess ? RLK_OK : RLK_ERR_HIP; }
-
-// Compute units of the current device (cached per device; 0 if unknown).
-static int cu_count() {
-  static std::atomic<int> cache[64];
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 0;
-  if (dev < 64) {
-    const int c = cache[dev].load(std::memory_order_relaxed);
-    if (c > 0) return c;
-  }
-  int n = 0;
-  if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) return 0;
-  if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
-// One workgroup per compute unit (its LDS fills one), each looping over its
-// tiles; a multiple of 8, so a workgroup's tiles keep their XCD.
-static unsigned grid_for(const TileGeo& g) {
-  const int64_t v = virtual_blocks(g);  // below 2^30
-  int64_t cap = cu_count();
-  cap = cap > 0 ? (cap + kXcds - 1) / kXcds * kXcds : 256;
-  return static_cast<unsigned>(v < cap ? v : cap);
-}
 
 static int32_t launch_quantize(const uint16_t* x, int64_t n_rows, int64_t d, int64_t ldx, uint8_t* codes,
                                uint8_t* scales, uint16_t* values, int64_t ldv, hipStream_t stream) {
@@ -757,16 +754,13 @@ int32_t rlk_mx4_linear(const uint16_t* hidden, int64_t n_rows, int64_t d_model, 
     t.g = g;
     t.m_tiles = static_cast<int>((n_rows + BM - 1) / BM);                       // at most 2^14
     t.n_tiles = static_cast<int>((layout->vocab_padded + BN - 1) / BN);         // at most 2^22
-    // groups of at most 4 rows of tiles, as even as they go, and as wide as 32 compute units allow
-    t.m_groups = (t.m_tiles + 3) / 4;
-    t.gm = (t.m_tiles + t.m_groups - 1) / t.m_groups;
-    t.gn = kGroup / t.gm;
-    const int64_t groups = static_cast<int64_t>(t.m_groups) * ((t.n_tiles + t.gn - 1) / t.gn);
-    if (groups > (int64_t(1) << 25)) return RLK_ERR_SHAPE;
-    t.groups = static_cast<int>(groups);
+    const int bands = (t.m_tiles + 3) / 4;
+    t.band = (t.m_tiles + bands - 1) / bands;                                   // as even as they go
+    t.chunk = bands > 1 ? 8 : t.n_tiles;
     t.h_end = row_tiles(n_rows);
     t.w_end = row_tiles(layout->vocab_real);
-    k_mx4_tiles<<<dim3(grid_for(t)), dim3(kTilesThreads), 0, stream>>>(t, logits_out);
+    // one workgroup for each of 256 compute units (its LDS fills one), each walking over its tiles
+    k_mx4_tiles<<<dim3(kXcds * kGroup), dim3(kTilesThreads), 0, stream>>>(t, logits_out);
     return launched();
   }
   const int64_t col_tiles = layout->vocab_padded / kRowsCols;
