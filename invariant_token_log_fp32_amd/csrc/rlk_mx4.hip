@@ -42,7 +42,7 @@ constexpr int kMaxD = 65536;
 static bool shape_ok(int64_t n_rows, int64_t d) {
   return n_rows >= 0 && n_rows <= kMaxRows && d >= 32 && d <= kMaxD && d % 32 == 0;
 }
-static int64_t row_tiles(int64_t n_rows) { return (n_rows + kTileRows - 1) / kTileRows; }
+__host__ __device__ static inline int64_t row_tiles(int64_t n_rows) { return (n_rows + kTileRows - 1) / kTileRows; }
 static int64_t scale_steps(int64_t d) { return (d + kScaleK - 1) / kScaleK; }
 
 // ---------------------------------------------------------------------------
@@ -64,22 +64,16 @@ __device__ __forceinline__ uint32_t quad_perm(uint32_t v) {
   return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), Ctrl, 0xF, 0xF, true));
 }
 
-// Codes of 8 values (one lane's quarter of a block) and the block's scale byte.
-__device__ __forceinline__ void quantize8(const u32x4& v, uint32_t& code, uint32_t& byte) {
-  const uint32_t mask = 0x7FFF7FFFu;
-  uint32_t m = pk_max_u16(pk_max_u16(v.x & mask, v.y & mask), pk_max_u16(v.z & mask, v.w & mask));
-  m = pk_max_u16(m, quad_perm<0xB1>(m));  // lanes 1 0 3 2
-  m = pk_max_u16(m, quad_perm<0x4E>(m));  // lanes 2 3 0 1
-  const uint32_t lo = m & 0xFFFFu, hi = m >> 16;
-  const uint32_t top = lo > hi ? lo : hi;
-  if (top >= 0x7F80u) {  // NaN or an infinity in the block
-    byte = 255u;
-    code = 0u;
-    return;
-  }
-  // floor(log2 a) = exponent field - 127; a subnormal or zero field ends at byte 0 as well
+// Scale byte of a block whose largest magnitude pattern is `top`: 255 where it
+// holds NaN or an infinity, else floor(log2 a) - 2 + 127, at least 0 (the
+// exponent field is floor(log2 a) + 127; a subnormal or zero one ends at 0 too).
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
   const uint32_t field = top >> 7;
-  byte = field > 2u ? field - 2u : 0u;
+  return top >= 0x7F80u ? 255u : (field > 2u ? field - 2u : 0u);
+}
+
+// Codes of 8 values of a block with that scale byte.
+__device__ __forceinline__ uint32_t codes8(const u32x4& v, uint32_t byte) {
   const float up = __uint_as_float((254u - byte) << 23);  // 2^-e, at most 2^127
   float x[8];
   rlk::unpack8(v, x);
@@ -90,7 +84,18 @@ __device__ __forceinline__ void quantize8(const u32x4& v, uint32_t& code, uint32
   c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[2], x[3], 1.0f, 1);
   c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[4], x[5], 1.0f, 2);
   c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[6], x[7], 1.0f, 3);
-  code = c;
+  return byte == 255u ? 0u : c;
+}
+
+// The same for one lane's quarter of a block, whose maximum the quad shares.
+__device__ __forceinline__ void quantize8(const u32x4& v, uint32_t& code, uint32_t& byte) {
+  const uint32_t mask = 0x7FFF7FFFu;
+  uint32_t m = pk_max_u16(pk_max_u16(v.x & mask, v.y & mask), pk_max_u16(v.z & mask, v.w & mask));
+  m = pk_max_u16(m, quad_perm<0xB1>(m));  // lanes 1 0 3 2
+  m = pk_max_u16(m, quad_perm<0x4E>(m));  // lanes 2 3 0 1
+  const uint32_t lo = m & 0xFFFFu, hi = m >> 16;
+  byte = scale_byte(lo > hi ? lo : hi);
+  code = codes8(v, byte);
 }
 
 // The BF16 values that 8 codes stand for.
@@ -170,6 +175,34 @@ __device__ __forceinline__ f32x16 mma(const i32x4& w, const i32x4& h, const f32x
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, Sel, sw, Sel, sh);
 }
 
+typedef i32x4 Frag4;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kSteps = kScaleK / kStepK;  // 4 instructions deep: one word of scales
+constexpr int kRsrcWord3 = 0x00020000;    // raw buffer, 32-bit data format, no swizzle
+constexpr int kNoLoad = 0x40000000;       // an offset behind the end of every resource
+
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6); }
+
+// The 16 bytes of this lane in the KiB at byte `at` of a resource. The
+// projection is read once: non-temporal (1 row of the 151936 x 4096 head: 62.6
+// instead of 68.9 us).
+constexpr int kNonTemporal = 2;
+__device__ __forceinline__ Frag4 load_frag(__amdgpu_buffer_rsrc_t r, int lane, int at) {
+  return __builtin_bit_cast(Frag4, __builtin_amdgcn_raw_buffer_load_b128(r, lane * 16, at, kNonTemporal));
+}
+__device__ __forceinline__ int load_word(__amdgpu_buffer_rsrc_t r, int lane, int at) {
+  return static_cast<int>(__builtin_amdgcn_raw_buffer_load_b32(r, lane * 4, at, kNonTemporal));
+}
+
+// One step of a wave's tile against NB blocks of hidden rows.
+template <int Sel, int NB>
+__device__ __forceinline__ void stream_step(const Frag4& w, const Frag4 (&h)[NB], f32x16 (&acc)[NB], int sw,
+                                            const int (&sh)[NB]) {
+#pragma unroll
+  for (int b = 0; b < NB; ++b) acc[b] = mma<Sel>(w, h[b], acc[b], sw, sh[b]);
+}
+
 constexpr int kRowsThreads = 256;
 constexpr int kRowsCols = 64;  // columns of a wave
 constexpr int64_t kRowsMost = 128;  // rows up to which k_mx4_rows runs
@@ -232,6 +265,195 @@ __global__ __launch_bounds__(kRowsThreads) void k_mx4_rows(Geo g, int64_t col_ti
 }
 
 // ---------------------------------------------------------------------------
+// product, up to 128 rows: the projection streamed past the hidden states
+// ---------------------------------------------------------------------------
+
+// Few rows are bound by reading the projection once. A workgroup of 4 waves
+// splits d in 4 and keeps its hidden states in registers for good (wave w the
+// fragments of its quarter); packed tiles of 32 vocabulary rows stream through:
+// wave 0 multiplies the first quarter of a tile and hands the accumulators to
+// wave 1 in LDS while it begins the next tile, and so on, so every logit's sum
+// still runs in increasing k. A fragment's registers take the next tile's as
+// soon as it is multiplied, so loads are always on their way.
+constexpr int kStreamWaves = 4;
+constexpr int kStreamThreads = kStreamWaves * 64;
+constexpr int kStreamBlocks = 4;   // blocks of 32 hidden rows, at most
+constexpr int kStreamGroups = 4;   // groups of 256 values of d a wave, at most (d <= 4096): the registers' limit
+
+// One lane's block of 32 values (64 bytes of BF16), quantised as k_mx4_quantize does.
+__device__ __forceinline__ Frag4 quantize32(const u32x4 (&v)[4], uint32_t& byte) {
+  const uint32_t mask = 0x7FFF7FFFu;
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    m = pk_max_u16(m, pk_max_u16(pk_max_u16(v[i].x & mask, v[i].y & mask), pk_max_u16(v[i].z & mask, v[i].w & mask)));
+  const uint32_t lo = m & 0xFFFFu, hi = m >> 16;
+  byte = scale_byte(lo > hi ? lo : hi);
+  Frag4 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = static_cast<int>(codes8(v[i], byte));
+  return f;
+}
+
+__device__ __forceinline__ void stream_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Tiles that a wave's registers hold ahead, and workgroups of a compute unit:
+// two tiles or two workgroups (136 KB on their way in a compute unit) where the
+// registers allow, else one of each (NB = 4 with d above 2048).
+constexpr int stream_depth(int nb, int gp) { return gp == 4 && (nb == 1 || nb == 4) ? 1 : 2; }
+constexpr int stream_groups(int nb) { return nb == 1 ? 2 : 1; }
+
+template <int GP>
+struct StreamPart {     // a wave's part of a tile of the projection
+  Frag4 f[GP * kSteps];
+  int sc[GP];
+};
+
+template <int NB, int GP>
+__global__ __launch_bounds__(kStreamThreads, stream_groups(NB)) void k_mx4_stream(
+    Geo g, const uint16_t* __restrict__ hidden, int64_t ldh, int d, int tiles, int w_tiles, uint16_t* __restrict__ out) {
+  constexpr int kDepth = stream_depth(NB, GP);
+  __shared__ f32x4 slots[kStreamWaves - 1][NB][4][64];
+  const int lane = threadIdx.x & 63;
+  const int w = wave_id();
+  const int per = (g.steps4 + kStreamWaves - 1) / kStreamWaves;   // groups of a wave, at most GP
+  const int g0 = w * per;
+  const int cnt = g.steps4 - g0 < per ? g.steps4 - g0 : per;       // may be below 1
+  // this workgroup's tiles: neighbours, so that the two halves of a line of logits meet in L2
+  const int share = (tiles + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  const int first = static_cast<int>(blockIdx.x) * share;
+  const int n_tiles = tiles - first < share ? tiles - first : share;
+  if (n_tiles <= 0) return;  // uniform across the workgroup
+  const int64_t codes = static_cast<int64_t>(g.steps4) * (kSteps * kStepBytes);  // of a packed tile
+  const int64_t scales = static_cast<int64_t>(g.steps4) * kScaleBytes;
+
+  // this wave's part of the i-th tile; behind the last one nothing is fetched
+  const auto rsrcs = [&](int i, __amdgpu_buffer_rsrc_t& rc, __amdgpu_buffer_rsrc_t& rs) {
+    const int t = first + i < w_tiles ? first + i : w_tiles - 1;  // pad columns alone: any tile, not stored
+    const int most = i < n_tiles ? kNoLoad : 0;
+    rc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(g.wc + t * codes + static_cast<int64_t>(g0) * (kSteps * kStepBytes)), 0, most, kRsrcWord3);
+    rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.ws + t * scales + static_cast<int64_t>(g0) * kScaleBytes), 0,
+                                           most, kRsrcWord3);
+  };
+  StreamPart<GP> part[kDepth];
+#pragma unroll
+  for (int p = 0; p < kDepth; ++p) {
+    __amdgpu_buffer_rsrc_t rc, rs;
+    rsrcs(p, rc, rs);
+#pragma unroll
+    for (int q = 0; q < GP; ++q)
+      if (q < cnt) {
+        part[p].sc[q] = load_word(rs, lane, q * kScaleBytes);
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) part[p].f[q * kSteps + u] = load_frag(rc, lane, (q * kSteps + u) * kStepBytes);
+      }
+  }
+
+  Frag4 hf[GP * kSteps][NB];
+  int hsc[GP][NB];
+#pragma unroll
+  for (int q = 0; q < GP; ++q) {
+    if (q >= cnt) continue;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      if constexpr (NB == 1) {
+        // few enough rows for every workgroup to quantise them itself: no launch before this one
+        const int row = lane & 31;
+        uint32_t word = 0;
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+          const int k = (g0 + q) * kScaleK + u * kStepK + (lane >> 5) * 32;
+          u32x4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i] = u32x4{0u, 0u, 0u, 0u};
+            if (row < g.n_rows && k < d) v[i] = *reinterpret_cast<const u32x4*>(hidden + row * ldh + k + 8 * i);
+          }
+          uint32_t byte;
+          hf[q * kSteps + u][b] = quantize32(v, byte);
+          word |= byte << (8 * u);
+        }
+        hsc[q][b] = static_cast<int>(word);
+      } else {
+        const int t = b < row_tiles(g.n_rows) ? b : 0;  // (three blocks of rows run as four)
+        const uint8_t* at = g.hc + t * codes + static_cast<int64_t>(g0 + q) * (kSteps * kStepBytes);
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) hf[q * kSteps + u][b] = *reinterpret_cast<const Frag4*>(at + u * kStepBytes + lane * 16);
+        hsc[q][b] = *reinterpret_cast<const int*>(g.hs + t * scales + static_cast<int64_t>(g0 + q) * kScaleBytes + lane * 4);
+      }
+    }
+  }
+
+  // the i-th tile: its products, each fragment's registers then taking tile i + kDepth's
+  const auto multiply = [&](StreamPart<GP>& p, int i, f32x16 (&acc)[NB]) {
+    __amdgpu_buffer_rsrc_t rc, rs;
+    rsrcs(i + kDepth, rc, rs);
+#pragma unroll
+    for (int q = 0; q < GP; ++q) {
+      if (q >= cnt) continue;
+      const int sw = p.sc[q];
+      p.sc[q] = load_word(rs, lane, q * kScaleBytes);
+      Frag4(&f)[GP * kSteps] = p.f;
+      stream_step<0, NB>(f[q * kSteps], hf[q * kSteps], acc, sw, hsc[q]);
+      f[q * kSteps] = load_frag(rc, lane, q * kSteps * kStepBytes);
+      stream_step<1, NB>(f[q * kSteps + 1], hf[q * kSteps + 1], acc, sw, hsc[q]);
+      f[q * kSteps + 1] = load_frag(rc, lane, (q * kSteps + 1) * kStepBytes);
+      stream_step<2, NB>(f[q * kSteps + 2], hf[q * kSteps + 2], acc, sw, hsc[q]);
+      f[q * kSteps + 2] = load_frag(rc, lane, (q * kSteps + 2) * kStepBytes);
+      stream_step<3, NB>(f[q * kSteps + 3], hf[q * kSteps + 3], acc, sw, hsc[q]);
+      f[q * kSteps + 3] = load_frag(rc, lane, (q * kSteps + 3) * kStepBytes);
+    }
+  };
+
+  for (int turn = 0; turn < n_tiles + kStreamWaves - 1; ++turn) {
+    const int i = turn - w;
+    const bool on = i >= 0 && i < n_tiles;  // uniform across the wave
+    f32x16 acc[NB];
+    if (on) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const f32x4 v = w == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : slots[w - 1][b][e][lane];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[b][4 * e + k] = v[k];
+        }
+    }
+    stream_barrier();  // every slot is read
+    if (on) {
+      if (kDepth == 1 || (i & 1) == 0)
+        multiply(part[0], i, acc);
+      else
+        multiply(part[kDepth - 1], i, acc);
+      if (w < kStreamWaves - 1) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            slots[w][b][e][lane] = f32x4{acc[b][4 * e], acc[b][4 * e + 1], acc[b][4 * e + 2], acc[b][4 * e + 3]};
+      } else {
+        const int h = lane >> 5;
+        const int64_t c = static_cast<int64_t>(first + i) * kTileRows + 16 * h;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint32_t x[8];
+          rlk::block_words(acc[b], x);
+          const int64_t row = b * kTileRows + (lane & 31);
+          if (row < g.n_rows && c < g.vocab_padded) {
+            rlk::store8(g.vocab_real, out + row * g.ldo + c, c, x[0], x[1], x[2], x[3]);
+            rlk::store8(g.vocab_real, out + row * g.ldo + c + 8, c + 8, x[4], x[5], x[6], x[7]);
+          }
+        }
+      }
+    }
+    stream_barrier();  // every slot is written
+  }
+}
+
+// ---------------------------------------------------------------------------
 // product, many rows: 256 x 256 tiles
 // ---------------------------------------------------------------------------
 
@@ -241,7 +463,6 @@ constexpr int kTilesThreads = 256;        // 4 waves, 2 x 2, each 128 x 128
 constexpr int kPanelTiles = BM / kTileRows;      // 8 packed tiles of either operand
 constexpr int kMB = 4;                    // 32 x 32 blocks of a wave, either way
 constexpr int kNB = 4;
-constexpr int kSteps = kScaleK / kStepK;  // 4 instructions deep: one word of scales
 constexpr int kHalfSteps = kSteps / 2;    // steps of a half stage (128 values of d)
 constexpr int kHalfPanel = kPanelTiles * kHalfSteps * kStepBytes;  // 16 KB of codes of one operand
 constexpr int kHalfBytes = 2 * kHalfPanel;                         // both operands
@@ -251,12 +472,10 @@ constexpr int kStageScales = 2 * kPanelScales;
 constexpr int kSmemBytes = kOffScales + 2 * kStageScales;          // 136 KB
 constexpr int kXcds = 8;
 constexpr int kGroup = 32;                // tiles that an XCD's compute units take together
-constexpr int kRsrcWord3 = 0x00020000;    // raw buffer, 32-bit data format, no swizzle
-constexpr int kNoLoad = 0x40000000;       // an offset behind the end of every resource
 static_assert(BM == BN, "one panel shape for both operands");
 
 typedef __attribute__((address_space(3))) void* LdsPtr;
-typedef i32x4 Frag;
+typedef Frag4 Frag;
 
 struct TileGeo {
   Geo g;
@@ -304,8 +523,6 @@ struct Walk {
     return false;
   }
 };
-
-__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6); }
 
 // What this wave loads of a tile: packed tiles 2w and 2w + 1 of either operand's
 // 8, and the scales of four (waves 0 and 1 the hidden states', 2 and 3 the
@@ -671,6 +888,31 @@ static int32_t launch_quantize(const uint16_t* x, int64_t n_rows, int64_t d, int
   return launched();
 }
 
+template <int NB>
+static void launch_stream_blocks(const Geo& g, const uint16_t* hidden, int64_t ldh, int d, uint16_t* out, hipStream_t stream) {
+  const int tiles = static_cast<int>(g.vocab_padded / kTileRows);  // at most 2^25
+  const int w_tiles = static_cast<int>(row_tiles(g.vocab_real));
+  const int most = 256 * stream_groups(NB);
+  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most)), block(kStreamThreads);
+  const int per = (g.steps4 + kStreamWaves - 1) / kStreamWaves;
+  if (per <= 1)
+    k_mx4_stream<NB, 1><<<grid, block, 0, stream>>>(g, hidden, ldh, d, tiles, w_tiles, out);
+  else if (per <= 2)
+    k_mx4_stream<NB, 2><<<grid, block, 0, stream>>>(g, hidden, ldh, d, tiles, w_tiles, out);
+  else
+    k_mx4_stream<NB, 4><<<grid, block, 0, stream>>>(g, hidden, ldh, d, tiles, w_tiles, out);
+}
+
+static void launch_stream(const Geo& g, int blocks, const uint16_t* hidden, int64_t ldh, int d, uint16_t* out,
+                          hipStream_t stream) {
+  if (blocks == 1)
+    launch_stream_blocks<1>(g, hidden, ldh, d, out, stream);
+  else if (blocks == 2)
+    launch_stream_blocks<2>(g, hidden, ldh, d, out, stream);
+  else
+    launch_stream_blocks<4>(g, hidden, ldh, d, out, stream);
+}
+
 static int32_t check_layout(const rlk_vocab_layout* L) {
   if (L == nullptr) return RLK_ERR_NULL;
   if (L->n_shards != 8) return RLK_ERR_SHAPE;
@@ -738,7 +980,6 @@ int32_t rlk_mx4_linear(const uint16_t* hidden, int64_t n_rows, int64_t d_model, 
   if (workspace_bytes < rlk_mx4_linear_workspace_bytes(n_rows, d_model)) return RLK_ERR_WORKSPACE;
   uint8_t* hc = static_cast<uint8_t*>(workspace);
   uint8_t* hs = hc + rlk_mx4_codes_bytes(n_rows, d_model);
-  if ((st = launch_quantize(hidden, n_rows, d_model, hidden_stride, hc, hs, nullptr, 0, stream)) != RLK_OK) return st;
   Geo g;
   g.hc = hc;
   g.hs = hs;
@@ -749,6 +990,15 @@ int32_t rlk_mx4_linear(const uint16_t* hidden, int64_t n_rows, int64_t d_model, 
   g.vocab_padded = layout->vocab_padded;
   g.ldo = layout->row_stride;
   g.steps4 = static_cast<int>(scale_steps(d_model));
+  const int blocks_of_rows = static_cast<int>(row_tiles(n_rows) < 8 ? row_tiles(n_rows) : 8);
+  const bool streamed = blocks_of_rows <= kStreamBlocks && g.steps4 <= kStreamWaves * kStreamGroups;
+  if (!(streamed && blocks_of_rows == 1) &&
+      (st = launch_quantize(hidden, n_rows, d_model, hidden_stride, hc, hs, nullptr, 0, stream)) != RLK_OK)
+    return st;
+  if (streamed) {
+    launch_stream(g, blocks_of_rows, hidden, hidden_stride, static_cast<int>(d_model), logits_out, stream);
+    return launched();
+  }
   if (n_rows > kRowsMost) {
     TileGeo t;
     t.g = g;
