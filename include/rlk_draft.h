@@ -98,7 +98,7 @@ int32_t rlk_draft_verify(const rlk_scored_rows* target, const rlk_scored_rows* d
                          const double* sample_u, int64_t* token_out, int32_t* accepted_out, float* policy_out,
                          float* ref_out, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
-/* Bytes of workspace: one float64 per sequence and 2048 columns; 0 for an
+/* Bytes of workspace: one float64 per sequence and 512 columns; 0 for an
  * invalid layout or n_seq outside [0, 2^22]. */
 size_t rlk_draft_workspace_bytes(int64_t n_seq, const rlk_vocab_layout* layout);
 

@@ -1,13 +1,18 @@
 // Verification of drafted tokens, and the C ABI declared in include/rlk_draft.h.
 //
 // Kernels:
-//   k_draft_sums  a wave per (sequence, chunk of 2048 columns): finds where the
-//                 sequence's accepted tokens end (64 drafted tokens at a time,
-//                 again in every wave: three numbers a token), then sums the
-//                 weights of its columns, max(p - q, 0) or p, in float64.
-//   k_draft_pick  a wave per sequence: the chunk in which the running sum
-//                 passes sample_u times the whole, that chunk's columns again,
-//                 the outputs.
+//   k_draft<.., kWhole>  one workgroup a sequence (kWhole, many sequences) or
+//                 several, each for a run of the row's pieces of 512 columns.
+//                 Every wave finds where the sequence's accepted tokens end (64
+//                 drafted tokens at a time: three numbers a token), then sums
+//                 the weights of its pieces, max(p - q, 0) or p, in float64. A
+//                 whole sequence is drawn from and written at once; else the
+//                 sums go to the workspace and
+//   k_draft_pick  a wave a sequence, finds the piece in which the running sum
+//                 passes sample_u times the whole, reads that piece's columns
+//                 again and writes the outputs.
+// Piece sums are formed in one order whichever kernel forms them, so a
+// sequence's outputs do not depend on the batch.
 #include <hip/hip_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -23,9 +28,9 @@ using rlk::u32x4;
 
 typedef unsigned long long u64;
 
-constexpr int kChunkVecs = 4;                          // 16-byte vectors of a lane in a chunk
-constexpr int kChunk = kChunkVecs * kWave * 8;         // 2048 columns
-constexpr int kThreads = 256;
+constexpr int kPiece = kWave * 8;   // 512 columns: one 16-byte vector a lane
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / kWave;
 constexpr int64_t kMaxRows = int64_t(1) << 22;
 constexpr int64_t kMaxVocab = int64_t(1) << 30;
 
@@ -35,7 +40,7 @@ struct Args {
   int64_t n_seq;
   int64_t n_draft;
   int64_t vocab_real;
-  int64_t n_chunks;
+  int64_t n_pieces;
   const int64_t* start;
   const int64_t* token;
   const double* accept_u;
@@ -44,7 +49,7 @@ struct Args {
   int32_t* accepted_out;
   float* policy_out;
   float* ref_out;
-  double* sums;           // [n_seq][n_chunks]
+  double* sums;           // [n_seq][n_pieces]
 };
 
 // Where a sequence's accepted tokens end (uniform across the wave).
@@ -103,6 +108,30 @@ __device__ __forceinline__ Stop find_stop(const Args& a, int64_t s, int lane) {
   return r;
 }
 
+// e^y for y up to about 1, to a few 2^-53 of the value: y = n ln 2 + r with ln 2
+// in two parts, the series of e^r to r^12 (|r| <= ln(2) / 2 leaves 2e-16). -inf
+// and anything below -1000 gives 0.
+__device__ __forceinline__ double exp_down(double y) {
+  y = fmax(y, -1000.0);
+  const double n = rint(y * 1.4426950408889634074);
+  double r = fma(-n, 6.93147180369123816490e-01, y);
+  r = fma(-n, 1.90821492927058770002e-10, r);
+  double p = 2.08767569878680989792e-09;  // 1 / 12!
+  p = fma(p, r, 2.50521083854417187751e-08);
+  p = fma(p, r, 2.75573192239858906526e-07);
+  p = fma(p, r, 2.75573192239858906526e-06);
+  p = fma(p, r, 2.48015873015873015873e-05);
+  p = fma(p, r, 1.98412698412698412698e-04);
+  p = fma(p, r, 1.38888888888888888889e-03);
+  p = fma(p, r, 8.33333333333333333333e-03);
+  p = fma(p, r, 4.16666666666666666667e-02);
+  p = fma(p, r, 1.66666666666666666667e-01);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return ldexp(p, static_cast<int>(n));
+}
+
 // One side's policy over the columns of a row.
 struct Policy {
   double inv_t;
@@ -121,9 +150,73 @@ struct Policy {
   __device__ __forceinline__ float scaled(float x) const { return static_cast<float>(static_cast<double>(x) * inv_t); }
 
   __device__ __forceinline__ double mass(float x) const {
-    return x >= threshold ? exp(static_cast<double>(scaled(x)) - part) : 0.0;
+    return x >= threshold ? exp_down(static_cast<double>(scaled(x)) - part) : 0.0;
   }
 };
+
+// Weights by BF16 pattern: a row of 152,000 columns holds a few thousand
+// distinct values, so a workgroup with many columns to weigh computes each
+// once. The table covers magnitudes of 2^-12 to 64 of either sign, interleaved
+// (slot 2 (m - kMagLo) + sign, m the 15-bit magnitude pattern); other values
+// are computed where they stand.
+constexpr uint32_t kMagLo = 0x3980u;                 // 2^-12
+constexpr int kMags = 0x4280 - 0x3980;               // to 64: 18 binades of 128 values
+constexpr int kSlots = 2 * kMags;                    // 36 KB of float64
+
+__device__ __forceinline__ uint32_t slot_bits(int slot) {
+  return (kMagLo + static_cast<uint32_t>(slot >> 1)) | (static_cast<uint32_t>(slot & 1) << 15);
+}
+
+// The slots of the two values of a word; at least kSlots where one is outside.
+__device__ __forceinline__ uint32_t slots2(uint32_t w) {
+  uint32_t sign, twice, slot;
+  asm("v_pk_lshrrev_b16 %[sign], %[c15], %[w]\n\t"
+      "v_pk_mad_u16 %[twice], %[w], %[c2], %[sign]\n\t"
+      "v_pk_sub_u16 %[slot], %[twice], %[lo]"
+      : [sign] "=&v"(sign), [twice] "=&v"(twice), [slot] "=&v"(slot)
+      : [w] "v"(w), [c15] "v"(0x000F000Fu), [c2] "v"(0x00020002u), [lo] "v"(2u * kMagLo * 0x10001u));
+  return slot;
+}
+static_assert(2u * kMagLo <= 0xFFFFu && kSlots <= 0xFFFF, "slots are 16-bit numbers");
+
+__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("v_pk_max_u16 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+
+// Weights of the 8 columns of a vector, from the table where all 8 are in it.
+__device__ __forceinline__ void look_up(const double* __restrict__ table, const Policy& p, const u32x4& v, double (&m)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] = slots2(w[i]);
+  const uint32_t top = pk_max(pk_max(s[0], s[1]), pk_max(s[2], s[3]));
+  if ((top & 0xFFFFu) < kSlots && (top >> 16) < kSlots) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[2 * i] = table[s[i] & 0xFFFFu];
+      m[2 * i + 1] = table[s[i] >> 16];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t slot = (s[e >> 1] >> ((e & 1) * 16)) & 0xFFFFu;
+      const uint32_t b = (w[e >> 1] >> ((e & 1) * 16)) & 0xFFFFu;
+      if (slot < kSlots)
+        m[e] = table[slot];
+      else
+        m[e] = b == 0xFF80u ? 0.0 : p.mass(__uint_as_float(b << 16));
+    }
+  }
+}
+
+__device__ __forceinline__ void compute(const Policy& p, const u32x4& v, double (&m)[8]) {
+  float x[8];
+  rlk::unpack8(v, x);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m[e] = p.mass(x[e]);
+}
 
 // What the columns of one sequence's row weigh.
 struct Weights {
@@ -150,18 +243,33 @@ struct Weights {
     }
   }
 
-  // Weights of the 8 columns of vector v (columns from `real` on weigh nothing).
-  __device__ __forceinline__ void columns(int64_t v, int64_t real, double (&w)[8]) const {
-    float x[8], y[8];
-    rlk::unpack8(p_row[v], x);
-    if (q_row != nullptr) rlk::unpack8(q_row[v], y);
+  // Weights of the 8 columns from `column` on (those from `real` on weigh
+  // nothing), given both sides' vectors and, with kTable, tables.
+  template <bool kTable>
+  __device__ __forceinline__ void columns(const u32x4& x, const u32x4& y, const double* __restrict__ table, int64_t column,
+                                          int64_t real, double (&m)[8]) const {
+    if constexpr (kTable)
+      look_up(table, p, x, m);
+    else
+      compute(p, x, m);
+    if (q_row != nullptr) {
+      double n[8];
+      if constexpr (kTable)
+        look_up(table + kSlots, q, y, n);
+      else
+        compute(q, y, n);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int64_t c = v * 8 + e;
-      double m = c < real ? p.mass(x[e]) : 0.0;
-      if (q_row != nullptr) m = c < real ? fmax(m - q.mass(y[e]), 0.0) : 0.0;
-      if (c == point) m = fmax(m - 1.0, 0.0);
-      w[e] = m;
+      for (int e = 0; e < 8; ++e) m[e] = fmax(m[e] - n[e], 0.0);
+    }
+    if (point >= column && point < column + 8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (column + e == point) m[e] = fmax(m[e] - 1.0, 0.0);
+    }
+    if (column + 8 > real) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (column + e >= real) m[e] = 0.0;
     }
   }
 };
@@ -172,7 +280,7 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-// Greedy rows: a chunk's record is its maximum's order key (16 bits) over the
+// Greedy rows: a piece's record is its maximum's order key (16 bits) over the
 // complement of its column, so the largest record is the lowest column of the
 // largest value. -0 counts as 0.
 __device__ __forceinline__ u64 greedy_key(uint32_t b, int64_t column) {
@@ -181,50 +289,13 @@ __device__ __forceinline__ u64 greedy_key(uint32_t b, int64_t column) {
   return (static_cast<u64>(key) << 32) | static_cast<u64>(0xFFFFFFFFu - static_cast<uint32_t>(column));
 }
 
-__global__ __launch_bounds__(kThreads) void k_draft_sums(Args a, int64_t n_work) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int64_t work = static_cast<int64_t>(blockIdx.x) * (kThreads / kWave) + (threadIdx.x / kWave);
-  if (work >= n_work) return;
-  const int64_t s = work / a.n_chunks;
-  const int64_t chunk = work % a.n_chunks;
-  const Stop st = find_stop(a, s, lane);
-  if (!st.in_range || !st.served) return;
-  const Weights w(a, s, st);
-  const int64_t v0 = chunk * (kChunk / 8);
-  const bool greedy = a.t.temperature[st.first + s + st.k] == 0.0f;
-  if (greedy) {
-    u64 best = 0;
-    for (int u = 0; u < kChunkVecs; ++u) {
-      const int64_t v = v0 + u * kWave + lane;
-      if (v * 8 >= a.vocab_real) break;
-      const u32x4 x = w.p_row[v];
-      const uint32_t bits[4] = {x.x, x.y, x.z, x.w};
-      for (int e = 0; e < 8; ++e) {
-        const int64_t c = v * 8 + e;
-        const u64 key = greedy_key((bits[e >> 1] >> ((e & 1) * 16)) & 0xFFFFu, c);
-        if (c < a.vocab_real && key > best) best = key;
-      }
-    }
-    for (int d = kWave / 2; d >= 1; d >>= 1) {
-      const u64 o = __shfl_xor(best, d, kWave);
-      best = o > best ? o : best;
-    }
-    if (lane == 0) a.sums[s * a.n_chunks + chunk] = __builtin_bit_cast(double, best);
-    return;
-  }
-  double sum = 0.0;
+__device__ __forceinline__ u64 wave_top(u64 v) {
 #pragma unroll
-  for (int u = 0; u < kChunkVecs; ++u) {
-    const int64_t v = v0 + u * kWave + lane;
-    if (v * 8 < a.vocab_real) {
-      double m[8];
-      w.columns(v, a.vocab_real, m);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum = sum + m[e];
-    }
+  for (int d = kWave / 2; d >= 1; d >>= 1) {
+    const u64 o = __shfl_xor(v, d, kWave);
+    v = o > v ? o : v;
   }
-  sum = wave_sum(sum);
-  if (lane == 0) a.sums[s * a.n_chunks + chunk] = sum;
+  return v;
 }
 
 __device__ __forceinline__ double wave_scan(double v, int lane) {  // inclusive
@@ -236,97 +307,120 @@ __device__ __forceinline__ double wave_scan(double v, int lane) {  // inclusive
   return v;
 }
 
-__global__ __launch_bounds__(kWave) void k_draft_pick(Args a) {
-  const int lane = threadIdx.x;
-  const int64_t s = blockIdx.x;
-  const Stop st = find_stop(a, s, lane);
-  if (!st.in_range) {
-    if (lane == 0) a.accepted_out[s] = -1;
-    return;
+__device__ __forceinline__ u32x4 vector_at(const u32x4* row, int64_t v, int64_t vecs) {
+  return v < vecs ? __builtin_nontemporal_load(row + v) : rlk::neg_inf_vec();
+}
+
+// The sums of the pieces [from, to) of a row, one wave a piece, into sums[piece].
+template <bool kTable>
+__device__ __forceinline__ void sum_pieces(const Args& a, const Weights& w, bool greedy, const double* __restrict__ table,
+                                           int64_t from, int64_t to, int wave, int lane, double* __restrict__ sums) {
+  const int64_t vecs = (a.vocab_real + 7) / 8;
+  int64_t piece = from + wave;
+  if (piece >= to) return;
+  u32x4 x = vector_at(w.p_row, piece * kWave + lane, vecs);
+  u32x4 y = w.q_row != nullptr ? vector_at(w.q_row, piece * kWave + lane, vecs) : rlk::neg_inf_vec();
+  while (piece < to) {
+    // the next piece's vectors are on their way while this one's are weighed
+    const int64_t next = piece + kWaves;
+    const int64_t vn = next < to ? next * kWave + lane : vecs;
+    const u32x4 xn = vector_at(w.p_row, vn, vecs);
+    const u32x4 yn = w.q_row != nullptr ? vector_at(w.q_row, vn, vecs) : rlk::neg_inf_vec();
+    const int64_t column = (piece * kWave + lane) * 8;
+    if (greedy) {
+      u64 best = 0;
+      const uint32_t bits[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const u64 key = greedy_key((bits[e >> 1] >> ((e & 1) * 16)) & 0xFFFFu, column + e);
+        if (column + e < a.vocab_real && key > best) best = key;
+      }
+      best = wave_top(best);
+      if (lane == 0) sums[piece] = __builtin_bit_cast(double, best);
+    } else {
+      double m[8];
+      w.columns<kTable>(x, y, table, column, a.vocab_real, m);
+      double sum = 0.0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = sum + m[e];
+      sum = wave_sum(sum);
+      if (lane == 0) sums[piece] = sum;
+    }
+    x = xn;
+    y = yn;
+    piece = next;
   }
+}
+
+// Draws a token from the pieces' sums (one wave) and writes a sequence's outputs.
+__device__ __forceinline__ void draw_and_write(const Args& a, int64_t s, const Stop& st, const double* sums, int lane) {
   const int64_t base = st.first + s;
   const int64_t row = base + st.k;
   int64_t pick = -1;
   float policy = NAN, ref = NAN;
   if (st.served) {
     const float t = a.t.temperature[row];
-    const double* sums = a.sums + s * a.n_chunks;
-    const Weights w(a, s, st);
     if (t == 0.0f) {
       u64 best = 0;
-      for (int64_t c = lane; c < a.n_chunks; c += kWave) {
+      for (int64_t c = lane; c < a.n_pieces; c += kWave) {
         const u64 o = __builtin_bit_cast(u64, sums[c]);
         best = o > best ? o : best;
       }
-      for (int d = kWave / 2; d >= 1; d >>= 1) {
-        const u64 o = __shfl_xor(best, d, kWave);
-        best = o > best ? o : best;
-      }
+      best = wave_top(best);
       pick = static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(best));
       policy = 0.0f;
       ref = 0.0f;
     } else {
       double total = 0.0;
-      for (int64_t c0 = 0; c0 < a.n_chunks; c0 += kWave) {
-        const double v = c0 + lane < a.n_chunks ? sums[c0 + lane] : 0.0;
+      for (int64_t c0 = 0; c0 < a.n_pieces; c0 += kWave) {
+        const double v = c0 + lane < a.n_pieces ? sums[c0 + lane] : 0.0;
         total = total + __shfl(wave_scan(v, lane), kWave - 1, kWave);
       }
       if (total > 0.0 && total < INFINITY) {
         const double want = a.sample_u[s] * total;
-        // the first chunk whose running sum passes `want`; by rounding none may: then the last with any weight
+        // the first piece whose running sum passes `want`; by rounding none may: then the last with any weight
         double before = 0.0, at_before = 0.0;
-        int64_t chunk = -1;
-        for (int64_t c0 = 0; c0 < a.n_chunks; c0 += kWave) {
-          const double v = c0 + lane < a.n_chunks ? sums[c0 + lane] : 0.0;
+        int64_t piece = 0;
+        for (int64_t c0 = 0; c0 < a.n_pieces; c0 += kWave) {
+          const double v = c0 + lane < a.n_pieces ? sums[c0 + lane] : 0.0;
           const double incl = before + wave_scan(v, lane);
           const u64 over = __ballot(incl > want && v > 0.0);
           const u64 any = __ballot(v > 0.0);
           const int l = over != 0 ? __ffsll(over) - 1 : (any != 0 ? 63 - __clzll(any) : -1);
           if (l >= 0) {
-            chunk = c0 + l;
+            piece = c0 + l;
             at_before = __shfl(incl, l, kWave) - __shfl(v, l, kWave);
           }
           if (over != 0) break;
           before = __shfl(incl, kWave - 1, kWave);
         }
-        // the columns of that chunk, 512 at a time
-        double run = at_before;
-        int64_t last = -1;
-        bool found = false;
-        for (int u = 0; u < kChunkVecs && !found; ++u) {
-          const int64_t v = chunk * (kChunk / 8) + u * kWave + lane;
-          double m[8] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
-          if (v * 8 < a.vocab_real) w.columns(v, a.vocab_real, m);
-          double mine = 0.0;
+        // its columns: the first whose running sum passes, else the last with any weight
+        const Weights w(a, s, st);
+        const int64_t vecs = (a.vocab_real + 7) / 8, v = piece * kWave + lane;
+        const u32x4 x = v < vecs ? w.p_row[v] : rlk::neg_inf_vec();
+        const u32x4 y = w.q_row != nullptr && v < vecs ? w.q_row[v] : rlk::neg_inf_vec();
+        double m[8];
+        w.columns<false>(x, y, nullptr, v * 8, a.vocab_real, m);
+        double mine = 0.0;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) mine = mine + m[e];
-          const double incl = wave_scan(mine, lane);
-          double c = run + (incl - mine);
-          int hit = -1, tail = -1;
+        for (int e = 0; e < 8; ++e) mine = mine + m[e];
+        double c = at_before + (wave_scan(mine, lane) - mine);
+        int hit = -1, tail = -1;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            c = c + m[e];
-            if (m[e] > 0.0) {
-              tail = e;
-              if (hit < 0 && c > want) hit = e;
-            }
+        for (int e = 0; e < 8; ++e) {
+          c = c + m[e];
+          if (m[e] > 0.0) {
+            tail = e;
+            if (hit < 0 && c > want) hit = e;
           }
-          const u64 hits = __ballot(hit >= 0);
-          const u64 tails = __ballot(tail >= 0);
-          if (hits != 0) {
-            const int l = __ffsll(hits) - 1;
-            last = (chunk * (kChunk / 8) + u * kWave + l) * 8 + __shfl(hit, l, kWave);
-            found = true;
-          } else if (tails != 0) {
-            const int l = 63 - __clzll(tails);
-            last = (chunk * (kChunk / 8) + u * kWave + l) * 8 + __shfl(tail, l, kWave);
-          }
-          run = run + __shfl(incl, kWave - 1, kWave);
         }
-        pick = last;
-        if (pick >= 0) {
-          const float x = __uint_as_float(static_cast<uint32_t>(a.t.logits[row * a.t.row_stride + pick]) << 16);
-          const double z = static_cast<double>(w.p.scaled(x));
+        const u64 hits = __ballot(hit >= 0), tails = __ballot(tail >= 0);
+        const int l = hits != 0 ? __ffsll(hits) - 1 : (tails != 0 ? 63 - __clzll(tails) : -1);
+        if (l >= 0) {
+          const int e = __shfl(hits != 0 ? hit : tail, l, kWave);
+          pick = (piece * kWave + l) * 8 + e;
+          const float xt = __uint_as_float(static_cast<uint32_t>(a.t.logits[row * a.t.row_stride + pick]) << 16);
+          const double z = static_cast<double>(w.p.scaled(xt));
           policy = static_cast<float>(z - w.p.part);
           ref = static_cast<float>(z - static_cast<double>(a.t.lse[row]));
         }
@@ -347,6 +441,59 @@ __global__ __launch_bounds__(kWave) void k_draft_pick(Args a) {
   if (lane == 0) a.accepted_out[s] = static_cast<int32_t>(st.k);
 }
 
+// Many sequences: a workgroup for each, with tables. Fewer: about 512
+// workgroups in all (two a compute unit); tables from 4 pieces a wave on, which
+// cost it about as much as weighing 2 pieces of both sides.
+constexpr int64_t kWholeFrom = 192;
+constexpr int64_t kWholePieces = 512;   // piece sums that stay in LDS
+constexpr int64_t kWantGroups = 512;
+
+// The pieces' sums of a sequence, in `parts` workgroups; with kWhole (parts 1)
+// in LDS, and the rest of its work. kTable: weights by table.
+template <bool kTable, bool kWhole>
+__global__ __launch_bounds__(kThreads) void k_draft(Args a, int parts, int64_t pieces_each) {
+  __shared__ double table[kTable ? 2 * kSlots : 1];        // 72 KB: two workgroups a compute unit
+  __shared__ double piece_sums[kWhole ? kWholePieces : 1];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+  const int64_t s = blockIdx.x / static_cast<unsigned>(parts);
+  const int64_t part = blockIdx.x % static_cast<unsigned>(parts);
+  const Stop st = find_stop(a, s, lane);
+  double* sums = kWhole ? piece_sums : a.sums + s * a.n_pieces;
+  if (st.in_range && st.served) {  // uniform across the workgroup
+    const Weights w(a, s, st);
+    const bool greedy = a.t.temperature[st.first + s + st.k] == 0.0f;
+    if (kTable && !greedy) {
+      for (int i = threadIdx.x; i < kSlots; i += kThreads) {
+        const float x = __uint_as_float(slot_bits(i) << 16);
+        table[i] = w.p.mass(x);
+        if (w.q_row != nullptr) table[kSlots + i] = w.q.mass(x);
+      }
+      __syncthreads();
+    }
+    const int64_t from = part * pieces_each;
+    const int64_t to = from + pieces_each < a.n_pieces ? from + pieces_each : a.n_pieces;
+    sum_pieces<kTable>(a, w, greedy, table, from, to, wave, lane, sums);
+  }
+  if constexpr (kWhole) {
+    __syncthreads();
+    if (wave != 0) return;
+    if (st.in_range)
+      draw_and_write(a, s, st, sums, lane);
+    else if (lane == 0)
+      a.accepted_out[s] = -1;
+  }
+}
+
+__global__ __launch_bounds__(kWave) void k_draft_pick(Args a) {
+  const int64_t s = blockIdx.x;
+  const Stop st = find_stop(a, s, threadIdx.x);
+  if (st.in_range)
+    draw_and_write(a, s, st, a.sums + s * a.n_pieces, threadIdx.x);
+  else if (threadIdx.x == 0)
+    a.accepted_out[s] = -1;
+}
+
 static bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 static int32_t launched() { return hipGetLastError() == hipSuccess ? RLK_OK : RLK_ERR_HIP; }
@@ -361,7 +508,29 @@ static int32_t check_layout(const rlk_vocab_layout* L) {
   return RLK_OK;
 }
 
-static int64_t chunks(const rlk_vocab_layout* L) { return (L->vocab_real + kChunk - 1) / kChunk; }
+static int64_t pieces(const rlk_vocab_layout* L) { return (L->vocab_real + kPiece - 1) / kPiece; }
+
+static int32_t launch(const Args& a, hipStream_t stream) {
+  if (a.n_seq >= kWholeFrom && a.n_pieces <= kWholePieces) {
+    k_draft<true, true><<<dim3(static_cast<unsigned>(a.n_seq)), dim3(kThreads), 0, stream>>>(a, 1, a.n_pieces);
+    return launched();
+  }
+  int64_t parts = (kWantGroups + a.n_seq - 1) / a.n_seq;
+  const int64_t most = (a.n_pieces + kWaves - 1) / kWaves;
+  parts = parts < most ? parts : most;
+  const int64_t each = (a.n_pieces + parts - 1) / parts;
+  parts = (a.n_pieces + each - 1) / each;
+  if (a.n_seq * parts > INT32_MAX) return RLK_ERR_SHAPE;
+  const dim3 grid(static_cast<unsigned>(a.n_seq * parts)), block(kThreads);
+  if (each >= 4 * kWaves)
+    k_draft<true, false><<<grid, block, 0, stream>>>(a, static_cast<int>(parts), each);
+  else
+    k_draft<false, false><<<grid, block, 0, stream>>>(a, static_cast<int>(parts), each);
+  const int32_t st = launched();
+  if (st != RLK_OK) return st;
+  k_draft_pick<<<dim3(static_cast<unsigned>(a.n_seq)), dim3(kWave), 0, stream>>>(a);
+  return launched();
+}
 
 static int32_t check_rows(const rlk_scored_rows* r, int64_t need, const rlk_vocab_layout* L) {
   if (r->n_rows < need || r->n_rows > 2 * kMaxRows) return RLK_ERR_SHAPE;
@@ -377,7 +546,7 @@ extern "C" {
 size_t rlk_draft_workspace_bytes(int64_t n_seq, const rlk_vocab_layout* layout) {
   using namespace rlk_draft;
   if (check_layout(layout) != RLK_OK || n_seq < 0 || n_seq > kMaxRows) return 0;
-  return static_cast<size_t>(n_seq) * static_cast<size_t>(chunks(layout)) * sizeof(double);
+  return static_cast<size_t>(n_seq) * static_cast<size_t>(pieces(layout)) * sizeof(double);
 }
 
 int32_t rlk_draft_verify(const rlk_scored_rows* target, const rlk_scored_rows* draft,
@@ -416,7 +585,7 @@ int32_t rlk_draft_verify(const rlk_scored_rows* target, const rlk_scored_rows* d
   a.n_seq = n_seq;
   a.n_draft = n_draft;
   a.vocab_real = layout->vocab_real;
-  a.n_chunks = chunks(layout);
+  a.n_pieces = pieces(layout);
   a.start = draft_start;
   a.token = draft_token;
   a.accept_u = accept_u;
@@ -426,13 +595,7 @@ int32_t rlk_draft_verify(const rlk_scored_rows* target, const rlk_scored_rows* d
   a.policy_out = policy_out;
   a.ref_out = ref_out;
   a.sums = static_cast<double*>(workspace);
-  const int64_t n_work = n_seq * a.n_chunks;
-  const int64_t blocks = (n_work + kThreads / kWave - 1) / (kThreads / kWave);
-  if (blocks > INT32_MAX) return RLK_ERR_SHAPE;
-  k_draft_sums<<<dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream>>>(a, n_work);
-  if ((st = launched()) != RLK_OK) return st;
-  k_draft_pick<<<dim3(static_cast<unsigned>(n_seq)), dim3(kWave), 0, stream>>>(a);
-  return launched();
+  return launch(a, stream);
 }
 
 }  // extern "C"

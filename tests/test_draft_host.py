@@ -117,7 +117,7 @@ class Call:
     (dict(t_n_rows=(1 << 23) + 1), SHAPE), (dict(t_row_stride=1 << 61), SHAPE),
     (dict(n_seq=-1), SHAPE), (dict(n_draft=-1), SHAPE), (dict(n_seq=(1 << 22) + 1, t_n_rows=1 << 23), SHAPE),
     (dict(layout=VocabLayout(1000, 1000, 1024, 8, 1)), SHAPE), (dict(layout=VocabLayout(1024, 0, 1024, 8, 1)), SHAPE),
-    (dict(layout=VocabLayout(1024, 1000, 1024, 8, 5)), GROUPS), (dict(wsb=3 * 8 - 1), WS),
+    (dict(layout=VocabLayout(1024, 1000, 1024, 8, 5)), GROUPS), (dict(wsb=3 * 2 * 8 - 1), WS),
 ])
 def test_verify_refuses(kw, code):
     assert Call(**kw)() == code
@@ -129,9 +129,9 @@ def test_no_sequences_enqueue_nothing():
 
 
 def test_workspace_size():
-    assert rlk.draft_workspace_bytes(3, 1024, 1000) == 3 * 8
-    assert rlk.draft_workspace_bytes(7, 152576, 151936) == 7 * 75 * 8
-    assert rlk.draft_workspace_bytes(7, 4096, 2048) == 7 * 8 and rlk.draft_workspace_bytes(7, 4096, 2049) == 7 * 16
+    assert rlk.draft_workspace_bytes(3, 1024, 1000) == 3 * 2 * 8
+    assert rlk.draft_workspace_bytes(7, 152576, 151936) == 7 * 297 * 8
+    assert rlk.draft_workspace_bytes(7, 4096, 512) == 7 * 8 and rlk.draft_workspace_bytes(7, 4096, 513) == 7 * 16
     assert rlk.draft_workspace_bytes(-1, 1024, 1000) == 0 and rlk.draft_workspace_bytes(3, 1000, 1000) == 0
 
 
