@@ -29,8 +29,9 @@ using rlk::u32x4;
 typedef unsigned long long u64;
 
 constexpr int kPiece = kWave * 8;   // 512 columns: one 16-byte vector a lane
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;        // of a workgroup for a part of a sequence
 constexpr int kWaves = kThreads / kWave;
+constexpr int kWholeThreads = 1024;  // and for a whole one
 constexpr int64_t kMaxRows = int64_t(1) << 22;
 constexpr int64_t kMaxVocab = int64_t(1) << 30;
 
@@ -52,59 +53,82 @@ struct Args {
   double* sums;           // [n_seq][n_pieces]
 };
 
-// Where a sequence's accepted tokens end (uniform across the wave).
+// Where a sequence's accepted tokens end, and what is known of the rows there
+// (uniform across the wave).
 struct Stop {
   int64_t first;   // draft_start[s]
   int64_t count;   // drafted tokens
   int64_t k;       // accepted tokens
+  int64_t token;   // the drafted token at k (k < count)
   bool in_range;   // draft_start is usable
   bool served;     // a token can be drawn at row k
+  bool sampled;    // q has logits there (else, with k < count, a point mass)
+  float t, lse, part, threshold;         // the target's row
+  float logp;                            // its policy logprob of the drafted token
+  float t_q, part_q, threshold_q;        // the draft's (sampled)
 };
 
 __device__ __forceinline__ bool unit(double u) { return u >= 0.0 && u < 1.0; }
 
+// One lane a place, the row behind the last drafted token included, so that all
+// a wave needs comes in two rounds of loads (the offsets, the rest).
 __device__ __forceinline__ Stop find_stop(const Args& a, int64_t s, int lane) {
-  Stop r;
+  Stop r = {};
   r.first = a.start[s];
   const int64_t end = a.start[s + 1];
   r.count = end - r.first;
-  r.k = 0;
   r.in_range = r.first >= 0 && r.first <= end && end <= a.n_draft;
-  r.served = false;
   if (!r.in_range) return r;
-  bool bad = false;
-  r.k = r.count;
-  for (int64_t k0 = 0; k0 < r.count; k0 += kWave) {
-    const int64_t k = k0 + lane;
-    bool stays = true, wrong = false;
+  const bool fair = unit(a.sample_u[s]);
+  const bool drafter = a.d.logits != nullptr;
+  for (int64_t k0 = 0; k0 <= r.count; k0 += kWave) {
+    const int64_t k = k0 + lane < r.count ? k0 + lane : r.count;
+    const int64_t i = r.first + k, row = i + s;
+    const rlk_support_state st = a.t.support[row];
+    const float t = a.t.temperature[row], lse = a.t.lse[row];
+    rlk_support_state sq = {};
+    float t_q = 0.0f, lp = 0.0f, lq = 0.0f;
+    int64_t tok = 0;
+    double u = 0.0;
     if (k < r.count) {
-      const int64_t i = r.first + k;
-      const int64_t row = i + s;
-      const int64_t tok = a.token[i];
-      const double u = a.accept_u[i];
-      const float lp = a.t.policy_logp[row];
-      float lq = 0.0f;
-      wrong = a.t.support[row].status < 0 || lp != lp || tok < 0 || tok >= a.vocab_real || !unit(u);
-      if (a.d.logits != nullptr && a.d.temperature[i] != 0.0f) {
+      tok = a.token[i];
+      u = a.accept_u[i];
+      lp = a.t.policy_logp[row];
+      if (drafter) {
+        t_q = a.d.temperature[i];
         lq = a.d.policy_logp[i];
-        wrong |= a.d.support[i].status < 0 || lq != lq;
+        sq = a.d.support[i];
       }
+    }
+    const bool sampled = k < r.count && drafter && t_q != 0.0f;
+    if (!sampled) lq = 0.0f;
+    bool wrong = st.status < 0, stays = false;
+    if (k < r.count) {
+      wrong |= lp != lp || tok < 0 || tok >= a.vocab_real || !unit(u) || (sampled && (sq.status < 0 || lq != lq));
       // a drafted token of no policy mass is never accepted (also where the drafter gave it none)
       stays = !wrong && lp > -INFINITY && u < exp(static_cast<double>(lp) - static_cast<double>(lq));
     }
     const u64 stops = __ballot(!stays);
-    if (stops != 0) {
-      const int l = __ffsll(stops) - 1;
-      r.k = k0 + l;
-      bad = (__ballot(wrong) >> l) & 1;
-      break;
-    }
+    if (stops == 0) continue;
+    const int l = __builtin_amdgcn_readfirstlane(__ffsll(stops) - 1);
+    const bool served = !wrong && fair && rlk::temperature_valid(t) && (t == 0.0f || st.lse_support == st.lse_support);
+    r.k = k0 + l;
+    r.token = __shfl(tok, l, kWave);
+    r.served = (__ballot(served) >> l) & 1;
+    r.sampled = (__ballot(sampled) >> l) & 1;
+    const auto from = [l](float v) {
+      return __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(v)), l)));
+    };
+    r.t = from(t);
+    r.lse = from(lse);
+    r.part = from(st.lse_support);
+    r.threshold = from(st.threshold);
+    r.logp = from(lp);
+    r.t_q = from(t_q);
+    r.part_q = from(sq.lse_support);
+    r.threshold_q = from(sq.threshold);
+    break;
   }
-  const int64_t row = r.first + s + r.k;
-  const float t = a.t.temperature[row];
-  const float part = a.t.support[row].lse_support;
-  r.served = !bad && a.t.support[row].status >= 0 && rlk::temperature_valid(t) && (t == 0.0f || part == part) &&
-             unit(a.sample_u[s]);
   return r;
 }
 
@@ -139,8 +163,8 @@ struct Policy {
   float threshold;
 
   __device__ __forceinline__ Policy() : inv_t(0.0), part(0.0), threshold(INFINITY) {}
-  __device__ __forceinline__ Policy(float t, const rlk_support_state& st)
-      : inv_t(1.0 / static_cast<double>(t)), part(static_cast<double>(st.lse_support)), threshold(st.threshold) {}
+  __device__ __forceinline__ Policy(float t, float lse_support, float thr)
+      : inv_t(1.0 / static_cast<double>(t)), part(static_cast<double>(lse_support)), threshold(thr) {}
 
   // fl32(x / T): the float64 product with 1/T is within 2^-52 of the quotient.
   // x has 8 significant bits and T 24, so a quotient that is no midpoint of two
@@ -226,22 +250,12 @@ struct Weights {
   Policy q;
   int64_t point;         // column of q's point mass, -1: none
 
-  __device__ __forceinline__ Weights(const Args& a, int64_t s, const Stop& st) {
-    const int64_t row = st.first + s + st.k;
-    p_row = reinterpret_cast<const u32x4*>(a.t.logits + row * a.t.row_stride);
-    p = Policy(a.t.temperature[row], a.t.support[row]);
-    q_row = nullptr;
-    point = -1;
-    if (st.k < st.count) {
-      const int64_t i = st.first + st.k;
-      if (a.d.logits != nullptr && a.d.temperature[i] != 0.0f) {
-        q_row = reinterpret_cast<const u32x4*>(a.d.logits + i * a.d.row_stride);
-        q = Policy(a.d.temperature[i], a.d.support[i]);
-      } else {
-        point = a.token[i];
-      }
-    }
-  }
+  __device__ __forceinline__ Weights(const Args& a, int64_t s, const Stop& st)
+      : p_row(reinterpret_cast<const u32x4*>(a.t.logits + (st.first + s + st.k) * a.t.row_stride)),
+        q_row(st.sampled ? reinterpret_cast<const u32x4*>(a.d.logits + (st.first + st.k) * a.d.row_stride) : nullptr),
+        p(st.t, st.part, st.threshold),
+        q(st.t_q, st.part_q, st.threshold_q),
+        point(st.k < st.count && !st.sampled ? st.token : -1) {}
 
   // Weights of the 8 columns from `column` on (those from `real` on weigh
   // nothing), given both sides' vectors and, with kTable, tables.
@@ -274,17 +288,44 @@ struct Weights {
   }
 };
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = kWave / 2; d >= 1; d >>= 1) v = v + __shfl_xor(v, d, kWave);
+// Inclusive sums over the lanes, and the whole sum, on lane moves of the vector
+// units (shuffles through LDS took most of a piece's time): within rows of 16
+// lanes by 1, 2, 4 and 8, then row 0's total into row 1 and 2's into 3, then
+// the lower half's into the upper.
+template <int Ctrl, int RowMask>
+__device__ __forceinline__ double moved(double v) {  // 0 where no lane is
+  const u64 u = __builtin_bit_cast(u64, v);
+  const uint32_t lo = static_cast<uint32_t>(
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(static_cast<uint32_t>(u)), Ctrl, RowMask, 0xF, true));
+  const uint32_t hi = static_cast<uint32_t>(
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(static_cast<uint32_t>(u >> 32)), Ctrl, RowMask, 0xF, true));
+  return __builtin_bit_cast(double, (static_cast<u64>(hi) << 32) | lo);
+}
+
+__device__ __forceinline__ double wave_scan(double v) {
+  v = v + moved<0x111, 0xF>(v);
+  v = v + moved<0x112, 0xF>(v);
+  v = v + moved<0x114, 0xF>(v);
+  v = v + moved<0x118, 0xF>(v);
+  v = v + moved<0x142, 0xA>(v);
+  v = v + moved<0x143, 0xC>(v);
   return v;
 }
 
-// Greedy rows: a piece's record is its maximum's order key (16 bits) over the
+__device__ __forceinline__ double lane_value(double v, int l) {  // l uniform
+  const u64 u = __builtin_bit_cast(u64, v);
+  const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(u)), l));
+  const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(u >> 32)), l));
+  return __builtin_bit_cast(double, (static_cast<u64>(hi) << 32) | lo);
+}
+
+__device__ __forceinline__ double wave_sum(double v) { return lane_value(wave_scan(v), kWave - 1); }
+
+// Greedy rows: a wave's record is its maximum's order key (16 bits) over the
 // complement of its column, so the largest record is the lowest column of the
 // largest value. -0 counts as 0.
-__device__ __forceinline__ u64 greedy_key(uint32_t b, int64_t column) {
-  b = b == 0x8000u ? 0u : b;
+__device__ __forceinline__ u64 greedy_key(float x, int64_t column) {
+  const uint32_t b = x == 0.0f ? 0u : __float_as_uint(x) >> 16;
   const uint32_t key = (b & 0x8000u) ? (~b & 0xFFFFu) : (b | 0x8000u);
   return (static_cast<u64>(key) << 32) | static_cast<u64>(0xFFFFFFFFu - static_cast<uint32_t>(column));
 }
@@ -298,58 +339,81 @@ __device__ __forceinline__ u64 wave_top(u64 v) {
   return v;
 }
 
-__device__ __forceinline__ double wave_scan(double v, int lane) {  // inclusive
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const double o = __shfl_up(v, d, kWave);
-    if (lane >= d) v = v + o;
-  }
-  return v;
-}
-
 __device__ __forceinline__ u32x4 vector_at(const u32x4* row, int64_t v, int64_t vecs) {
   return v < vecs ? __builtin_nontemporal_load(row + v) : rlk::neg_inf_vec();
 }
 
-// The sums of the pieces [from, to) of a row, one wave a piece, into sums[piece].
-template <bool kTable>
-__device__ __forceinline__ void sum_pieces(const Args& a, const Weights& w, bool greedy, const double* __restrict__ table,
-                                           int64_t from, int64_t to, int wave, int lane, double* __restrict__ sums) {
-  const int64_t vecs = (a.vocab_real + 7) / 8;
-  int64_t piece = from + wave;
-  if (piece >= to) return;
-  u32x4 x = vector_at(w.p_row, piece * kWave + lane, vecs);
-  u32x4 y = w.q_row != nullptr ? vector_at(w.q_row, piece * kWave + lane, vecs) : rlk::neg_inf_vec();
-  while (piece < to) {
-    // the next piece's vectors are on their way while this one's are weighed
-    const int64_t next = piece + kWaves;
-    const int64_t vn = next < to ? next * kWave + lane : vecs;
-    const u32x4 xn = vector_at(w.p_row, vn, vecs);
-    const u32x4 yn = w.q_row != nullptr ? vector_at(w.q_row, vn, vecs) : rlk::neg_inf_vec();
-    const int64_t column = (piece * kWave + lane) * 8;
-    if (greedy) {
-      u64 best = 0;
-      const uint32_t bits[4] = {x.x, x.y, x.z, x.w};
+constexpr int kBatch = 2;  // pieces that a wave weighs together
+
+struct Vectors {
+  u32x4 x[kBatch];
+  u32x4 y[kBatch];
+
+  __device__ __forceinline__ void load(const Weights& w, int64_t piece, int64_t stride, int64_t to, int64_t vecs, int lane) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const u64 key = greedy_key((bits[e >> 1] >> ((e & 1) * 16)) & 0xFFFFu, column + e);
-        if (column + e < a.vocab_real && key > best) best = key;
-      }
-      best = wave_top(best);
-      if (lane == 0) sums[piece] = __builtin_bit_cast(double, best);
-    } else {
-      double m[8];
-      w.columns<kTable>(x, y, table, column, a.vocab_real, m);
-      double sum = 0.0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum = sum + m[e];
-      sum = wave_sum(sum);
-      if (lane == 0) sums[piece] = sum;
+    for (int b = 0; b < kBatch; ++b) {
+      const int64_t at = piece + b * stride;
+      const int64_t v = at < to ? at * kWave + lane : vecs;
+      x[b] = vector_at(w.p_row, v, vecs);
+      y[b] = w.q_row != nullptr ? vector_at(w.q_row, v, vecs) : rlk::neg_inf_vec();
     }
-    x = xn;
-    y = yn;
-    piece = next;
   }
+};
+
+// The sums of the pieces [from, to) of a row, one wave a piece, into sums[piece].
+// `waves` waves share them; the next pieces' vectors are on their way while a
+// wave weighs its pieces (`now` holds the first ones).
+template <bool kTable>
+__device__ __forceinline__ void sum_pieces(const Args& a, const Weights& w, const double* __restrict__ table, int64_t from,
+                                           int64_t to, int wave, int waves, int lane, Vectors now, double* __restrict__ sums) {
+  const int64_t vecs = (a.vocab_real + 7) / 8;
+  for (int64_t piece = from + wave; piece < to; piece += kBatch * waves) {
+    Vectors next;
+    next.load(w, piece + kBatch * waves, waves, to, vecs, lane);
+    double sum[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      double m[8];
+      w.columns<kTable>(now.x[b], now.y[b], table, ((piece + b * waves) * kWave + lane) * 8, a.vocab_real, m);
+      sum[b] = 0.0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[b] = sum[b] + m[e];
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      sum[b] = wave_sum(sum[b]);
+      if (lane == 0 && piece + b * waves < to) sums[piece + b * waves] = sum[b];
+    }
+    now = next;
+  }
+}
+
+// A greedy row's pieces: the wave's record in its first piece's place, 0 in the others'.
+__device__ __forceinline__ void top_pieces(const Args& a, const Weights& w, int64_t from, int64_t to, int wave, int waves,
+                                           int lane, Vectors now, double* __restrict__ sums) {
+  const int64_t vecs = (a.vocab_real + 7) / 8;
+  float top = -INFINITY;
+  int64_t column = -1;
+  for (int64_t piece = from + wave; piece < to; piece += kBatch * waves) {
+    Vectors next;
+    next.load(w, piece + kBatch * waves, waves, to, vecs, lane);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int64_t at = ((piece + b * waves) * kWave + lane) * 8;
+      float x[8];
+      rlk::unpack8(now.x[b], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (at + e < a.vocab_real && (column < 0 || x[e] > top)) {  // columns rise: the first of equal values stays
+          top = x[e];
+          column = at + e;
+        }
+      if (lane == 0 && piece + b * waves < to) sums[piece + b * waves] = 0.0;
+    }
+    now = next;
+  }
+  const u64 best = wave_top(column < 0 ? 0 : greedy_key(top, column));
+  if (lane == 0 && from + wave < to) sums[from + wave] = __builtin_bit_cast(double, best);
 }
 
 // Draws a token from the pieces' sums (one wave) and writes a sequence's outputs.
@@ -359,8 +423,7 @@ __device__ __forceinline__ void draw_and_write(const Args& a, int64_t s, const S
   int64_t pick = -1;
   float policy = NAN, ref = NAN;
   if (st.served) {
-    const float t = a.t.temperature[row];
-    if (t == 0.0f) {
+    if (st.t == 0.0f) {
       u64 best = 0;
       for (int64_t c = lane; c < a.n_pieces; c += kWave) {
         const u64 o = __builtin_bit_cast(u64, sums[c]);
@@ -374,7 +437,7 @@ __device__ __forceinline__ void draw_and_write(const Args& a, int64_t s, const S
       double total = 0.0;
       for (int64_t c0 = 0; c0 < a.n_pieces; c0 += kWave) {
         const double v = c0 + lane < a.n_pieces ? sums[c0 + lane] : 0.0;
-        total = total + __shfl(wave_scan(v, lane), kWave - 1, kWave);
+        total = total + wave_sum(v);
       }
       if (total > 0.0 && total < INFINITY) {
         const double want = a.sample_u[s] * total;
@@ -383,16 +446,16 @@ __device__ __forceinline__ void draw_and_write(const Args& a, int64_t s, const S
         int64_t piece = 0;
         for (int64_t c0 = 0; c0 < a.n_pieces; c0 += kWave) {
           const double v = c0 + lane < a.n_pieces ? sums[c0 + lane] : 0.0;
-          const double incl = before + wave_scan(v, lane);
+          const double incl = before + wave_scan(v);
           const u64 over = __ballot(incl > want && v > 0.0);
           const u64 any = __ballot(v > 0.0);
-          const int l = over != 0 ? __ffsll(over) - 1 : (any != 0 ? 63 - __clzll(any) : -1);
+          const int l = __builtin_amdgcn_readfirstlane(over != 0 ? __ffsll(over) - 1 : (any != 0 ? 63 - __clzll(any) : -1));
           if (l >= 0) {
             piece = c0 + l;
-            at_before = __shfl(incl, l, kWave) - __shfl(v, l, kWave);
+            at_before = lane_value(incl, l) - lane_value(v, l);
           }
           if (over != 0) break;
-          before = __shfl(incl, kWave - 1, kWave);
+          before = lane_value(incl, kWave - 1);
         }
         // its columns: the first whose running sum passes, else the last with any weight
         const Weights w(a, s, st);
@@ -404,7 +467,7 @@ __device__ __forceinline__ void draw_and_write(const Args& a, int64_t s, const S
         double mine = 0.0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) mine = mine + m[e];
-        double c = at_before + (wave_scan(mine, lane) - mine);
+        double c = at_before + (wave_scan(mine) - mine);
         int hit = -1, tail = -1;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -417,17 +480,20 @@ __device__ __forceinline__ void draw_and_write(const Args& a, int64_t s, const S
         const u64 hits = __ballot(hit >= 0), tails = __ballot(tail >= 0);
         const int l = hits != 0 ? __ffsll(hits) - 1 : (tails != 0 ? 63 - __clzll(tails) : -1);
         if (l >= 0) {
-          const int e = __shfl(hits != 0 ? hit : tail, l, kWave);
-          pick = (piece * kWave + l) * 8 + e;
-          const float xt = __uint_as_float(static_cast<uint32_t>(a.t.logits[row * a.t.row_stride + pick]) << 16);
-          const double z = static_cast<double>(w.p.scaled(xt));
+          const int mine_e = hits != 0 ? hit : tail;
+          float x8[8], xt = 0.0f;
+          rlk::unpack8(x, x8);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) xt = e == mine_e ? x8[e] : xt;
+          pick = (piece * kWave + l) * 8 + __shfl(mine_e, l, kWave);
+          const double z = static_cast<double>(w.p.scaled(__shfl(xt, l, kWave)));
           policy = static_cast<float>(z - w.p.part);
-          ref = static_cast<float>(z - static_cast<double>(a.t.lse[row]));
+          ref = static_cast<float>(z - static_cast<double>(st.lse));
         }
-      } else if (total == 0.0 && st.k < st.count && a.t.policy_logp[row] > -INFINITY) {
+      } else if (total == 0.0 && st.k < st.count && st.logp > -INFINITY) {
         // p is nowhere above q: the drafted token
-        pick = a.token[st.first + st.k];
-        policy = a.t.policy_logp[row];
+        pick = st.token;
+        policy = st.logp;
         ref = a.t.ref_logp[row];
       }
     }
@@ -451,7 +517,8 @@ constexpr int64_t kWantGroups = 512;
 // The pieces' sums of a sequence, in `parts` workgroups; with kWhole (parts 1)
 // in LDS, and the rest of its work. kTable: weights by table.
 template <bool kTable, bool kWhole>
-__global__ __launch_bounds__(kThreads) void k_draft(Args a, int parts, int64_t pieces_each) {
+__global__ __launch_bounds__(kWhole ? kWholeThreads : kThreads) void k_draft(Args a, int parts, int64_t pieces_each) {
+  constexpr int kN = kWhole ? kWholeThreads : kThreads;
   __shared__ double table[kTable ? 2 * kSlots : 1];        // 72 KB: two workgroups a compute unit
   __shared__ double piece_sums[kWhole ? kWholePieces : 1];
   const int lane = threadIdx.x & (kWave - 1);
@@ -462,18 +529,23 @@ __global__ __launch_bounds__(kThreads) void k_draft(Args a, int parts, int64_t p
   double* sums = kWhole ? piece_sums : a.sums + s * a.n_pieces;
   if (st.in_range && st.served) {  // uniform across the workgroup
     const Weights w(a, s, st);
-    const bool greedy = a.t.temperature[st.first + s + st.k] == 0.0f;
-    if (kTable && !greedy) {
-      for (int i = threadIdx.x; i < kSlots; i += kThreads) {
-        const float x = __uint_as_float(slot_bits(i) << 16);
-        table[i] = w.p.mass(x);
-        if (w.q_row != nullptr) table[kSlots + i] = w.q.mass(x);
-      }
-      __syncthreads();
-    }
     const int64_t from = part * pieces_each;
     const int64_t to = from + pieces_each < a.n_pieces ? from + pieces_each : a.n_pieces;
-    sum_pieces<kTable>(a, w, greedy, table, from, to, wave, lane, sums);
+    Vectors now;
+    now.load(w, from + wave, kN / kWave, to, (a.vocab_real + 7) / 8, lane);
+    if (st.t == 0.0f) {
+      top_pieces(a, w, from, to, wave, kN / kWave, lane, now, sums);
+    } else {
+      if (kTable) {
+        for (int i = threadIdx.x; i < kSlots; i += kN) {
+          const float x = __uint_as_float(slot_bits(i) << 16);
+          table[i] = w.p.mass(x);
+          if (w.q_row != nullptr) table[kSlots + i] = w.q.mass(x);
+        }
+        __syncthreads();
+      }
+      sum_pieces<kTable>(a, w, table, from, to, wave, kN / kWave, lane, now, sums);
+    }
   }
   if constexpr (kWhole) {
     __syncthreads();
@@ -512,7 +584,7 @@ static int64_t pieces(const rlk_vocab_layout* L) { return (L->vocab_real + kPiec
 
 static int32_t launch(const Args& a, hipStream_t stream) {
   if (a.n_seq >= kWholeFrom && a.n_pieces <= kWholePieces) {
-    k_draft<true, true><<<dim3(static_cast<unsigned>(a.n_seq)), dim3(kThreads), 0, stream>>>(a, 1, a.n_pieces);
+    k_draft<true, true><<<dim3(static_cast<unsigned>(a.n_seq)), dim3(kWholeThreads), 0, stream>>>(a, 1, a.n_pieces);
     return launched();
   }
   int64_t parts = (kWantGroups + a.n_seq - 1) / a.n_seq;
