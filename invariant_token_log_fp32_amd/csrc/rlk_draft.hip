@@ -29,9 +29,6 @@ using rlk::u32x4;
 typedef unsigned long long u64;
 
 constexpr int kPiece = kWave * 8;   // 512 columns: one 16-byte vector a lane
-constexpr int kThreads = 512;        // of a workgroup for a part of a sequence
-constexpr int kWaves = kThreads / kWave;
-constexpr int kWholeThreads = 1024;  // and for a whole one
 constexpr int64_t kMaxRows = int64_t(1) << 22;
 constexpr int64_t kMaxVocab = int64_t(1) << 30;
 
@@ -41,7 +38,7 @@ struct Args {
   int64_t n_seq;
   int64_t n_draft;
   int64_t vocab_real;
-  int64_t n_pieces;
+  int n_pieces;
   const int64_t* start;
   const int64_t* token;
   const double* accept_u;
@@ -133,12 +130,16 @@ __device__ __forceinline__ Stop find_stop(const Args& a, int64_t s, int lane) {
 }
 
 // e^y for y up to about 1, to a few 2^-53 of the value: y = n ln 2 + r with ln 2
-// in two parts, the series of e^r to r^12 (|r| <= ln(2) / 2 leaves 2e-16). -inf
-// and anything below -1000 gives 0.
+// in two parts, the series of e^r to r^12 (|r| <= ln(2) / 2 leaves 2e-16). n is
+// rounded by an addition of 1.5 * 2^52, whose low word then holds it, and 2^n
+// is added to the exponent (conversions and ldexp run at a quarter of the rate).
+// Where the result nears the subnormal range (and for -inf) ldexp takes over.
 __device__ __forceinline__ double exp_down(double y) {
-  y = fmax(y, -1000.0);
-  const double n = rint(y * 1.4426950408889634074);
-  double r = fma(-n, 6.93147180369123816490e-01, y);
+  constexpr double kRound = 6755399441055744.0;
+  const double c = fmax(y, -1000.0);
+  const double t = fma(c, 1.4426950408889634074, kRound);
+  const double n = t - kRound;
+  double r = fma(-n, 6.93147180369123816490e-01, c);
   r = fma(-n, 1.90821492927058770002e-10, r);
   double p = 2.08767569878680989792e-09;  // 1 / 12!
   p = fma(p, r, 2.50521083854417187751e-08);
@@ -153,7 +154,9 @@ __device__ __forceinline__ double exp_down(double y) {
   p = fma(p, r, 0.5);
   p = fma(p, r, 1.0);
   p = fma(p, r, 1.0);
-  return ldexp(p, static_cast<int>(n));
+  const int e = static_cast<int>(static_cast<uint32_t>(__builtin_bit_cast(u64, t)));
+  if (!(y > -700.0 && y < 700.0)) return ldexp(p, e);  // also NaN and +inf, whose sums are refused
+  return __builtin_bit_cast(double, __builtin_bit_cast(u64, p) + (static_cast<u64>(static_cast<uint32_t>(e)) << 52));
 }
 
 // One side's policy over the columns of a row.
@@ -257,11 +260,11 @@ struct Weights {
         q(st.t_q, st.part_q, st.threshold_q),
         point(st.k < st.count && !st.sampled ? st.token : -1) {}
 
-  // Weights of the 8 columns from `column` on (those from `real` on weigh
-  // nothing), given both sides' vectors and, with kTable, tables.
+  // Weights of a lane's 8 columns of a piece, given both sides' vectors and, with
+  // kTable, tables. Columns from `real` on weigh nothing.
   template <bool kTable>
-  __device__ __forceinline__ void columns(const u32x4& x, const u32x4& y, const double* __restrict__ table, int64_t column,
-                                          int64_t real, double (&m)[8]) const {
+  __device__ __forceinline__ void columns(const u32x4& x, const u32x4& y, const double* __restrict__ table, int piece,
+                                          int lane, int64_t real, double (&m)[8]) const {
     if constexpr (kTable)
       look_up(table, p, x, m);
     else
@@ -275,15 +278,16 @@ struct Weights {
 #pragma unroll
       for (int e = 0; e < 8; ++e) m[e] = fmax(m[e] - n[e], 0.0);
     }
-    if (point >= column && point < column + 8) {
+    const int64_t first = static_cast<int64_t>(piece) * kPiece;  // uniform, as both conditions are
+    if (point >= first && point < first + kPiece) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (column + e == point) m[e] = fmax(m[e] - 1.0, 0.0);
+        if (first + lane * 8 + e == point) m[e] = fmax(m[e] - 1.0, 0.0);
     }
-    if (column + 8 > real) {
+    if (first + kPiece > real) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (column + e >= real) m[e] = 0.0;
+        if (first + lane * 8 + e >= real) m[e] = 0.0;
     }
   }
 };
@@ -339,23 +343,23 @@ __device__ __forceinline__ u64 wave_top(u64 v) {
   return v;
 }
 
-__device__ __forceinline__ u32x4 vector_at(const u32x4* row, int64_t v, int64_t vecs) {
-  return v < vecs ? __builtin_nontemporal_load(row + v) : rlk::neg_inf_vec();
+// A lane's vector of a piece; behind the row's last vector (or the last piece
+// asked for) -inf, which weighs nothing.
+__device__ __forceinline__ u32x4 vector_at(const u32x4* row, int piece, int to, int vecs, int lane) {
+  const int v = piece * kWave + lane;
+  return piece < to && v < vecs ? __builtin_nontemporal_load(row + v) : rlk::neg_inf_vec();
 }
 
-constexpr int kBatch = 2;  // pieces that a wave weighs together
-
-struct Vectors {
+template <int kBatch>
+struct Vectors {   // of the pieces that a wave weighs together
   u32x4 x[kBatch];
   u32x4 y[kBatch];
 
-  __device__ __forceinline__ void load(const Weights& w, int64_t piece, int64_t stride, int64_t to, int64_t vecs, int lane) {
+  __device__ __forceinline__ void load(const Weights& w, int piece, int stride, int to, int vecs, int lane) {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int64_t at = piece + b * stride;
-      const int64_t v = at < to ? at * kWave + lane : vecs;
-      x[b] = vector_at(w.p_row, v, vecs);
-      y[b] = w.q_row != nullptr ? vector_at(w.q_row, v, vecs) : rlk::neg_inf_vec();
+      x[b] = vector_at(w.p_row, piece + b * stride, to, vecs, lane);
+      if (w.q_row != nullptr) y[b] = vector_at(w.q_row, piece + b * stride, to, vecs, lane);
     }
   }
 };
@@ -363,18 +367,19 @@ struct Vectors {
 // The sums of the pieces [from, to) of a row, one wave a piece, into sums[piece].
 // `waves` waves share them; the next pieces' vectors are on their way while a
 // wave weighs its pieces (`now` holds the first ones).
-template <bool kTable>
-__device__ __forceinline__ void sum_pieces(const Args& a, const Weights& w, const double* __restrict__ table, int64_t from,
-                                           int64_t to, int wave, int waves, int lane, Vectors now, double* __restrict__ sums) {
-  const int64_t vecs = (a.vocab_real + 7) / 8;
-  for (int64_t piece = from + wave; piece < to; piece += kBatch * waves) {
-    Vectors next;
+template <bool kTable, int kBatch>
+__device__ __forceinline__ void sum_pieces(const Args& a, const Weights& w, const double* __restrict__ table, int from,
+                                           int to, int wave, int waves, int lane, Vectors<kBatch> now,
+                                           double* __restrict__ sums) {
+  const int vecs = static_cast<int>((a.vocab_real + 7) / 8);
+  for (int piece = from + wave; piece < to; piece += kBatch * waves) {
+    Vectors<kBatch> next;
     next.load(w, piece + kBatch * waves, waves, to, vecs, lane);
     double sum[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       double m[8];
-      w.columns<kTable>(now.x[b], now.y[b], table, ((piece + b * waves) * kWave + lane) * 8, a.vocab_real, m);
+      w.columns<kTable>(now.x[b], now.y[b], table, piece + b * waves, lane, a.vocab_real, m);
       sum[b] = 0.0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[b] = sum[b] + m[e];
@@ -389,17 +394,18 @@ __device__ __forceinline__ void sum_pieces(const Args& a, const Weights& w, cons
 }
 
 // A greedy row's pieces: the wave's record in its first piece's place, 0 in the others'.
-__device__ __forceinline__ void top_pieces(const Args& a, const Weights& w, int64_t from, int64_t to, int wave, int waves,
-                                           int lane, Vectors now, double* __restrict__ sums) {
-  const int64_t vecs = (a.vocab_real + 7) / 8;
+template <int kBatch>
+__device__ __forceinline__ void top_pieces(const Args& a, const Weights& w, int from, int to, int wave, int waves, int lane,
+                                           Vectors<kBatch> now, double* __restrict__ sums) {
+  const int vecs = static_cast<int>((a.vocab_real + 7) / 8);
   float top = -INFINITY;
   int64_t column = -1;
-  for (int64_t piece = from + wave; piece < to; piece += kBatch * waves) {
-    Vectors next;
+  for (int piece = from + wave; piece < to; piece += kBatch * waves) {
+    Vectors<kBatch> next;
     next.load(w, piece + kBatch * waves, waves, to, vecs, lane);
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int64_t at = ((piece + b * waves) * kWave + lane) * 8;
+      const int64_t at = (static_cast<int64_t>(piece + b * waves) * kWave + lane) * 8;
       float x[8];
       rlk::unpack8(now.x[b], x);
 #pragma unroll
@@ -416,8 +422,39 @@ __device__ __forceinline__ void top_pieces(const Args& a, const Weights& w, int6
   if (lane == 0 && from + wave < to) sums[from + wave] = __builtin_bit_cast(double, best);
 }
 
+// Piece sums of a sequence, 64 a register, for a wave that draws from them: all
+// loads at once, before anything else is known. Longer rows read them in place.
+constexpr int kHeld = 8;
+
+struct Sums {
+  const double* at;
+  int n;
+  bool held;
+  double v[kHeld];
+
+  __device__ __forceinline__ Sums(const double* sums, int n_pieces, int lane)
+      : at(sums), n(n_pieces), held(n_pieces <= kHeld * kWave) {
+    if (!held) return;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) v[i] = i * kWave + lane < n ? at[i * kWave + lane] : 0.0;
+  }
+
+  // f(register or load, first piece) over the 64-piece groups until it returns true
+  template <typename F>
+  __device__ __forceinline__ void each(int lane, F f) const {
+    if (held) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (i * kWave < n && f(v[i], i * kWave)) return;
+    } else {
+      for (int c0 = 0; c0 < n; c0 += kWave)
+        if (f(c0 + lane < n ? at[c0 + lane] : 0.0, c0)) return;
+    }
+  }
+};
+
 // Draws a token from the pieces' sums (one wave) and writes a sequence's outputs.
-__device__ __forceinline__ void draw_and_write(const Args& a, int64_t s, const Stop& st, const double* sums, int lane) {
+__device__ __forceinline__ void draw_and_write(const Args& a, int64_t s, const Stop& st, const Sums& sums, int lane) {
   const int64_t base = st.first + s;
   const int64_t row = base + st.k;
   int64_t pick = -1;
@@ -425,27 +462,27 @@ __device__ __forceinline__ void draw_and_write(const Args& a, int64_t s, const S
   if (st.served) {
     if (st.t == 0.0f) {
       u64 best = 0;
-      for (int64_t c = lane; c < a.n_pieces; c += kWave) {
-        const u64 o = __builtin_bit_cast(u64, sums[c]);
+      sums.each(lane, [&](double v, int) {
+        const u64 o = __builtin_bit_cast(u64, v);
         best = o > best ? o : best;
-      }
+        return false;
+      });
       best = wave_top(best);
       pick = static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(best));
       policy = 0.0f;
       ref = 0.0f;
     } else {
       double total = 0.0;
-      for (int64_t c0 = 0; c0 < a.n_pieces; c0 += kWave) {
-        const double v = c0 + lane < a.n_pieces ? sums[c0 + lane] : 0.0;
+      sums.each(lane, [&](double v, int) {
         total = total + wave_sum(v);
-      }
+        return false;
+      });
       if (total > 0.0 && total < INFINITY) {
         const double want = a.sample_u[s] * total;
         // the first piece whose running sum passes `want`; by rounding none may: then the last with any weight
         double before = 0.0, at_before = 0.0;
-        int64_t piece = 0;
-        for (int64_t c0 = 0; c0 < a.n_pieces; c0 += kWave) {
-          const double v = c0 + lane < a.n_pieces ? sums[c0 + lane] : 0.0;
+        int piece = 0;
+        sums.each(lane, [&](double v, int c0) {
           const double incl = before + wave_scan(v);
           const u64 over = __ballot(incl > want && v > 0.0);
           const u64 any = __ballot(v > 0.0);
@@ -454,16 +491,16 @@ __device__ __forceinline__ void draw_and_write(const Args& a, int64_t s, const S
             piece = c0 + l;
             at_before = lane_value(incl, l) - lane_value(v, l);
           }
-          if (over != 0) break;
           before = lane_value(incl, kWave - 1);
-        }
+          return over != 0;
+        });
         // its columns: the first whose running sum passes, else the last with any weight
         const Weights w(a, s, st);
-        const int64_t vecs = (a.vocab_real + 7) / 8, v = piece * kWave + lane;
+        const int vecs = static_cast<int>((a.vocab_real + 7) / 8), v = piece * kWave + lane;
         const u32x4 x = v < vecs ? w.p_row[v] : rlk::neg_inf_vec();
         const u32x4 y = w.q_row != nullptr && v < vecs ? w.q_row[v] : rlk::neg_inf_vec();
         double m[8];
-        w.columns<false>(x, y, nullptr, v * 8, a.vocab_real, m);
+        w.columns<false>(x, y, nullptr, piece, lane, a.vocab_real, m);
         double mine = 0.0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) mine = mine + m[e];
@@ -485,7 +522,7 @@ __device__ __forceinline__ void draw_and_write(const Args& a, int64_t s, const S
           rlk::unpack8(x, x8);
 #pragma unroll
           for (int e = 0; e < 8; ++e) xt = e == mine_e ? x8[e] : xt;
-          pick = (piece * kWave + l) * 8 + __shfl(mine_e, l, kWave);
+          pick = (static_cast<int64_t>(piece) * kWave + l) * 8 + __shfl(mine_e, l, kWave);
           const double z = static_cast<double>(w.p.scaled(__shfl(xt, l, kWave)));
           policy = static_cast<float>(z - w.p.part);
           ref = static_cast<float>(z - static_cast<double>(st.lse));
@@ -507,34 +544,28 @@ __device__ __forceinline__ void draw_and_write(const Args& a, int64_t s, const S
   if (lane == 0) a.accepted_out[s] = static_cast<int32_t>(st.k);
 }
 
-// Many sequences: a workgroup for each, with tables. Fewer: about 512
-// workgroups in all (two a compute unit); tables from 4 pieces a wave on, which
-// cost it about as much as weighing 2 pieces of both sides.
-constexpr int64_t kWholeFrom = 192;
-constexpr int64_t kWholePieces = 512;   // piece sums that stay in LDS
-constexpr int64_t kWantGroups = 512;
+constexpr int kWholePieces = 512;   // piece sums that stay in LDS
 
 // The pieces' sums of a sequence, in `parts` workgroups; with kWhole (parts 1)
 // in LDS, and the rest of its work. kTable: weights by table.
-template <bool kTable, bool kWhole>
-__global__ __launch_bounds__(kWhole ? kWholeThreads : kThreads) void k_draft(Args a, int parts, int64_t pieces_each) {
-  constexpr int kN = kWhole ? kWholeThreads : kThreads;
+template <bool kTable, bool kWhole, int kN, int kBatch, int kWavesEach>
+__global__ __launch_bounds__(kN, kWavesEach) void k_draft(Args a, int parts, int pieces_each) {
   __shared__ double table[kTable ? 2 * kSlots : 1];        // 72 KB: two workgroups a compute unit
   __shared__ double piece_sums[kWhole ? kWholePieces : 1];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int64_t s = blockIdx.x / static_cast<unsigned>(parts);
-  const int64_t part = blockIdx.x % static_cast<unsigned>(parts);
+  const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(parts));
   const Stop st = find_stop(a, s, lane);
   double* sums = kWhole ? piece_sums : a.sums + s * a.n_pieces;
   if (st.in_range && st.served) {  // uniform across the workgroup
     const Weights w(a, s, st);
-    const int64_t from = part * pieces_each;
-    const int64_t to = from + pieces_each < a.n_pieces ? from + pieces_each : a.n_pieces;
-    Vectors now;
-    now.load(w, from + wave, kN / kWave, to, (a.vocab_real + 7) / 8, lane);
+    const int from = part * pieces_each;
+    const int to = from + pieces_each < a.n_pieces ? from + pieces_each : a.n_pieces;
+    Vectors<kBatch> now;
+    now.load(w, from + wave, kN / kWave, to, static_cast<int>((a.vocab_real + 7) / 8), lane);
     if (st.t == 0.0f) {
-      top_pieces(a, w, from, to, wave, kN / kWave, lane, now, sums);
+      top_pieces<kBatch>(a, w, from, to, wave, kN / kWave, lane, now, sums);
     } else {
       if (kTable) {
         for (int i = threadIdx.x; i < kSlots; i += kN) {
@@ -544,14 +575,14 @@ __global__ __launch_bounds__(kWhole ? kWholeThreads : kThreads) void k_draft(Arg
         }
         __syncthreads();
       }
-      sum_pieces<kTable>(a, w, table, from, to, wave, kN / kWave, lane, now, sums);
+      sum_pieces<kTable, kBatch>(a, w, table, from, to, wave, kN / kWave, lane, now, sums);
     }
   }
   if constexpr (kWhole) {
     __syncthreads();
     if (wave != 0) return;
     if (st.in_range)
-      draw_and_write(a, s, st, sums, lane);
+      draw_and_write(a, s, st, Sums(sums, a.n_pieces, lane), lane);
     else if (lane == 0)
       a.accepted_out[s] = -1;
   }
@@ -559,9 +590,10 @@ __global__ __launch_bounds__(kWhole ? kWholeThreads : kThreads) void k_draft(Arg
 
 __global__ __launch_bounds__(kWave) void k_draft_pick(Args a) {
   const int64_t s = blockIdx.x;
+  const Sums sums(a.sums + s * a.n_pieces, a.n_pieces, threadIdx.x);
   const Stop st = find_stop(a, s, threadIdx.x);
   if (st.in_range)
-    draw_and_write(a, s, st, a.sums + s * a.n_pieces, threadIdx.x);
+    draw_and_write(a, s, st, sums, threadIdx.x);
   else if (threadIdx.x == 0)
     a.accepted_out[s] = -1;
 }
@@ -582,22 +614,35 @@ static int32_t check_layout(const rlk_vocab_layout* L) {
 
 static int64_t pieces(const rlk_vocab_layout* L) { return (L->vocab_real + kPiece - 1) / kPiece; }
 
+// A table costs a wave of 16 about as much as weighing half a piece of both
+// sides column by column, so it pays from one piece a wave on. From 129
+// sequences on there is a compute unit for at most one each: the sequence is
+// drawn from where it was summed (no second launch). Above 256, two workgroups
+// of half the threads share a compute unit, so that one weighs while the other
+// waits for its first rows or draws (1024 x 3: 117 us, with one of 1024 threads 126).
 static int32_t launch(const Args& a, hipStream_t stream) {
-  if (a.n_seq >= kWholeFrom && a.n_pieces <= kWholePieces) {
-    k_draft<true, true><<<dim3(static_cast<unsigned>(a.n_seq)), dim3(kWholeThreads), 0, stream>>>(a, 1, a.n_pieces);
+  constexpr int kUnits = 256;
+  if (a.n_seq > kUnits / 2 && a.n_pieces <= kWholePieces) {
+    const dim3 grid(static_cast<unsigned>(a.n_seq));
+    if (a.n_seq <= kUnits)
+      k_draft<true, true, 1024, 2, 4><<<grid, dim3(1024), 0, stream>>>(a, 1, a.n_pieces);
+    else
+      k_draft<true, true, 512, 2, 4><<<grid, dim3(512), 0, stream>>>(a, 1, a.n_pieces);
     return launched();
   }
-  int64_t parts = (kWantGroups + a.n_seq - 1) / a.n_seq;
-  const int64_t most = (a.n_pieces + kWaves - 1) / kWaves;
-  parts = parts < most ? parts : most;
-  const int64_t each = (a.n_pieces + parts - 1) / parts;
+  const bool table = a.n_seq * a.n_pieces >= kUnits * 16;
+  const int64_t wanted = table ? kUnits : 2 * kUnits;             // workgroups: one of 1024 or two of 512 threads
+  const int64_t least = table ? 16 : 8;                           // pieces each: one a wave
+  int64_t parts = wanted / a.n_seq > 1 ? wanted / a.n_seq : 1;
+  int64_t each = (a.n_pieces + parts - 1) / parts;
+  each = each > least ? each : least;
   parts = (a.n_pieces + each - 1) / each;
   if (a.n_seq * parts > INT32_MAX) return RLK_ERR_SHAPE;
-  const dim3 grid(static_cast<unsigned>(a.n_seq * parts)), block(kThreads);
-  if (each >= 4 * kWaves)
-    k_draft<true, false><<<grid, block, 0, stream>>>(a, static_cast<int>(parts), each);
+  const dim3 grid(static_cast<unsigned>(a.n_seq * parts));
+  if (table)
+    k_draft<true, false, 1024, 2, 4><<<grid, dim3(1024), 0, stream>>>(a, static_cast<int>(parts), static_cast<int>(each));
   else
-    k_draft<false, false><<<grid, block, 0, stream>>>(a, static_cast<int>(parts), each);
+    k_draft<false, false, 512, 1, 4><<<grid, dim3(512), 0, stream>>>(a, static_cast<int>(parts), static_cast<int>(each));
   const int32_t st = launched();
   if (st != RLK_OK) return st;
   k_draft_pick<<<dim3(static_cast<unsigned>(a.n_seq)), dim3(kWave), 0, stream>>>(a);
@@ -657,7 +702,7 @@ int32_t rlk_draft_verify(const rlk_scored_rows* target, const rlk_scored_rows* d
   a.n_seq = n_seq;
   a.n_draft = n_draft;
   a.vocab_real = layout->vocab_real;
-  a.n_pieces = pieces(layout);
+  a.n_pieces = static_cast<int>(pieces(layout));  // at most 2^21
   a.start = draft_start;
   a.token = draft_token;
   a.accept_u = accept_u;
