@@ -10,8 +10,8 @@ Build the library first with ``python -m invariant_token_log_fp32_amd.build``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 import re
 from typing import Optional, Tuple, Union
@@ -657,12 +657,47 @@ def linear_logp_merge(summaries, temperature, target, *, n_rows: int, groups: in
 # microscaled 4-bit quantisation and LM-head linear (include/rlk_mx4.h)
 # ---------------------------------------------------------------------------
 
-def _on_device(device):
-    """The context a launch needs: the tensors' device made current, when it is not."""
+def _on_stream(fn):
+    """With ``stream=`` the whole call runs in that stream's context: what it
+    allocates and fills belongs to the stream, in order with its kernels."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with _torch().cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _run(name, device, *args):
+    """Calls an entry point on the device's current stream, with that device current."""
     torch = _torch()
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    handle = torch._C._cuda_getCurrentRawStream(device.index)
+    fn = getattr(load_library(), name)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, handle)
+    if st != RLK_OK:
+        raise RlkError(st, name)
+
+
+@functools.lru_cache(maxsize=256)
+def _layout_ref(vocab_padded, vocab_real, row_stride):
+    """A rlk_vocab_layout of one group and its reference (never written to)."""
+    lay = make_layout(vocab_padded, vocab_real, row_stride)
+    return lay, ctypes.byref(lay)
+
+
+@functools.lru_cache(maxsize=1024)
+def _draft_need(n_seq, vocab_padded, vocab_real):
+    return draft_workspace_bytes(n_seq, vocab_padded, vocab_real)
+
+
+@functools.lru_cache(maxsize=1024)
+def _mx4_need(n_rows, d):
+    return mx4_bytes(n_rows, d)
 
 
 def _bytes_tensor(value, need, device, name):
@@ -681,7 +716,8 @@ def mx4_bytes(n_rows: int, d: int) -> Tuple[int, int]:
     return int(lib.rlk_mx4_codes_bytes(int(n_rows), int(d))), int(lib.rlk_mx4_scales_bytes(int(n_rows), int(d)))
 
 
-def mx4_quantize(x, *, codes=None, scales=None, values_out=None, return_values: bool = False, stream=None):
+@_on_stream
+def mx4_quantize(x, *, codes=None, scales=None, values_out=None, return_values: bool = False):
     """Microscaled 4-bit form of the rows of ``x`` (rlk_mx4_quantize): blocks of
     32 BF16 values that share a power of two, in the layout that mx4_linear
     reads. ``x`` is a [n_rows, d] device tensor of BF16 bits, d a multiple of
@@ -692,8 +728,7 @@ def mx4_quantize(x, *, codes=None, scales=None, values_out=None, return_values: 
     ldx = _bf16_matrix(x, "x")
     n, d = x.shape
     dev = x.device
-    lib = load_library()
-    need_c, need_s = int(lib.rlk_mx4_codes_bytes(n, d)), int(lib.rlk_mx4_scales_bytes(n, d))
+    need_c, need_s = _mx4_need(n, d)
     codes = _bytes_tensor(codes, need_c, dev, "codes")
     scales = _bytes_tensor(scales, need_s, dev, "scales")
     if return_values and values_out is None:
@@ -703,12 +738,8 @@ def mx4_quantize(x, *, codes=None, scales=None, values_out=None, return_values: 
         ldv = _bf16_matrix(values_out, "values_out")
         if values_out.device != dev or tuple(values_out.shape) != (n, d):
             raise ValueError(f"values_out must hold {n} rows of {d} BF16 values on {dev}")
-    with _on_device(dev):
-        st = lib.rlk_mx4_quantize(x.data_ptr(), n, d, ldx, codes.data_ptr(), codes.numel(), scales.data_ptr(),
-                                  scales.numel(), values_out.data_ptr() if values_out is not None else None, ldv,
-                                  _stream_handle(stream, dev))
-    if st != RLK_OK:
-        raise RlkError(st, "rlk_mx4_quantize")
+    _run("rlk_mx4_quantize", dev, x.data_ptr(), n, d, ldx, codes.data_ptr(), codes.numel(), scales.data_ptr(),
+         scales.numel(), values_out.data_ptr() if values_out is not None else None, ldv)
     return (codes, scales, values_out) if return_values else (codes, scales)
 
 
@@ -716,8 +747,8 @@ def mx4_linear_workspace_bytes(n_rows: int, d_model: int) -> int:
     return int(load_library().rlk_mx4_linear_workspace_bytes(int(n_rows), int(d_model)))
 
 
-def mx4_linear(hidden, weight_codes, weight_scales, *, vocab_real: int, vocab_padded: int, out=None, workspace=None,
-               stream=None):
+@_on_stream
+def mx4_linear(hidden, weight_codes, weight_scales, *, vocab_real: int, vocab_padded: int, out=None, workspace=None):
     """BF16 logits [n_rows, vocab_padded] of the LM head with both operands in 4
     bits, pads -inf (rlk_mx4_linear). ``hidden`` is BF16 [n_rows, d_model],
     quantised by the call; ``weight_codes`` and ``weight_scales`` come from
@@ -726,9 +757,8 @@ def mx4_linear(hidden, weight_codes, weight_scales, *, vocab_real: int, vocab_pa
     ldh = _bf16_matrix(hidden, "hidden")
     n, d = hidden.shape
     dev = hidden.device
-    lib = load_library()
-    for value, need, name in ((weight_codes, int(lib.rlk_mx4_codes_bytes(int(vocab_real), d)), "weight_codes"),
-                              (weight_scales, int(lib.rlk_mx4_scales_bytes(int(vocab_real), d)), "weight_scales")):
+    need_c, need_s = _mx4_need(int(vocab_real), d)
+    for value, need, name in ((weight_codes, need_c, "weight_codes"), (weight_scales, need_s, "weight_scales")):
         if value is None:
             raise ValueError(f"{name} is missing")
         _bytes_tensor(value, need, dev, name)
@@ -738,16 +768,10 @@ def mx4_linear(hidden, weight_codes, weight_scales, *, vocab_real: int, vocab_pa
     if out.device != dev or out.shape[0] != n or out.shape[1] < vocab_padded or (ldo % 8) != 0:
         raise ValueError(f"out must hold {n} rows of at least {vocab_padded} BF16 columns, row stride a multiple "
                          f"of 8, on {dev}")
-    lay = make_layout(vocab_padded, vocab_real, ldo)
-    need = int(lib.rlk_mx4_linear_workspace_bytes(n, d))
-    workspace, ws_bytes = _workspace(workspace, need, dev)
-    with _on_device(dev):
-        st = lib.rlk_mx4_linear(hidden.data_ptr(), n, d, ldh, weight_codes.data_ptr(), weight_scales.data_ptr(),
-                                ctypes.byref(lay), out.data_ptr(),
-                                workspace.data_ptr() if workspace is not None else None, ws_bytes,
-                                _stream_handle(stream, dev))
-    if st != RLK_OK:
-        raise RlkError(st, "rlk_mx4_linear")
+    workspace, ws_bytes = _workspace(workspace, sum(_mx4_need(n, d)), dev)
+    _run("rlk_mx4_linear", dev, hidden.data_ptr(), n, d, ldh, weight_codes.data_ptr(), weight_scales.data_ptr(),
+         _layout_ref(vocab_padded, vocab_real, ldo)[1], out.data_ptr(),
+         workspace.data_ptr() if workspace is not None else None, ws_bytes)
     return out
 
 
@@ -763,16 +787,17 @@ def draft_workspace_bytes(n_seq: int, vocab_padded: int, vocab_real: int) -> int
 def _given(value, shape, dtype, device, name):
     """A required input tensor, checked."""
     torch = _torch()
-    if not isinstance(value, torch.Tensor) or value.dtype != dtype or value.device != device or \
-            tuple(value.shape) != tuple(shape) or not value.is_contiguous():
+    if not isinstance(value, torch.Tensor) or value.dtype is not dtype or value.shape != shape or \
+            value.device != device or not value.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return value
 
 
+@_on_stream
 def draft_verify(logits, draft_token, draft_start, accept_u, sample_u, *, temperature, policy_logp, ref_logp, lse,
                  support_state, vocab_real: int, vocab_padded: Optional[int] = None, draft_logits=None,
                  draft_temperature=None, draft_policy_logp=None, draft_support_state=None, token_out=None,
-                 accepted_out=None, policy_out=None, ref_out=None, workspace=None, stream=None):
+                 accepted_out=None, policy_out=None, ref_out=None, workspace=None):
     """Accept or refuse drafted tokens and draw one more per sequence (rlk_draft_verify).
 
     ``logits`` are the target's rows, sequence after sequence, K + 1 for a
@@ -830,20 +855,13 @@ def draft_verify(logits, draft_token, draft_start, accept_u, sample_u, *, temper
         policy_out = torch.zeros(n, dtype=torch.float32, device=dev)
     if ref_out is None:
         ref_out = torch.zeros(n, dtype=torch.float32, device=dev)
-    _out(token_out, (n,), torch.int64, dev, "token_out")
-    _out(accepted_out, (n_seq,), torch.int32, dev, "accepted_out")
-    _out(policy_out, (n,), torch.float32, dev, "policy_out")
-    _out(ref_out, (n,), torch.float32, dev, "ref_out")
-    lay = make_layout(vp, vocab_real, vp)
-    lib = load_library()
-    need = int(lib.rlk_draft_workspace_bytes(n_seq, ctypes.byref(lay)))
-    workspace, ws_bytes = _workspace(workspace, need, dev)
-    with _on_device(dev):
-        st = lib.rlk_draft_verify(
-            ctypes.byref(target), ctypes.byref(draft) if draft is not None else None, ctypes.byref(lay), n_seq,
-            n_draft, draft_start.data_ptr(), draft_token.data_ptr(), accept_u.data_ptr(), sample_u.data_ptr(),
-            token_out.data_ptr(), accepted_out.data_ptr(), policy_out.data_ptr(), ref_out.data_ptr(),
-            workspace.data_ptr() if workspace is not None else None, ws_bytes, _stream_handle(stream, dev))
-    if st != RLK_OK:
-        raise RlkError(st, "rlk_draft_verify")
+    _given(token_out, (n,), torch.int64, dev, "token_out")
+    _given(accepted_out, (n_seq,), torch.int32, dev, "accepted_out")
+    _given(policy_out, (n,), torch.float32, dev, "policy_out")
+    _given(ref_out, (n,), torch.float32, dev, "ref_out")
+    workspace, ws_bytes = _workspace(workspace, _draft_need(n_seq, vp, vocab_real), dev)
+    _run("rlk_draft_verify", dev, ctypes.byref(target), ctypes.byref(draft) if draft is not None else None,
+         _layout_ref(vp, vocab_real, vp)[1], n_seq, n_draft, draft_start.data_ptr(), draft_token.data_ptr(),
+         accept_u.data_ptr(), sample_u.data_ptr(), token_out.data_ptr(), accepted_out.data_ptr(), policy_out.data_ptr(),
+         ref_out.data_ptr(), workspace.data_ptr() if workspace is not None else None, ws_bytes)
     return token_out, accepted_out, policy_out, ref_out

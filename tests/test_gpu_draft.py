@@ -328,6 +328,28 @@ def test_a_sequence_does_not_depend_on_the_batch():
             assert to_host(g).tobytes() == w[at].tobytes(), (lo, hi)
 
 
+def test_calls_on_two_streams_at_once():
+    """The same call on two side streams that are not waited for, with outputs
+    and workspaces of its own making, many times: as on the main stream."""
+    import torch
+    say("case: two streams at once")
+    b = Batch(np.random.default_rng(13), [3] * 50, 20000, 20032, (0.7, 1.0, 0.0), 0.97, -1, "sampled").score()
+    want = [w.tobytes() for w in b.check()]
+    pol, ref, lse, state = b.stats
+    args = (b.lg, dev(b.token), dev(b.start), dev(b.accept_u), dev(b.sample_u))
+    kw = dict(temperature=dev(b.t), policy_logp=pol, ref_logp=ref, lse=lse, support_state=state, vocab_real=b.vr,
+              vocab_padded=b.vp, draft_logits=b.qlg, draft_temperature=dev(b.tq), draft_policy_logp=b.qstats[0],
+              draft_support_state=b.qstats[3])
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [rlk.draft_verify(*args, **kw, stream=sides[i % 2]) for i in range(20)]
+    noise = [torch.full((len(b.t),), 9.0, device="cuda:0") for _ in range(40)]   # memory that the side streams' may not be
+    torch.cuda.synchronize()
+    for g in got:
+        assert [to_host(t).tobytes() for t in g] == want
+    assert all((t == 9.0).all() for t in noise)
+
+
 def test_graph_replays_with_other_lengths():
     """Two captured calls, each with a workspace of its own, replayed with new
     offsets, tokens and numbers, eager calls and poisoned outputs between."""
