@@ -268,17 +268,23 @@ __global__ __launch_bounds__(kRowsThreads) void k_mx4_rows(Geo g, int64_t col_ti
 // product, up to 128 rows: the projection streamed past the hidden states
 // ---------------------------------------------------------------------------
 
-// Few rows are bound by reading the projection once. A workgroup of 4 waves
-// splits d in 4 and keeps its hidden states in registers for good (wave w the
-// fragments of its quarter); packed tiles of 32 vocabulary rows stream through:
-// wave 0 multiplies the first quarter of a tile and hands the accumulators to
-// wave 1 in LDS while it begins the next tile, and so on, so every logit's sum
-// still runs in increasing k. A fragment's registers take the next tile's as
-// soon as it is multiplied, so loads are always on their way.
-constexpr int kStreamWaves = 4;
-constexpr int kStreamThreads = kStreamWaves * 64;
-constexpr int kStreamBlocks = 4;   // blocks of 32 hidden rows, at most
-constexpr int kStreamGroups = 4;   // groups of 256 values of d a wave, at most (d <= 4096): the registers' limit
+// Few rows are bound by reading the projection once. The waves of a workgroup
+// split d and keep their parts of the hidden states in registers for good;
+// packed tiles of 32 vocabulary rows stream through: wave 0 multiplies its part
+// of a tile and hands the accumulators to wave 1 in LDS while it begins the next
+// tile, and so on, so every logit's sum still runs in increasing k. A fragment's
+// registers take a later tile's as soon as it is multiplied, so loads are always
+// on their way.
+constexpr int kStreamBlocks = 4;    // blocks of 32 hidden rows, at most
+constexpr int kStreamSteps4 = 16;   // groups of 256 values of d, at most (d <= 4096): the registers' limit
+
+// Waves of a workgroup, workgroups of a compute unit and tiles that a wave's
+// registers hold ahead, by blocks of rows (NB) and groups a wave (GP): what the
+// 512 registers that the waves of a SIMD share allow, with 8 waves a compute
+// unit for one and two blocks (48 rows: 70 us, with 4 waves 78 us).
+constexpr int stream_waves(int nb) { return nb == 2 ? 8 : 4; }
+constexpr int stream_groups(int nb) { return nb == 1 ? 2 : 1; }
+constexpr int stream_depth(int nb, int gp) { return (nb == 1 || nb == 4) && gp == 4 ? 1 : 2; }
 
 // One lane's block of 32 values (64 bytes of BF16), quantised as k_mx4_quantize does.
 __device__ __forceinline__ Frag4 quantize32(const u32x4 (&v)[4], uint32_t& byte) {
@@ -299,12 +305,6 @@ __device__ __forceinline__ void stream_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// Tiles that a wave's registers hold ahead, and workgroups of a compute unit:
-// two tiles or two workgroups (136 KB on their way in a compute unit) where the
-// registers allow, else one of each (NB = 4 with d above 2048).
-constexpr int stream_depth(int nb, int gp) { return gp == 4 && (nb == 1 || nb == 4) ? 1 : 2; }
-constexpr int stream_groups(int nb) { return nb == 1 ? 2 : 1; }
-
 template <int GP>
 struct StreamPart {     // a wave's part of a tile of the projection
   Frag4 f[GP * kSteps];
@@ -312,9 +312,10 @@ struct StreamPart {     // a wave's part of a tile of the projection
 };
 
 template <int NB, int GP>
-__global__ __launch_bounds__(kStreamThreads, stream_groups(NB)) void k_mx4_stream(
+__global__ __launch_bounds__(stream_waves(NB) * 64, stream_waves(NB) * stream_groups(NB) / 4) void k_mx4_stream(
     Geo g, const uint16_t* __restrict__ hidden, int64_t ldh, int d, int tiles, int w_tiles, uint16_t* __restrict__ out) {
   constexpr int kDepth = stream_depth(NB, GP);
+  constexpr int kStreamWaves = stream_waves(NB);
   __shared__ f32x4 slots[kStreamWaves - 1][NB][4][64];
   const int lane = threadIdx.x & 63;
   const int w = wave_id();
@@ -893,13 +894,13 @@ static void launch_stream_blocks(const Geo& g, const uint16_t* hidden, int64_t l
   const int tiles = static_cast<int>(g.vocab_padded / kTileRows);  // at most 2^25
   const int w_tiles = static_cast<int>(row_tiles(g.vocab_real));
   const int most = 256 * stream_groups(NB);
-  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most)), block(kStreamThreads);
-  const int per = (g.steps4 + kStreamWaves - 1) / kStreamWaves;
+  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most)), block(stream_waves(NB) * 64);
+  const int per = (g.steps4 + stream_waves(NB) - 1) / stream_waves(NB);
   if (per <= 1)
     k_mx4_stream<NB, 1><<<grid, block, 0, stream>>>(g, hidden, ldh, d, tiles, w_tiles, out);
   else if (per <= 2)
     k_mx4_stream<NB, 2><<<grid, block, 0, stream>>>(g, hidden, ldh, d, tiles, w_tiles, out);
-  else
+  else if constexpr (stream_waves(NB) == 4)
     k_mx4_stream<NB, 4><<<grid, block, 0, stream>>>(g, hidden, ldh, d, tiles, w_tiles, out);
 }
 
@@ -991,7 +992,7 @@ int32_t rlk_mx4_linear(const uint16_t* hidden, int64_t n_rows, int64_t d_model, 
   g.ldo = layout->row_stride;
   g.steps4 = static_cast<int>(scale_steps(d_model));
   const int blocks_of_rows = static_cast<int>(row_tiles(n_rows) < 8 ? row_tiles(n_rows) : 8);
-  const bool streamed = blocks_of_rows <= kStreamBlocks && g.steps4 <= kStreamWaves * kStreamGroups;
+  const bool streamed = blocks_of_rows <= kStreamBlocks && g.steps4 <= kStreamSteps4;
   if (!(streamed && blocks_of_rows == 1) &&
       (st = launch_quantize(hidden, n_rows, d_model, hidden_stride, hc, hs, nullptr, 0, stream)) != RLK_OK)
     return st;
