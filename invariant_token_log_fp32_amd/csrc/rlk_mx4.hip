@@ -268,22 +268,25 @@ __global__ __launch_bounds__(kRowsThreads) void k_mx4_rows(Geo g, int64_t col_ti
 // product, up to 128 rows: the projection streamed past the hidden states
 // ---------------------------------------------------------------------------
 
-// Few rows are bound by reading the projection once. The waves of a workgroup
-// split d and keep their parts of the hidden states in registers for good;
-// packed tiles of 32 vocabulary rows stream through: wave 0 multiplies its part
-// of a tile and hands the accumulators to wave 1 in LDS while it begins the next
-// tile, and so on, so every logit's sum still runs in increasing k. A fragment's
-// registers take a later tile's as soon as it is multiplied, so loads are always
-// on their way.
+// Few rows are bound by reading the projection once. SP waves (1, 2, 4 or 8: as
+// few as hold it) split d and keep their parts of the hidden states in registers
+// for good; packed tiles of 32 vocabulary rows stream through: the first wave
+// multiplies its part of a tile and hands the accumulators to the second in LDS
+// while it begins the next tile, and so on, so every logit's sum still runs in
+// increasing k. A fragment's registers take a later tile's as soon as it is
+// multiplied, so loads are always on their way. (With d always in four parts a
+// short d spends its time on turns: 77 x 1056 x 50021 21.7 us.)
 constexpr int kStreamBlocks = 4;    // blocks of 32 hidden rows, at most
 constexpr int kStreamSteps4 = 16;   // groups of 256 values of d, at most (d <= 4096): the registers' limit
 
-// Waves of a workgroup, workgroups of a compute unit and tiles that a wave's
-// registers hold ahead, by blocks of rows (NB) and groups a wave (GP): what the
-// 512 registers that the waves of a SIMD share allow, with 8 waves a compute
-// unit for one and two blocks (48 rows: 70 us, with 4 waves 78 us).
+// Waves of a workgroup, workgroups of a compute unit, groups of 256 values that
+// a wave holds at most and tiles that its registers hold ahead, by blocks of
+// rows (NB) and groups (GP): what the 512 registers that the waves of a SIMD
+// share allow, with 8 waves a compute unit for one and two blocks (48 rows of
+// the 151936 x 4096 head: 70 us, with 4 waves 78 us).
 constexpr int stream_waves(int nb) { return nb == 2 ? 8 : 4; }
 constexpr int stream_groups(int nb) { return nb == 1 ? 2 : 1; }
+constexpr int stream_most(int nb) { return nb == 2 ? 2 : 4; }
 constexpr int stream_depth(int nb, int gp) { return (nb == 1 || nb == 4) && gp == 4 ? 1 : 2; }
 
 // One lane's block of 32 values (64 bytes of BF16), quantised as k_mx4_quantize does.
@@ -311,22 +314,23 @@ struct StreamPart {     // a wave's part of a tile of the projection
   int sc[GP];
 };
 
-template <int NB, int GP>
+template <int NB, int GP, int SP>
 __global__ __launch_bounds__(stream_waves(NB) * 64, stream_waves(NB) * stream_groups(NB) / 4) void k_mx4_stream(
     Geo g, const uint16_t* __restrict__ hidden, int64_t ldh, int d, int tiles, int w_tiles, uint16_t* __restrict__ out) {
   constexpr int kDepth = stream_depth(NB, GP);
-  constexpr int kStreamWaves = stream_waves(NB);
-  __shared__ f32x4 slots[kStreamWaves - 1][NB][4][64];
+  constexpr int kTeams = stream_waves(NB) / SP;   // teams of SP waves, each with tiles of its own
+  __shared__ f32x4 slots[kTeams][SP > 1 ? SP - 1 : 1][SP > 1 ? NB : 1][4][64];
   const int lane = threadIdx.x & 63;
-  const int w = wave_id();
-  const int per = (g.steps4 + kStreamWaves - 1) / kStreamWaves;   // groups of a wave, at most GP
+  const int team = wave_id() / SP;
+  const int w = wave_id() % SP;                   // this wave's place in its team
+  const int per = (g.steps4 + SP - 1) / SP;       // groups of a wave, at most GP
   const int g0 = w * per;
-  const int cnt = g.steps4 - g0 < per ? g.steps4 - g0 : per;       // may be below 1
-  // this workgroup's tiles: neighbours, so that the two halves of a line of logits meet in L2
-  const int share = (tiles + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-  const int first = static_cast<int>(blockIdx.x) * share;
-  const int n_tiles = tiles - first < share ? tiles - first : share;
-  if (n_tiles <= 0) return;  // uniform across the workgroup
+  const int cnt = g.steps4 - g0 < per ? g.steps4 - g0 : per;  // may be below 1
+  // this team's tiles: neighbours, so that the two halves of a line of logits meet in L2
+  const int teams = static_cast<int>(gridDim.x) * kTeams;
+  const int share = (tiles + teams - 1) / teams;
+  const int first = (static_cast<int>(blockIdx.x) * kTeams + team) * share;
+  const int n_tiles = tiles - first < share ? tiles - first : share;  // may be below 1
   const int64_t codes = static_cast<int64_t>(g.steps4) * (kSteps * kStepBytes);  // of a packed tile
   const int64_t scales = static_cast<int64_t>(g.steps4) * kScaleBytes;
 
@@ -409,7 +413,7 @@ __global__ __launch_bounds__(stream_waves(NB) * 64, stream_waves(NB) * stream_gr
     }
   };
 
-  for (int turn = 0; turn < n_tiles + kStreamWaves - 1; ++turn) {
+  for (int turn = 0; turn < share + SP - 1; ++turn) {  // as many in every team: their barriers are one
     const int i = turn - w;
     const bool on = i >= 0 && i < n_tiles;  // uniform across the wave
     f32x16 acc[NB];
@@ -418,23 +422,24 @@ __global__ __launch_bounds__(stream_waves(NB) * 64, stream_waves(NB) * stream_gr
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const f32x4 v = w == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : slots[w - 1][b][e][lane];
+          f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (SP > 1 && w > 0) v = slots[team][w - 1][SP > 1 ? b : 0][e][lane];
 #pragma unroll
           for (int k = 0; k < 4; ++k) acc[b][4 * e + k] = v[k];
         }
     }
-    stream_barrier();  // every slot is read
+    if (SP > 1) stream_barrier();  // every slot is read
     if (on) {
       if (kDepth == 1 || (i & 1) == 0)
         multiply(part[0], i, acc);
       else
         multiply(part[kDepth - 1], i, acc);
-      if (w < kStreamWaves - 1) {
+      if (SP > 1 && w < SP - 1) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            slots[w][b][e][lane] = f32x4{acc[b][4 * e], acc[b][4 * e + 1], acc[b][4 * e + 2], acc[b][4 * e + 3]};
+            slots[team][SP > 1 ? w : 0][SP > 1 ? b : 0][e][lane] = f32x4{acc[b][4 * e], acc[b][4 * e + 1], acc[b][4 * e + 2], acc[b][4 * e + 3]};
       } else {
         const int h = lane >> 5;
         const int64_t c = static_cast<int64_t>(first + i) * kTileRows + 16 * h;
@@ -450,7 +455,7 @@ __global__ __launch_bounds__(stream_waves(NB) * 64, stream_waves(NB) * stream_gr
         }
       }
     }
-    stream_barrier();  // every slot is written
+    if (SP > 1) stream_barrier();  // every slot is written
   }
 }
 
@@ -893,15 +898,26 @@ template <int NB>
 static void launch_stream_blocks(const Geo& g, const uint16_t* hidden, int64_t ldh, int d, uint16_t* out, hipStream_t stream) {
   const int tiles = static_cast<int>(g.vocab_padded / kTileRows);  // at most 2^25
   const int w_tiles = static_cast<int>(row_tiles(g.vocab_real));
-  const int most = 256 * stream_groups(NB);
-  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most)), block(stream_waves(NB) * 64);
-  const int per = (g.steps4 + stream_waves(NB) - 1) / stream_waves(NB);
-  if (per <= 1)
-    k_mx4_stream<NB, 1><<<grid, block, 0, stream>>>(g, hidden, ldh, d, tiles, w_tiles, out);
-  else if (per <= 2)
-    k_mx4_stream<NB, 2><<<grid, block, 0, stream>>>(g, hidden, ldh, d, tiles, w_tiles, out);
-  else if constexpr (stream_waves(NB) == 4)
-    k_mx4_stream<NB, 4><<<grid, block, 0, stream>>>(g, hidden, ldh, d, tiles, w_tiles, out);
+  constexpr int kMost = stream_most(NB);
+  const auto run = [&](auto kernel, int split) {
+    const int teams = stream_waves(NB) / split;
+    const int wanted = (tiles + teams - 1) / teams, most = 256 * stream_groups(NB);
+    kernel<<<dim3(static_cast<unsigned>(wanted < most ? wanted : most)), dim3(stream_waves(NB) * 64), 0, stream>>>(
+        g, hidden, ldh, d, tiles, w_tiles, out);
+  };
+  // as few parts of d as the registers hold
+  if (g.steps4 <= 1)
+    run(k_mx4_stream<NB, 1, 1>, 1);
+  else if (g.steps4 <= 2)
+    run(k_mx4_stream<NB, 2, 1>, 1);
+  else if (g.steps4 <= kMost)
+    run(k_mx4_stream<NB, kMost, 1>, 1);
+  else if (g.steps4 <= 2 * kMost)
+    run(k_mx4_stream<NB, kMost, 2>, 2);
+  else if (g.steps4 <= 4 * kMost)
+    run(k_mx4_stream<NB, kMost, 4>, 4);
+  else if constexpr (8 * kMost <= kStreamSteps4)
+    run(k_mx4_stream<NB, kMost, 8>, 8);
 }
 
 static void launch_stream(const Geo& g, int blocks, const uint16_t* hidden, int64_t ldh, int d, uint16_t* out,
