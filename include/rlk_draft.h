@@ -83,15 +83,16 @@ typedef struct rlk_scored_rows {
  *               behind it
  *   workspace   rlk_draft_workspace_bytes(n_seq, layout) bytes, 16-byte
  *               aligned; calls that overlap need one each
+ * Outputs and workspace must not overlap the inputs.
  * Rows of no sequence are left as they were in the outputs. draft_token,
  * accept_u and draft may be NULL when n_draft is 0.
  * Device data that cannot be served: a sequence whose draft_start is out of
- * order or range has accepted_out = -1 and nothing else written. Where the
- * row reached has no policy (status < 0 or NaN on either side), the drafted
- * token is outside [0, vocab_real), a random number is outside [0, 1) or there
- * is nothing to draw from (p has no mass; or p is nowhere above q and gives
- * the drafted token none), token_out is -1 and both logprobs are NaN at that
- * place, and the sequence ends there. */
+ * order or range has accepted_out = -1 and nothing else written. Where the row
+ * reached has no policy (status < 0, or NaN in its record, logprob or
+ * temperature, on either side), the drafted token is outside [0, vocab_real), a
+ * random number is outside [0, 1) or there is nothing to draw from (p has no
+ * mass; or p is nowhere above q and gives the drafted token none), token_out is
+ * -1 and both logprobs are NaN at that place, and the sequence ends there. */
 int32_t rlk_draft_verify(const rlk_scored_rows* target, const rlk_scored_rows* draft,
                          const rlk_vocab_layout* layout, int64_t n_seq, int64_t n_draft,
                          const int64_t* draft_start, const int64_t* draft_token, const double* accept_u,

@@ -77,7 +77,8 @@ int32_t rlk_mx4_quantize(const uint16_t* x, int64_t n_rows, int64_t d, int64_t r
  *   weight_codes, weight_scales
  *                 rlk_mx4_quantize's output for the projection [vocab_real x
  *                 d_model], 16-byte aligned
- *   layout        as for rlk_linear; row_stride is the row stride of logits_out
+ *   layout        as for rlk_linear, vocab_real at most 2^22; row_stride is the
+ *                 row stride of logits_out
  *   logits_out    BF16 [n_rows x row_stride], 16-byte aligned: columns [0,
  *                 vocab_real) hold x, [vocab_real, vocab_padded) -inf, the rest
  *                 of each row is not written

@@ -101,7 +101,8 @@ __device__ __forceinline__ Stop find_stop(const Args& a, int64_t s, int lane) {
     if (!sampled) lq = 0.0f;
     bool wrong = st.status < 0, stays = false;
     if (k < r.count) {
-      wrong |= lp != lp || tok < 0 || tok >= a.vocab_real || !unit(u) || (sampled && (sq.status < 0 || lq != lq));
+      wrong |= lp != lp || tok < 0 || tok >= a.vocab_real || !unit(u) || 
+               (sampled && (sq.status < 0 || lq != lq || sq.lse_support != sq.lse_support || !rlk::temperature_valid(t_q)));
       // a drafted token of no policy mass is never accepted (also where the drafter gave it none)
       stays = !wrong && lp > -INFINITY && u < exp(static_cast<double>(lp) - static_cast<double>(lq));
     }

@@ -59,7 +59,9 @@ def verify(target: Rows, draft: Optional[Rows], vocab_real, start, token, accept
             wrong = target.status[row] < 0 or math.isnan(lp) or not 0 <= token[i] < vocab_real or not 0 <= accept_u[i] < 1
             if draft is not None and draft.temperature[i] != 0:
                 lq, q_row = float(draft.policy[i]), i
-                wrong = wrong or draft.status[i] < 0 or math.isnan(lq)
+                tq = float(draft.temperature[i])
+                wrong = (wrong or draft.status[i] < 0 or math.isnan(lq) or math.isnan(draft.lse_support[i])
+                         or not 0 <= tq < math.inf)
             if wrong or lp == -math.inf:
                 break
             ratio = math.inf if lp - lq > 700 else math.exp(lp - lq)

@@ -144,6 +144,15 @@ CASES = [
     ([1] * 64, 1, 64, (1.0, 0.0), 1.0, -1, "sampled"),
     ([0, 7, 0, 0, 63, 64, 65, 200, 1], 700, 704, (1.0,), 1.0, -1, "sampled"),
     ([1] * 500, 130000, 130048, (1.0,), 1.0, -1, "point"),
+    # more pieces of 512 columns than a workgroup keeps: few and many sequences
+    ([2, 0, 1], 300001, 300032, (0.9,), 1.0, -1, "sampled"),
+    ([1] * 140, 262145, 262208, (1.0, 0.0), 0.98, -1, "sampled"),
+    # around the numbers of sequences at which the work is shared out in another way
+    ([1] * 8, 151936, 152576, (0.8, 0.0), 1.0, -1, "sampled"),
+    ([1] * 14, 151936, 152576, (0.8, 0.0), 1.0, -1, "sampled"),
+    ([2] * 128, 9000, 9024, (0.7,), 0.9, -1, "sampled"),
+    ([2] * 129, 9000, 9024, (0.7, 1.3), 1.0, -1, "sampled"),
+    ([1] * 257, 9000, 9024, (0.7, 1.3), 1.0, 400, "sampled"),
 ]
 
 
@@ -288,6 +297,67 @@ def test_what_cannot_be_served():
     want = b.want()
     assert np.array_equal(got[1], want[1]) and (want[1][[0, 4, 8, 9]] == -1).all()
     assert (got[0][0:2] == 77).all()
+
+
+def test_values_outside_the_table():
+    """Rows of many columns, so that weights come from the table, with zeros, -0,
+    tiny, huge and -inf values among them, and a support of exactly those."""
+    say("case: zeros, tiny and huge logits")
+    rng = np.random.default_rng(14)
+    vr, vp, n = 40000, 40064, 140
+    b = Batch(rng, [1] * n, vr, vp, (1.0, 7.0), 1.0, -1, "sampled")
+    odd = np.array([0.0, -0.0, 1e-20, -1e-20, 2.0 ** -13, -(2.0 ** -13), 63.75, 64.0, -64.0, -700.0, -1e4, -3e38, -np.inf])
+    for bits in (b.bits, b.q_bits):
+        where = rng.random((len(bits), vr)) < 0.3
+        values = rng.choice(odd, (len(bits), vr))
+        values[values > 60] = np.where(rng.random((values > 60).sum()) < 0.001, values[values > 60], 0.0)
+        bits[:, :vr][where] = datagen.f32_to_bf16_bits(values.astype(np.float32))[where]
+    got = b.score().check()
+    assert (got[0][:2 * n:2] >= 0).all()
+
+
+def test_unusable_statistics_of_the_draft():
+    """A draft row whose record or temperature is not a number ends its
+    sequence there; it is never taken for a drafter that gives nothing."""
+    say("case: NaN in the draft's statistics")
+    import torch
+    b = Batch(np.random.default_rng(15), [1] * 4, 3000, 3008, (1.0,), 1.0, -1, "sampled").score()
+    b.accept_u[:] = 1 - 2.0 ** -53
+    b.qstats[3].view(torch.float32)[0, 0] = float("nan")   # lse_support, status left at 1
+    b.tq[1] = np.nan
+    b.tq[2] = -1.0
+    got = b.call()
+    assert got[1][:3].tolist() == [0, 0, 0]
+    assert (got[0][[0, 2, 4]] == -1).all() and np.isnan(got[2][[0, 2, 4]]).all()
+
+
+def test_offsets_past_31_bits():
+    """Sequences at the end of 14,100 rows of 152,576 columns (more than 2^31
+    elements): as in a call on those rows alone."""
+    import torch
+    say("case: rows past 2^31 elements")
+    b = Batch(np.random.default_rng(16), [2, 0, 3, 1], 151936, 152576, (0.8,), 1.0, -1, "sampled").score()
+    want = b.check()
+    nd, n, big = len(b.token), 4, 14100
+    rows = big + nd + n
+
+    def tail(t, total):
+        shape = (total,) + tuple(t.shape[1:])
+        out = torch.zeros(shape, dtype=t.dtype, device="cuda:0")
+        out[total - t.shape[0]:] = t
+        return out
+
+    pol, ref, lse, state = b.stats
+    got = rlk.draft_verify(
+        tail(b.lg, rows), tail(dev(b.token), big + nd), dev(b.start) + big, tail(dev(b.accept_u), big + nd), dev(b.sample_u),
+        temperature=tail(dev(b.t), rows), policy_logp=tail(pol, rows), ref_logp=tail(ref, rows), lse=tail(lse, rows),
+        support_state=tail(state, rows), vocab_real=b.vr, vocab_padded=b.vp, draft_logits=tail(b.qlg, big + nd),
+        draft_temperature=tail(dev(b.tq), big + nd), draft_policy_logp=tail(b.qstats[0], big + nd),
+        draft_support_state=tail(b.qstats[3], big + nd))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert to_host(g[g.shape[0] - len(w):]).tobytes() == w.tobytes()
+    assert (to_host(got[0][:big]) == -1).all()
 
 
 def test_inf_rows_in_masked_places():

@@ -140,6 +140,26 @@ def test_linear_is_exact_where_the_sums_are(n, d, vr, vp):
     assert np.array_equal(got, datagen.f32_to_bf16_bits(want.astype(np.float32)))
 
 
+# every way of splitting d over the waves (1, 2, 4 and 8 parts; d above 4096 goes another way), for one, two and four
+# blocks of rows, with more tiles of the vocabulary than teams of waves
+SPLITS = [(3, 96, 70001, 70016), (20, 512, 70001, 70016), (32, 1024, 66001, 66048), (7, 1280, 35001, 35008),
+          (1, 2304, 17001, 17024), (31, 4096, 16500, 16512), (1, 4352, 1000, 1024), (32, 8192, 500, 512),
+          (40, 256, 66001, 66048), (64, 512, 66001, 66048), (33, 800, 33001, 33024), (50, 2048, 17001, 17024),
+          (64, 2080, 9001, 9024), (48, 4096, 8300, 8320), (64, 5120, 600, 640),
+          (70, 160, 33001, 33024), (128, 512, 33001, 33024), (100, 992, 33001, 33024), (65, 1056, 17001, 17024),
+          (96, 3328, 8300, 8320), (128, 4096, 8300, 8320), (128, 4128, 300, 320), (130, 4352, 700, 704)]
+
+
+@pytest.mark.parametrize("n,d,vr,vp", SPLITS)
+def test_linear_is_exact_at_every_split_of_d(n, d, vr, vp):
+    say(f"case: exact 4-bit linear {n} x {d} x {vr}/{vp}")
+    rng = np.random.default_rng(n + 3 * d)
+    hb, wb = exact_matrix(rng, n, d), exact_matrix(rng, vr, d)
+    got = run_linear(hb, wb, vp)
+    want = MX.decode_bf16(hb).astype(np.float32) @ MX.decode_bf16(wb).astype(np.float32).T   # exact in float32 in any order
+    assert np.array_equal(got, datagen.f32_to_bf16_bits(want))
+
+
 @pytest.mark.parametrize("n,d,vr,vp", [(3, 4096, 2000, 2048), (48, 1056, 3000, 3008), (300, 2080, 1500, 1536), (700, 512, 5000, 5056)])
 def test_linear_random_values(n, d, vr, vp):
     say(f"case: random 4-bit linear {n} x {d} x {vr}/{vp}")
@@ -169,6 +189,45 @@ def test_linear_rows_do_not_depend_on_the_batch():
     order = torch.from_numpy(rng.permutation(n)).to("cuda:0")
     mixed = to_host(rlk.mx4_linear(h[order].contiguous(), wc, ws, vocab_real=vr, vocab_padded=vp).view(torch.int16))
     assert np.array_equal(mixed, whole[to_host(order)])
+
+
+def test_linear_rows_do_not_depend_on_the_batch_with_a_long_d():
+    import torch
+    say("case: 4-bit linear, d above 4096, one row in several batches")
+    rng = np.random.default_rng(22)
+    n, d, vr, vp = 260, 4640, 1001, 1024
+    h = upload(random_bits(rng, n, d, 2))
+    wc, ws = rlk.mx4_quantize(upload(random_bits(rng, vr, d, 2)))
+    whole = to_host(rlk.mx4_linear(h, wc, ws, vocab_real=vr, vocab_padded=vp).view(torch.int16))
+    for m in (1, 33, 128, 129):
+        part = to_host(rlk.mx4_linear(h[9:9 + m], wc, ws, vocab_real=vr, vocab_padded=vp).view(torch.int16))
+        assert np.array_equal(part, whole[9:9 + m]), m
+
+
+def test_offsets_past_31_bits():
+    """A matrix of more than 2^32 bytes to quantise, logits of more than 2^31
+    elements: the last rows as in a call of their own."""
+    import torch
+    say("case: 4-bit quantise 34000 x 65536, linear 14200 x 64 x 151936")
+    gen = torch.Generator(device="cuda:0")
+    gen.manual_seed(1)
+    n, d = 34000, 65536
+    x = torch.zeros((n, d), dtype=torch.bfloat16, device="cuda:0")
+    x[-40:] = torch.randn((40, d), generator=gen, device="cuda:0").to(torch.bfloat16)
+    c, s, v = rlk.mx4_quantize(x, return_values=True)
+    c2, s2, v2 = rlk.mx4_quantize(x[-48:].contiguous(), return_values=True)   # 34000 - 48 is no multiple of 32: rows 16 ..
+    assert torch.equal(v[-48:], v2)
+    last = rlk.mx4_bytes(32, d)
+    c3, s3 = rlk.mx4_quantize(x[-16:].contiguous())   # 34000 = 32 * 1062 + 16: the last tile's rows
+    assert torch.equal(c[-last[0]:], c3) and torch.equal(s[-last[1]:], s3)
+    del x, v, v2, c, c2
+    n, d, vr, vp = 14200, 64, 151936, 152576
+    h = torch.randn((n, d), generator=gen, device="cuda:0").to(torch.bfloat16)
+    w = torch.randn((vr, d), generator=gen, device="cuda:0").to(torch.bfloat16)
+    wc, ws = rlk.mx4_quantize(w)
+    out = rlk.mx4_linear(h, wc, ws, vocab_real=vr, vocab_padded=vp)
+    tail = rlk.mx4_linear(h[-50:].contiguous(), wc, ws, vocab_real=vr, vocab_padded=vp)
+    assert torch.equal(out[-50:], tail)
 
 
 @pytest.mark.parametrize("n", [6, 300])
