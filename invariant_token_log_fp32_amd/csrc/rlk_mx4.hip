@@ -7,10 +7,22 @@
 //                    whose largest magnitude comes from packed 16-bit maxima
 //                    and two steps over the four lanes; the hardware's
 //                    conversion rounds to 4 bits (nearest even, saturating).
-//   k_mx4_rows       a wave takes 32 rows x 64 vocabulary columns of the
-//                    product and streams both operands from memory straight
-//                    into the matrix instructions' registers: the packed
-//                    layout holds, lane after lane, what one instruction takes.
+//                    Bound by memory: 151936 x 4096 with values 2.8 GB in 0.53
+//                    ms, 5.4 TB/s, as fast as a large copy (4.8-5.1 TB/s).
+//   k_mx4_stream     up to 128 rows, d up to 4096: the projection streamed past
+//                    hidden states in registers. Bound by reading it: 332 MB of
+//                    the 151936 x 4096 head, 1 row 59 us (5.6 TB/s; a bare read
+//                    of as much takes 49 us), 48 rows 70 us, 128 rows 85 us.
+//   k_mx4_tiles      more rows: 256 x 256 tiles, operands through LDS. 8192
+//                    rows of the head 2.41 ms, 4.2 PFLOP/s: the bare scaled
+//                    matrix instructions run at 6.3 on all compute units, where
+//                    power holds the clock at 1.5 GHz.
+//   k_mx4_rows       up to 128 rows with a longer d: a wave takes 32 rows x 64
+//                    vocabulary columns and streams both operands from memory
+//                    straight into the matrix instructions' registers: the
+//                    packed layout holds, lane after lane, what one takes.
+// All of them add a logit's products in the same order (64 values of d an
+// instruction, the accumulator carried), so its bits do not depend on the kernel.
 #include <hip/hip_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -205,7 +217,12 @@ __device__ __forceinline__ void stream_step(const Frag4& w, const Frag4 (&h)[NB]
 
 constexpr int kRowsThreads = 256;
 constexpr int kRowsCols = 64;  // columns of a wave
-constexpr int64_t kRowsMost = 128;  // rows up to which k_mx4_rows runs
+// Up to 128 rows with d above 4096 (where k_mx4_stream's registers end) run on
+// k_mx4_rows if they are one block of 32, or if the vocabulary has fewer than
+// 128 tiles of the wide kernel (half the compute units): 151936 x 8192, 32 rows
+// 131 us (wide 183), 64 rows 225 (wide 188); 20000 x 16384, 64 rows 71 us (wide 113).
+constexpr int64_t kRowsMost = 128;
+constexpr int64_t kRowsTiles = 128;
 
 __global__ __launch_bounds__(kRowsThreads) void k_mx4_rows(Geo g, int64_t col_tiles, int64_t n_work,
                                                            uint16_t* __restrict__ out) {
@@ -701,6 +718,12 @@ __device__ __forceinline__ void read_first(const uint8_t* __restrict__ smem, int
   for (int j = 0; j < kNB; ++j) f.sc.w[j] = scale_word(scales + kPanelScales, fn, j);
 }
 
+// The tile's K loop takes 46-48,000 cycles at d = 4096 (the instructions alone
+// 32,768), its store 6-7,000, the step to the next tile 2,000, at 1.75-1.85 GHz:
+// the chip's power sets the clock. Without the loads into LDS the loop would take
+// 39,300, and 42,700 with every load from one place; waiting for them costs
+// nothing (counted waits against none), nor do the fragment reads.
+//
 // Products of one tile. Half stage x of the tile lives in LDS buffer (2 par +
 // x) % 4. While it is multiplied, the fragments of half stage x + 1 are read;
 // the barrier before it waits for x + 1 to land in LDS and for every wave's
@@ -1016,7 +1039,7 @@ int32_t rlk_mx4_linear(const uint16_t* hidden, int64_t n_rows, int64_t d_model, 
     launch_stream(g, blocks_of_rows, hidden, hidden_stride, static_cast<int>(d_model), logits_out, stream);
     return launched();
   }
-  if (n_rows > kRowsMost) {
+  if (n_rows > kRowsMost || (blocks_of_rows > 1 && layout->vocab_padded >= kRowsTiles * BN)) {
     TileGeo t;
     t.g = g;
     t.m_tiles = static_cast<int>((n_rows + BM - 1) / BM);                       // at most 2^14

@@ -191,17 +191,18 @@ def test_linear_rows_do_not_depend_on_the_batch():
     assert np.array_equal(mixed, whole[to_host(order)])
 
 
-def test_linear_rows_do_not_depend_on_the_batch_with_a_long_d():
+@pytest.mark.parametrize("vr,vp", [(1001, 1024), (33000, 33024)])
+def test_linear_rows_do_not_depend_on_the_batch_with_a_long_d(vr, vp):
     import torch
-    say("case: 4-bit linear, d above 4096, one row in several batches")
-    rng = np.random.default_rng(22)
-    n, d, vr, vp = 260, 4640, 1001, 1024
-    h = upload(random_bits(rng, n, d, 2))
-    wc, ws = rlk.mx4_quantize(upload(random_bits(rng, vr, d, 2)))
-    whole = to_host(rlk.mx4_linear(h, wc, ws, vocab_real=vr, vocab_padded=vp).view(torch.int16))
-    for m in (1, 33, 128, 129):
-        part = to_host(rlk.mx4_linear(h[9:9 + m], wc, ws, vocab_real=vr, vocab_padded=vp).view(torch.int16))
-        assert np.array_equal(part, whole[9:9 + m]), m
+    say(f"case: 4-bit linear, d above 4096, {vr} columns, one row in several batches")
+    gen = torch.Generator(device="cuda:0")
+    gen.manual_seed(22)
+    n, d = 260, 4640
+    h = torch.randn((n, d), generator=gen, device="cuda:0").to(torch.bfloat16)
+    wc, ws = rlk.mx4_quantize(torch.randn((vr, d), generator=gen, device="cuda:0").to(torch.bfloat16))
+    whole = rlk.mx4_linear(h, wc, ws, vocab_real=vr, vocab_padded=vp)
+    for m in (1, 32, 33, 128, 129):
+        assert torch.equal(rlk.mx4_linear(h[9:9 + m], wc, ws, vocab_real=vr, vocab_padded=vp), whole[9:9 + m]), m
 
 
 def test_offsets_past_31_bits():
