@@ -784,13 +784,14 @@ def draft_workspace_bytes(n_seq: int, vocab_padded: int, vocab_real: int) -> int
     return int(load_library().rlk_draft_workspace_bytes(int(n_seq), ctypes.byref(lay)))
 
 
-def _given(value, shape, dtype, device, name):
-    """A required input tensor, checked."""
-    torch = _torch()
-    if not isinstance(value, torch.Tensor) or value.dtype is not dtype or value.shape != shape or \
-            value.device != device or not value.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
-    return value
+def _given(device, *wanted):
+    """Checks required tensors, (tensor, shape, dtype, name) each (in one loop: a
+    call of a small batch takes less time on the GPU than its checks)."""
+    tensor = _torch().Tensor
+    for value, shape, dtype, name in wanted:
+        if not (isinstance(value, tensor) and value.dtype is dtype and value.shape == shape and
+                value.device == device and value.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
 @_on_stream
@@ -822,16 +823,26 @@ def draft_verify(logits, draft_token, draft_start, accept_u, sample_u, *, temper
     n_seq, n_draft = draft_start.numel() - 1, draft_token.numel()
     if n_seq < 0:
         raise ValueError("draft_start must hold n_seq + 1 offsets")
-    _given(draft_start, (n_seq + 1,), torch.int64, dev, "draft_start")
-    _given(draft_token, (n_draft,), torch.int64, dev, "draft_token")
-    _given(accept_u, (n_draft,), torch.float64, dev, "accept_u")
-    _given(sample_u, (n_seq,), torch.float64, dev, "sample_u")
     if n < n_draft + n_seq:
         raise ValueError(f"logits must hold a row for each of {n_draft} drafted tokens and {n_seq} sequences")
-    temperature = _per_row(temperature, n, torch.float32, dev, "temperature")
-    for value, name in ((policy_logp, "policy_logp"), (ref_logp, "ref_logp"), (lse, "lse")):
-        _given(value, (n,), torch.float32, dev, name)
-    _given(support_state, (n, 4), torch.int32, dev, "support_state")
+    f32, f64, i64, i32 = torch.float32, torch.float64, torch.int64, torch.int32
+    rows, drafts, seqs = (n,), (n_draft,), (n_seq,)
+    if isinstance(temperature, (int, float)):
+        temperature = torch.full(rows, temperature, dtype=f32, device=dev)
+    if token_out is None:
+        token_out = torch.full(rows, -1, dtype=i64, device=dev)
+    if accepted_out is None:
+        accepted_out = torch.full(seqs, -1, dtype=i32, device=dev)
+    if policy_out is None:
+        policy_out = torch.zeros(rows, dtype=f32, device=dev)
+    if ref_out is None:
+        ref_out = torch.zeros(rows, dtype=f32, device=dev)
+    _given(dev, (draft_start, (n_seq + 1,), i64, "draft_start"), (draft_token, drafts, i64, "draft_token"),
+           (accept_u, drafts, f64, "accept_u"), (sample_u, seqs, f64, "sample_u"),
+           (temperature, rows, f32, "temperature"), (policy_logp, rows, f32, "policy_logp"),
+           (ref_logp, rows, f32, "ref_logp"), (lse, rows, f32, "lse"), (support_state, (n, 4), i32, "support_state"),
+           (token_out, rows, i64, "token_out"), (accepted_out, seqs, i32, "accepted_out"),
+           (policy_out, rows, f32, "policy_out"), (ref_out, rows, f32, "ref_out"))
     target = ScoredRows(logits.data_ptr(), n, stride, temperature.data_ptr(), policy_logp.data_ptr(),
                         ref_logp.data_ptr(), lse.data_ptr(), support_state.data_ptr())
     draft = None
@@ -840,25 +851,13 @@ def draft_verify(logits, draft_token, draft_start, accept_u, sample_u, *, temper
         m = draft_logits.shape[0]
         if draft_logits.device != dev or m < n_draft or draft_logits.shape[1] < vp:
             raise ValueError(f"draft_logits must hold {n_draft} rows of at least {vp} columns on {dev}")
-        if not isinstance(draft_temperature, (int, float)):
-            _given(draft_temperature, (m,), torch.float32, dev, "draft_temperature")
-        draft_temperature = _per_row(draft_temperature, m, torch.float32, dev, "draft_temperature")
-        _given(draft_policy_logp, (m,), torch.float32, dev, "draft_policy_logp")
-        _given(draft_support_state, (m, 4), torch.int32, dev, "draft_support_state")
+        if isinstance(draft_temperature, (int, float)):
+            draft_temperature = torch.full((m,), draft_temperature, dtype=f32, device=dev)
+        _given(dev, (draft_temperature, (m,), f32, "draft_temperature"),
+               (draft_policy_logp, (m,), f32, "draft_policy_logp"),
+               (draft_support_state, (m, 4), i32, "draft_support_state"))
         draft = ScoredRows(draft_logits.data_ptr(), m, dstride, draft_temperature.data_ptr(),
                            draft_policy_logp.data_ptr(), None, None, draft_support_state.data_ptr())
-    if token_out is None:
-        token_out = torch.full((n,), -1, dtype=torch.int64, device=dev)
-    if accepted_out is None:
-        accepted_out = torch.full((n_seq,), -1, dtype=torch.int32, device=dev)
-    if policy_out is None:
-        policy_out = torch.zeros(n, dtype=torch.float32, device=dev)
-    if ref_out is None:
-        ref_out = torch.zeros(n, dtype=torch.float32, device=dev)
-    _given(token_out, (n,), torch.int64, dev, "token_out")
-    _given(accepted_out, (n_seq,), torch.int32, dev, "accepted_out")
-    _given(policy_out, (n,), torch.float32, dev, "policy_out")
-    _given(ref_out, (n,), torch.float32, dev, "ref_out")
     workspace, ws_bytes = _workspace(workspace, _draft_need(n_seq, vp, vocab_real), dev)
     _run("rlk_draft_verify", dev, ctypes.byref(target), ctypes.byref(draft) if draft is not None else None,
          _layout_ref(vp, vocab_real, vp)[1], n_seq, n_draft, draft_start.data_ptr(), draft_token.data_ptr(),

@@ -144,8 +144,8 @@ def test_struct_layout_matches_the_header():
 def test_binding_checks_inputs():
     meta = torch.device("meta")
     ok = torch.empty(4, dtype=torch.int64, device=meta)
-    assert rlk._given(ok, (4,), torch.int64, meta, "draft_token") is ok
+    rlk._given(meta, (ok, (4,), torch.int64, "draft_token"), (ok, (4,), torch.int64, "again"))
     for bad in (None, 3, ok.int(), ok[:3], torch.empty(8, dtype=torch.int64, device=meta)[::2],
                 torch.empty(4, dtype=torch.int64)):
         with pytest.raises(ValueError):
-            rlk._given(bad, (4,), torch.int64, meta, "draft_token")
+            rlk._given(meta, (ok, (4,), torch.int64, "first"), (bad, (4,), torch.int64, "draft_token"))
