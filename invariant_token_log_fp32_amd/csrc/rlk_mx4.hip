@@ -14,7 +14,7 @@
 //                    the 151936 x 4096 head, 1 row 59 us (5.6 TB/s; a bare read
 //                    of as much takes 49 us), 48 rows 70 us, 128 rows 85 us.
 //   k_mx4_tiles      more rows: 256 x 256 tiles, operands through LDS. 8192
-//                    rows of the head 2.41 ms, 4.2 PFLOP/s: the bare scaled
+//                    rows of the head 2.42 to 2.57 ms, 4.0 to 4.2 PFLOP/s: the bare scaled
 //                    matrix instructions run at 6.3 on all compute units, where
 //                    power holds the clock at 1.5 GHz.
 //   k_mx4_rows       up to 128 rows with a longer d: a wave takes 32 rows x 64
