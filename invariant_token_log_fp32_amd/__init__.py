@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 import re
 from typing import Optional, Tuple, Union
@@ -659,11 +660,17 @@ def linear_logp_merge(summaries, temperature, target, *, n_rows: int, groups: in
 
 def _on_stream(fn):
     """With ``stream=`` the whole call runs in that stream's context: what it
-    allocates and fills belongs to the stream, in order with its kernels."""
+    allocates and fills belongs to the stream, in order with its kernels. A
+    stream of another device than the first argument's is refused."""
+    first = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
         if stream is None:
             return fn(*args, **kw)
+        at = args[0] if args else kw[first]
+        if stream.device != at.device:
+            raise ValueError(f"stream is on {stream.device}, {first} on {at.device}")
         with _torch().cuda.stream(stream):
             return fn(*args, **kw)
     return call

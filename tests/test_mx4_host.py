@@ -161,3 +161,20 @@ def test_binding_checks_tensors():
         rlk.mx4_quantize(torch.zeros((4, 64), dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         rlk.mx4_linear(torch.zeros((4, 64), dtype=torch.bfloat16), None, None, vocab_real=10, vocab_padded=64)
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Before anything is asked of the stream; a stream's device is all that is read."""
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    x = torch.zeros((4, 64), dtype=torch.bfloat16, device=META)
+    with pytest.raises(ValueError, match="stream is on cuda:1, x on meta"):
+        rlk.mx4_quantize(x, stream=Stream())
+    with pytest.raises(ValueError, match="stream is on cuda:1, x on meta"):
+        rlk.mx4_quantize(x=x, stream=Stream())
+    with pytest.raises(ValueError, match="hidden on meta"):
+        rlk.mx4_linear(x, None, None, vocab_real=10, vocab_padded=64, stream=Stream())
+    with pytest.raises(ValueError, match="logits on meta"):
+        rlk.draft_verify(x, None, None, None, None, temperature=1.0, policy_logp=None, ref_logp=None, lse=None,
+                         support_state=None, vocab_real=10, stream=Stream())
