@@ -134,8 +134,8 @@ __device__ __forceinline__ Stop find_stop(const Args& a, int64_t s, int lane) {
   return r;
 }
 
-// e^y for y up to about 1, to a few 2^-53 of the value: y = n ln 2 + r with ln 2
-// in two parts, the series of e^r to r^12 (|r| <= ln(2) / 2 leaves 2e-16). n is
+// e^y for y up to about 1, to about 3 * 2^-53 of the value: y = n ln 2 + r with ln 2
+// as its float64 and the rest of it (one fused step each), the series of e^r to r^12 (|r| <= ln(2) / 2 leaves 2e-16). n is
 // rounded by an addition of 1.5 * 2^52, whose low word then holds it, and 2^n
 // is added to the exponent (conversions and ldexp run at a quarter of the rate).
 // Where the result nears the subnormal range (and for -inf) ldexp takes over.
@@ -144,8 +144,8 @@ __device__ __forceinline__ double exp_down(double y) {
   const double c = fmax(y, -1000.0);
   const double t = fma(c, 1.4426950408889634074, kRound);
   const double n = t - kRound;
-  double r = fma(-n, 6.93147180369123816490e-01, c);
-  r = fma(-n, 1.90821492927058770002e-10, r);
+  double r = fma(-n, 0x1.62e42fefa39efp-1, c);
+  r = fma(-n, 0x1.abc9e3b39803fp-56, r);
   double p = 2.08767569878680989792e-09;  // 1 / 12!
   p = fma(p, r, 2.50521083854417187751e-08);
   p = fma(p, r, 2.75573192239858906526e-07);
