@@ -87,7 +87,8 @@ typedef struct rlk_scored_rows {
  * Rows of no sequence are left as they were in the outputs. draft_token,
  * accept_u and draft may be NULL when n_draft is 0.
  * Device data that cannot be served: a sequence whose draft_start is out of
- * order or range has accepted_out = -1 and nothing else written. Where the row
+ * order or range has accepted_out = -1 and nothing else written (of two other
+ * sequences that then share rows, either may have written them). Where the row
  * reached has no policy (status < 0, or NaN in its record, logprob or
  * temperature, on either side), the drafted token is outside [0, vocab_real), a
  * random number is outside [0, 1) or there is nothing to draw from (p has no

@@ -81,7 +81,9 @@ int32_t rlk_mx4_quantize(const uint16_t* x, int64_t n_rows, int64_t d, int64_t r
  *                 row stride of logits_out
  *   logits_out    BF16 [n_rows x row_stride], 16-byte aligned: columns [0,
  *                 vocab_real) hold x, [vocab_real, vocab_padded) -inf, the rest
- *                 of each row is not written
+ *                 of each row is not written. It must not overlap the
+ *                 inputs or the workspace (a kernel may read hidden states
+ *                 while another part of it stores logits)
  *   workspace     rlk_mx4_linear_workspace_bytes(n_rows, d_model) bytes,
  *                 16-byte aligned; calls that overlap need one each
  * d_model: a multiple of 32 in [32, 65536]. A hidden row with NaN or an
