@@ -71,6 +71,14 @@ struct Stop {
 
 __device__ __forceinline__ bool unit(double u) { return u >= 0.0 && u < 1.0; }
 
+// Whether a row has a policy: the forward call's status, a temperature that is
+// one and, where the record's numbers count (greedy rows' lse_support is NaN),
+// a finite sum and a threshold.
+__device__ __forceinline__ bool usable(const rlk_support_state& st, float t) {
+  return st.status >= 0 && rlk::temperature_valid(t) &&
+         (t == 0.0f || (fabsf(st.lse_support) < INFINITY && st.threshold == st.threshold));
+}
+
 // One lane a place, the row behind the last drafted token included, so that all
 // a wave needs comes in two rounds of loads (the offsets, the rest).
 __device__ __forceinline__ Stop find_stop(const Args& a, int64_t s, int lane) {
@@ -103,17 +111,16 @@ __device__ __forceinline__ Stop find_stop(const Args& a, int64_t s, int lane) {
     }
     const bool sampled = k < r.count && drafter && t_q != 0.0f;
     if (!sampled) lq = 0.0f;
-    bool wrong = st.status < 0, stays = false;
+    bool wrong = !usable(st, t), stays = false;
     if (k < r.count) {
-      wrong |= lp != lp || tok < 0 || tok >= a.vocab_real || !unit(u) || 
-               (sampled && (sq.status < 0 || lq != lq || sq.lse_support != sq.lse_support || !rlk::temperature_valid(t_q)));
+      wrong |= lp != lp || tok < 0 || tok >= a.vocab_real || !unit(u) || (sampled && (!usable(sq, t_q) || lq != lq));
       // a drafted token of no policy mass is never accepted (also where the drafter gave it none)
       stays = !wrong && lp > -INFINITY && u < exp(static_cast<double>(lp) - static_cast<double>(lq));
     }
     const u64 stops = __ballot(!stays);
     if (stops == 0) continue;
     const int l = __builtin_amdgcn_readfirstlane(__ffsll(stops) - 1);
-    const bool served = !wrong && fair && rlk::temperature_valid(t) && (t == 0.0f || st.lse_support == st.lse_support);
+    const bool served = !wrong && fair;
     r.k = k0 + l;
     r.token = __shfl(tok, l, kWave);
     r.served = (__ballot(served) >> l) & 1;

@@ -37,6 +37,14 @@ def distribution(rows: Rows, i: int, vocab_real: int) -> np.ndarray:
     return np.where(x >= rows.threshold[i], p, 0.0)
 
 
+def usable(rows: Rows, i: int) -> bool:
+    """Whether row i has a policy."""
+    t = float(rows.temperature[i])
+    if rows.status[i] < 0 or not 0 <= t < math.inf:
+        return False
+    return t == 0 or (math.isfinite(rows.lse_support[i]) and not math.isnan(rows.threshold[i]))
+
+
 def verify(target: Rows, draft: Optional[Rows], vocab_real, start, token, accept_u, sample_u):
     """(tokens, accepted, policy, ref, margin): the outputs over the rows of the
     sequences, and per sequence the distance of the drawn token's borders from
@@ -56,12 +64,10 @@ def verify(target: Rows, draft: Optional[Rows], vocab_real, start, token, accept
         while k < count:
             i, row = first + k, base + k
             lp, lq, q_row = float(target.policy[row]), 0.0, None
-            wrong = target.status[row] < 0 or math.isnan(lp) or not 0 <= token[i] < vocab_real or not 0 <= accept_u[i] < 1
+            wrong = not usable(target, row) or math.isnan(lp) or not 0 <= token[i] < vocab_real or not 0 <= accept_u[i] < 1
             if draft is not None and draft.temperature[i] != 0:
                 lq, q_row = float(draft.policy[i]), i
-                tq = float(draft.temperature[i])
-                wrong = (wrong or draft.status[i] < 0 or math.isnan(lq) or math.isnan(draft.lse_support[i])
-                         or not 0 <= tq < math.inf)
+                wrong = wrong or not usable(draft, i) or math.isnan(lq)
             if wrong or lp == -math.inf:
                 break
             ratio = math.inf if lp - lq > 700 else math.exp(lp - lq)
@@ -73,9 +79,7 @@ def verify(target: Rows, draft: Optional[Rows], vocab_real, start, token, accept
         row = base + k
         t = float(target.temperature[row])
         policy[row] = ref[row] = np.nan
-        if wrong or target.status[row] < 0 or not 0 <= sample_u[s] < 1 or not (0 <= t < math.inf):
-            continue
-        if t != 0 and math.isnan(target.lse_support[row]):
+        if wrong or not usable(target, row) or not 0 <= sample_u[s] < 1:
             continue
         r = distribution(target, row, vocab_real)
         if t == 0:

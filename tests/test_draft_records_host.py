@@ -1,0 +1,37 @@
+"""The oracle of the verification on records that cannot be served: a row
+reached whose record, policy logprob or temperature is no number ends its
+sequence with token -1, whichever side it is on and whether or not its drafted
+token would have stayed."""
+import numpy as np
+import pytest
+
+from oracle import draft as OD
+from test_draft_host import scored
+
+
+def one(side, field, value, place, accept_u):
+    """A sequence of two drafted tokens, equal rows on both sides; one field of row `place` of a side is changed."""
+    rng = np.random.default_rng(1)
+    x = rng.normal(0, 1, (3, 12))
+    t, d = scored(x, 0.8, [2, 5, 0]), scored(x[:2], 0.8, [2, 5])
+    rows = t if side == "target" else d
+    changed = getattr(rows, field).copy()
+    changed[place] = value
+    rows = rows._replace(**{field: changed})
+    t, d = (rows, d) if side == "target" else (t, rows)
+    return OD.verify(t, d, 12, [0, 2], [2, 5], [accept_u, accept_u], [0.5])
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("accept_u", [0.0, 1 - 2.0 ** -53])
+@pytest.mark.parametrize("field,value", [("threshold", NAN), ("lse_support", NAN), ("lse_support", INF), ("lse_support", -INF),
+                                         ("temperature", NAN), ("temperature", INF), ("temperature", -1.0), ("status", -1),
+                                         ("status", -2)])
+@pytest.mark.parametrize("side,place", [("target", 0), ("target", 1), ("target", 2), ("draft", 0), ("draft", 1)])
+def test_a_row_without_a_policy_ends_its_sequence(side, place, field, value, accept_u):
+    out, accepted, policy, ref, margin = one(side, field, value, place, accept_u)
+    assert accepted[0] == place                 # equal rows: every drafted token before it stays
+    assert out[place] == -1 and np.isnan(policy[place]) and np.isnan(ref[place])
+    assert (out[place + 1:] == -1).all() and (policy[place + 1:] == 0).all() and margin[0] == INF

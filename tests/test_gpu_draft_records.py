@@ -1,0 +1,68 @@
+"""GPU parity of the verification on rows that cannot be served, against the
+float64 oracle (oracle/draft.py) on the same statistics. Tokens and counts are
+equal, logprobs those of the parity tests (one float32 rounding)."""
+import numpy as np
+import pytest
+
+from oracle import draft as OD
+
+from gpu_util import say, to_host
+from test_gpu_draft import Batch
+
+pytestmark = pytest.mark.gpu
+
+
+def reread(b):
+    """The oracle's rows from the statistics on the device, after a test has changed them."""
+    import invariant_token_log_fp32_amd as rlk
+
+    def rows(old, t, stats):
+        part, thr, status = (to_host(f.contiguous()) for f in rlk.support_state_fields(stats[3]))
+        return old._replace(temperature=t, policy=to_host(stats[0]), lse_support=part, threshold=thr, status=status)
+
+    b.rows = rows(b.rows, b.t, b.stats)
+    if b.qlg is not None:
+        b.q_rows = rows(b.q_rows, b.tq, b.qstats)
+
+
+def likely(b):
+    """Drafted tokens that are the drafter's maxima."""
+    b.token[:] = [int(np.argmax(OD.decode_bf16(q[:b.vr]))) for q in b.q_bits]
+
+
+# sequences that share a workgroup's work out, one workgroup each, and half a compute unit each
+@pytest.mark.parametrize("times", [1, 17, 33])
+@pytest.mark.parametrize("accept_u", [0.0, 1 - 2.0 ** -53])
+def test_a_row_without_a_policy_ends_its_sequence(times, accept_u):
+    """NaN in either field of a record, an infinite lse_support, a temperature
+    that is none: in the first row, in a row behind accepted tokens, in the row
+    behind the last drafted token, on either side."""
+    import torch
+    say(f"case: rows without a policy, {8 * times} sequences, accept_u {accept_u}")
+    b = Batch(np.random.default_rng(31), [2] * 8 * times, 2100, 2112, (1.0,), 0.9, -1, "sampled")
+    b.bits[1::3] = b.bits[0::3]
+    b.q_bits[0::2] = b.bits[0::3]        # equal rows: drafted tokens before the changed row stay
+    b.q_bits[1::2] = b.bits[1::3]
+    likely(b)
+    for s in range(7, 8 * times, 8):     # greedy targets, whose records hold NaN, are served
+        b.t[3 * s:3 * s + 3] = 0.0
+    b.accept_u[:] = accept_u
+    b.score()
+    tr, qr = b.stats[3].view(torch.float32), b.qstats[3].view(torch.float32)
+    for s in range(0, 8 * times, 8):
+        tr[3 * s, 1] = float("nan")                    # sequence 0: the first row's threshold
+        tr[3 * (s + 1) + 1, 0] = float("nan")          # 1: the second row's lse_support
+        tr[3 * (s + 2) + 2, 1] = float("nan")          # 2: the last row's threshold
+        qr[2 * (s + 3), 1] = float("nan")              # 3: the draft's first row's threshold
+        qr[2 * (s + 4) + 1, 0] = float("inf")          # 4: its second row's lse_support
+        b.t[3 * (s + 5)] = np.nan                      # 5: temperatures
+        b.tq[2 * (s + 6) + 1] = np.inf
+    reread(b)
+    got = b.check()
+    for s in range(0, 8 * times, 8):
+        at = [0, 1, 2, 0, 1, 0, 1]
+        assert got[1][s:s + 7].tolist() == at
+        for i, k in enumerate(at):
+            row = 3 * (s + i) + k
+            assert got[0][row] == -1 and np.isnan(got[2][row]) and np.isnan(got[3][row])
+        assert got[0][3 * (s + 7)] >= 0
