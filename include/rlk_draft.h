@@ -91,12 +91,12 @@ typedef struct rlk_scored_rows {
  * sequences that then share rows, either may have written them). Where the row
  * reached has no policy (status < 0, a temperature that is NaN, infinite or
  * below 0, a threshold that is NaN or an lse_support that is NaN or infinite,
- * on either side; a NaN policy logprob of a drafted token; greedy target rows'
- * records are read for their status alone), the drafted token is outside [0,
- * vocab_real), a random number is outside [0, 1) or there is nothing to draw
- * from (p has no mass; or p is nowhere above q and gives the drafted token
- * none), token_out is -1 and both logprobs are NaN at that place, and the
- * sequence ends there. */
+ * on either side; greedy rows' records are read for their status alone), a
+ * drafted token's policy logprob is NaN, on either side, the drafted token is
+ * outside [0, vocab_real), a random number is outside [0, 1) or there is
+ * nothing to draw from (p has no mass; or p is nowhere above q and gives the
+ * drafted token none), token_out is -1 and both logprobs are NaN at that place,
+ * and the sequence ends there. */
 int32_t rlk_draft_verify(const rlk_scored_rows* target, const rlk_scored_rows* draft,
                          const rlk_vocab_layout* layout, int64_t n_seq, int64_t n_draft,
                          const int64_t* draft_start, const int64_t* draft_token, const double* accept_u,

@@ -110,10 +110,10 @@ __device__ __forceinline__ Stop find_stop(const Args& a, int64_t s, int lane) {
       }
     }
     const bool sampled = k < r.count && drafter && t_q != 0.0f;
-    if (!sampled) lq = 0.0f;
     bool wrong = !usable(st, t), stays = false;
     if (k < r.count) {
-      wrong |= lp != lp || tok < 0 || tok >= a.vocab_real || !unit(u) || (sampled && (!usable(sq, t_q) || lq != lq));
+      wrong |= lp != lp || tok < 0 || tok >= a.vocab_real || !unit(u) || (drafter && (!usable(sq, t_q) || lq != lq));
+      if (!sampled) lq = 0.0f;  // a point mass
       // a drafted token of no policy mass is never accepted (also where the drafter gave it none)
       stays = !wrong && lp > -INFINITY && u < exp(static_cast<double>(lp) - static_cast<double>(lq));
     }

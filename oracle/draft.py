@@ -65,9 +65,10 @@ def verify(target: Rows, draft: Optional[Rows], vocab_real, start, token, accept
             i, row = first + k, base + k
             lp, lq, q_row = float(target.policy[row]), 0.0, None
             wrong = not usable(target, row) or math.isnan(lp) or not 0 <= token[i] < vocab_real or not 0 <= accept_u[i] < 1
-            if draft is not None and draft.temperature[i] != 0:
-                lq, q_row = float(draft.policy[i]), i
-                wrong = wrong or not usable(draft, i) or math.isnan(lq)
+            if draft is not None:
+                wrong = wrong or not usable(draft, i) or math.isnan(draft.policy[i])
+                if draft.temperature[i] != 0:
+                    lq, q_row = float(draft.policy[i]), i
             if wrong or lp == -math.inf:
                 break
             ratio = math.inf if lp - lq > 700 else math.exp(lp - lq)

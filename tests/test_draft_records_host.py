@@ -35,3 +35,18 @@ def test_a_row_without_a_policy_ends_its_sequence(side, place, field, value, acc
     assert accepted[0] == place                 # equal rows: every drafted token before it stays
     assert out[place] == -1 and np.isnan(policy[place]) and np.isnan(ref[place])
     assert (out[place + 1:] == -1).all() and (policy[place + 1:] == 0).all() and margin[0] == INF
+
+
+@pytest.mark.parametrize("field,value,served", [("status", -1, False), ("status", -2, False), ("policy", NAN, False),
+                                                ("lse_support", NAN, True), ("policy", -INF, True)])
+@pytest.mark.parametrize("place", [0, 1])
+def test_a_greedy_draft_row_is_a_point_mass_if_it_has_a_policy(place, field, value, served):
+    x = np.random.default_rng(2).normal(0, 1, (3, 12))
+    t, d = scored(x, 0.8, [2, 5, 0]), scored(x[:2], 0.8, [2, 5])
+    d = d._replace(temperature=np.zeros(2, np.float32), policy=np.zeros(2, np.float32), lse_support=np.full(2, NAN, np.float32))
+    changed = getattr(d, field).copy()
+    changed[place] = value
+    out, accepted, policy, _, _ = OD.verify(t, d._replace(**{field: changed}), 12, [0, 2], [2, 5], [0.0, 0.0], [0.5])
+    assert accepted[0] == (2 if served else place)
+    assert served or (out[place] == -1 and np.isnan(policy[place]))
+    assert not served or out[2] >= 0

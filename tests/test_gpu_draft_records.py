@@ -66,3 +66,27 @@ def test_a_row_without_a_policy_ends_its_sequence(times, accept_u):
             row = 3 * (s + i) + k
             assert got[0][row] == -1 and np.isnan(got[2][row]) and np.isnan(got[3][row])
         assert got[0][3 * (s + 7)] >= 0
+
+
+@pytest.mark.parametrize("times", [1, 33])
+def test_a_greedy_draft_row_without_a_policy_ends_its_sequence(times):
+    """Greedy rows of a drafter are point masses whose records hold NaN; one
+    that the forward call refused (a status below 0, a NaN logprob) is none."""
+    say(f"case: greedy draft rows without a policy, {4 * times} sequences")
+    b = Batch(np.random.default_rng(32), [2] * 4 * times, 2100, 2112, (1.0,), 1.0, -1, "sampled")
+    likely(b)
+    b.tq[:] = 0.0
+    b.accept_u[:] = 0.0
+    b.q_bits[0::8, 9] = 0x7FC0                          # sequence 0: NaN in the draft's first row
+    b.score()
+    b.qstats[3][3::8, 2] = -1                           # 1: a status of the second row
+    b.qstats[0][4::8] = float("nan")                    # 2: a logprob of the first row; 3 is served
+    reread(b)
+    assert b.q_rows.status[0] == -2 and np.isnan(b.q_rows.policy[0])
+    got = b.check()
+    for s in range(0, 4 * times, 4):
+        assert got[1][s:s + 4].tolist() == [0, 1, 0, 2]
+        for i, k in enumerate([0, 1, 0]):
+            row = 3 * (s + i) + k
+            assert got[0][row] == -1 and np.isnan(got[2][row]) and np.isnan(got[3][row])
+        assert (got[0][3 * (s + 3):3 * (s + 3) + 3] >= 0).all()
