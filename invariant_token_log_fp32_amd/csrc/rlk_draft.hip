@@ -141,14 +141,19 @@ __device__ __forceinline__ Stop find_stop(const Args& a, int64_t s, int lane) {
   return r;
 }
 
-// e^y for y up to about 1, to about 3 * 2^-53 of the value: y = n ln 2 + r with ln 2
+// e^y, to about 3 * 2^-53 of the value: y = n ln 2 + r with ln 2
 // as its float64 and the rest of it (one fused step each), the series of e^r to r^12 (|r| <= ln(2) / 2 leaves 2e-16). n is
 // rounded by an addition of 1.5 * 2^52, whose low word then holds it, and 2^n
 // is added to the exponent (conversions and ldexp run at a quarter of the rate).
-// Where the result nears the subnormal range (and for -inf) ldexp takes over.
+// Where the result nears the ends of the range ldexp takes over: 0 for y down to
+// -inf, infinity for y up to +inf (n fits its word because y is held to +-1000).
+// A drafter's weight (kDraft) stays finite, so that no p - q is a NaN and a sum
+// with an infinite p is refused. y is a number: lse_support is finite, and a NaN
+// logit never reaches the threshold.
+template <bool kDraft>
 __device__ __forceinline__ double exp_down(double y) {
   constexpr double kRound = 6755399441055744.0;
-  const double c = fmax(y, -1000.0);
+  const double c = fmin(fmax(y, -1000.0), kDraft ? 709.782712893384 : 1000.0);
   const double t = fma(c, 1.4426950408889634074, kRound);
   const double n = t - kRound;
   double r = fma(-n, 0x1.62e42fefa39efp-1, c);
@@ -167,17 +172,17 @@ __device__ __forceinline__ double exp_down(double y) {
   p = fma(p, r, 1.0);
   p = fma(p, r, 1.0);
   const int e = static_cast<int>(static_cast<uint32_t>(__builtin_bit_cast(u64, t)));
-  if (!(y > -700.0 && y < 700.0)) return ldexp(p, e);  // also NaN and +inf, whose sums are refused
+  if (!(y > -700.0 && y < 700.0)) return ldexp(p, e);
   return __builtin_bit_cast(double, __builtin_bit_cast(u64, p) + (static_cast<u64>(static_cast<uint32_t>(e)) << 52));
 }
 
 // One side's policy over the columns of a row.
+template <bool kDraft>
 struct Policy {
   double inv_t;
   double part;      // lse_support
   float threshold;
 
-  __device__ __forceinline__ Policy() : inv_t(0.0), part(0.0), threshold(INFINITY) {}
   __device__ __forceinline__ Policy(float t, float lse_support, float thr)
       : inv_t(1.0 / static_cast<double>(t)), part(static_cast<double>(lse_support)), threshold(thr) {}
 
@@ -189,7 +194,7 @@ struct Policy {
   __device__ __forceinline__ float scaled(float x) const { return static_cast<float>(static_cast<double>(x) * inv_t); }
 
   __device__ __forceinline__ double mass(float x) const {
-    return x >= threshold ? exp_down(static_cast<double>(scaled(x)) - part) : 0.0;
+    return x >= threshold ? exp_down<kDraft>(static_cast<double>(scaled(x)) - part) : 0.0;
   }
 };
 
@@ -225,7 +230,8 @@ __device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
 }
 
 // Weights of the 8 columns of a vector, from the table where all 8 are in it.
-__device__ __forceinline__ void look_up(const double* __restrict__ table, const Policy& p, const u32x4& v, double (&m)[8]) {
+template <bool kDraft>
+__device__ __forceinline__ void look_up(const double* __restrict__ table, const Policy<kDraft>& p, const u32x4& v, double (&m)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t s[4];
 #pragma unroll
@@ -250,7 +256,8 @@ __device__ __forceinline__ void look_up(const double* __restrict__ table, const 
   }
 }
 
-__device__ __forceinline__ void compute(const Policy& p, const u32x4& v, double (&m)[8]) {
+template <bool kDraft>
+__device__ __forceinline__ void compute(const Policy<kDraft>& p, const u32x4& v, double (&m)[8]) {
   float x[8];
   rlk::unpack8(v, x);
 #pragma unroll
@@ -261,8 +268,8 @@ __device__ __forceinline__ void compute(const Policy& p, const u32x4& v, double 
 struct Weights {
   const u32x4* p_row;
   const u32x4* q_row;    // NULL: no residual, or q is a point mass
-  Policy p;
-  Policy q;
+  Policy<false> p;
+  Policy<true> q;
   int64_t point;         // column of q's point mass, -1: none
 
   __device__ __forceinline__ Weights(const Args& a, int64_t s, const Stop& st)

@@ -92,9 +92,10 @@ def verify(target: Rows, draft: Optional[Rows], vocab_real, start, token, accept
                 q = distribution(draft, q_row, vocab_real)
             else:
                 q[token[first + k]] = 1.0
-            r = np.maximum(r - q, 0.0)
+            with np.errstate(invalid="ignore"):
+                r = np.maximum(r - q, 0.0)
         sums = np.cumsum(r)
-        if sums[-1] > 0:
+        if 0 < sums[-1] < math.inf:
             over = np.flatnonzero(sums > sample_u[s] * sums[-1])
             pick = int(over[0]) if over.size else int(np.flatnonzero(r > 0)[-1])
             near = np.abs(sums[max(0, pick - 1):pick + 1] - sample_u[s] * sums[-1])
@@ -102,6 +103,6 @@ def verify(target: Rows, draft: Optional[Rows], vocab_real, start, token, accept
             z = float(np.float32(decode_bf16(target.logits[row, pick:pick + 1])[0]) / np.float32(t))
             out[row] = pick
             policy[row], ref[row] = z - float(target.lse_support[row]), z - float(target.lse[row])
-        elif k < count and target.policy[row] > -math.inf:
+        elif sums[-1] == 0 and k < count and target.policy[row] > -math.inf:
             out[row], policy[row], ref[row] = token[first + k], target.policy[row], target.ref[row]
     return out, accepted, policy, ref, margin

@@ -50,3 +50,23 @@ def test_a_greedy_draft_row_is_a_point_mass_if_it_has_a_policy(place, field, val
     assert accepted[0] == (2 if served else place)
     assert served or (out[place] == -1 and np.isnan(policy[place]))
     assert not served or out[2] >= 0
+
+
+@pytest.mark.parametrize("kind", ["none", "point", "drafter"])
+@pytest.mark.parametrize("part,drawn", [(0.0, True), (-500.0, True), (-800.0, False), (-2e9, False), (800.0, False), (2e9, False)])
+def test_sums_that_are_not_finite_are_not_drawn_from(kind, part, drawn):
+    """lse_support far below the logits: weights up to e^500 are drawn from, an
+    infinite sum is not, nor is a row whose weights all vanish."""
+    x = np.random.default_rng(3).normal(0, 1, (2, 12))
+    t = scored(x, 1.0, [2, 0])
+    t = t._replace(lse_support=np.full(2, part, np.float32), policy=np.full(2, -np.inf if part > 0 else -60.0, np.float32))
+    d = scored(x[:1], 1.0, [2])
+    d = d._replace(lse_support=np.full(1, part + 1 if drawn else part, np.float32), policy=np.zeros(1, np.float32))
+    count = 0 if kind == "none" else 1
+    out, accepted, policy, _, margin = OD.verify(t, d if kind == "drafter" else None, 12, [0, count], [2] * count,
+                                                 [1 - 2.0 ** -53] * count, [0.5])
+    assert accepted[0] == 0
+    if drawn:
+        assert out[0] >= 0 and margin[0] < 1
+    else:
+        assert out[0] == -1 and np.isnan(policy[0]) and margin[0] == INF

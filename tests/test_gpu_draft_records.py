@@ -4,6 +4,7 @@ equal, logprobs those of the parity tests (one float32 rounding)."""
 import numpy as np
 import pytest
 
+import datagen
 from oracle import draft as OD
 
 from gpu_util import say, to_host
@@ -90,3 +91,47 @@ def test_a_greedy_draft_row_without_a_policy_ends_its_sequence(times):
             row = 3 * (s + i) + k
             assert got[0][row] == -1 and np.isnan(got[2][row]) and np.isnan(got[3][row])
         assert (got[0][3 * (s + 3):3 * (s + 3) + 3] >= 0).all()
+
+
+@pytest.mark.parametrize("n,kind", [(5, "none"), (140, "none"), (5, "point"), (140, "point"), (5, "sampled"), (140, "sampled")])
+@pytest.mark.parametrize("above", [500.0, 800.0, 2e9, 3e9, 1e12])
+def test_weights_beyond_float64(n, kind, above):
+    """A record whose lse_support lies far below a column's logit: e^500 can be
+    drawn from, e^800 and more is no weight and refuses the sequence, whatever
+    an integer of its exponent would wrap to; also where the drafter's weight
+    of that column is as large."""
+    import torch
+    say(f"case: weights of e^{above:g}, {n} sequences, drafter {kind}")
+    vr, vp = 40000, 40064
+    b = Batch(np.random.default_rng(33), [0 if kind == "none" else 1] * n, vr, vp, (1.0,), 1.0, -1,
+              "sampled" if kind == "sampled" else "point")
+    big = datagen.f32_to_bf16_bits(np.array([above], np.float32))[0]
+    step = 1 if kind == "none" else 2
+    b.bits[::step, 777] = big
+    b.accept_u[:] = 1 - 2.0 ** -53
+    b.token[:] = 5
+    b.q_bits[:, 777] = big
+    b.score()
+    b.stats[3].view(torch.float32)[:, 0] = 0.0          # as if the large column were none
+    b.stats[0][:] = -60.0
+    if kind == "sampled":
+        b.qstats[3].view(torch.float32)[:, 0] = 0.0
+        b.qstats[0][:] = -1.0
+    reread(b)
+    got = b.check()
+    if kind == "sampled" and above == 500.0:            # equal weights of that column: drawn among the others
+        assert (got[0][::step] >= 0).all() and (got[0][::step] != 777).all()
+    else:
+        assert (got[0][::step] == (777 if above == 500.0 else -1)).all()
+
+
+@pytest.mark.parametrize("counts", [[0] * 40, [2] * 40, [1] * 200])
+def test_tiny_temperatures(counts):
+    """Temperatures down to a subnormal one: the oracle's tokens, or its refusal
+    where the forward call's float32 statistics give no finite weight."""
+    say(f"case: tiny temperatures, {len(counts)} sequences of {max(counts)} drafted tokens")
+    b = Batch(np.random.default_rng(34), counts, 3000, 3008, (1e-4, 1e-8, 1e-10, 1e-12, 1e-17, 1e-40), 1.0, -1, "sampled")
+    likely(b)
+    got = b.score().check()
+    sharp = (b.t == np.float32(1e-4)) & (got[0] >= 0)
+    assert sharp.any()
