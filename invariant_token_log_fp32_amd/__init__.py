@@ -690,6 +690,8 @@ def _run(name, device, *args):
         raise RlkError(st, name)
 
 
+# Layouts and sizes are kept by value: what is looked up are ints (a tensor would
+# be looked up by its identity, whatever it holds by then).
 @functools.lru_cache(maxsize=256)
 def _layout_ref(vocab_padded, vocab_real, row_stride):
     """A rlk_vocab_layout of one group and its reference (never written to)."""
@@ -764,7 +766,8 @@ def mx4_linear(hidden, weight_codes, weight_scales, *, vocab_real: int, vocab_pa
     ldh = _bf16_matrix(hidden, "hidden")
     n, d = hidden.shape
     dev = hidden.device
-    need_c, need_s = _mx4_need(int(vocab_real), d)
+    vocab_real, vocab_padded = int(vocab_real), int(vocab_padded)
+    need_c, need_s = _mx4_need(vocab_real, d)
     for value, need, name in ((weight_codes, need_c, "weight_codes"), (weight_scales, need_s, "weight_scales")):
         if value is None:
             raise ValueError(f"{name} is missing")
@@ -824,7 +827,7 @@ def draft_verify(logits, draft_token, draft_start, accept_u, sample_u, *, temper
     stride = _check_logits(logits)
     n = logits.shape[0]
     dev = logits.device
-    vp = int(vocab_padded if vocab_padded is not None else logits.shape[1])
+    vocab_real, vp = int(vocab_real), int(vocab_padded if vocab_padded is not None else logits.shape[1])
     if logits.shape[1] < vp:
         raise ValueError(f"logits must have at least {vp} columns")
     n_seq, n_draft = draft_start.numel() - 1, draft_token.numel()
