@@ -656,8 +656,7 @@ static int32_t launch(const Args& a, hipStream_t stream) {
   int64_t each = (a.n_pieces + parts - 1) / parts;
   each = each > least ? each : least;
   parts = (a.n_pieces + each - 1) / each;
-  if (a.n_seq * parts > INT32_MAX) return RLK_ERR_SHAPE;
-  const dim3 grid(static_cast<unsigned>(a.n_seq * parts));
+  const dim3 grid(static_cast<unsigned>(a.n_seq * parts));        // at most 2^22: more than `wanted` only at one part
   if (table)
     k_draft<true, false, 1024, 2, 4><<<grid, dim3(1024), 0, stream>>>(a, static_cast<int>(parts), static_cast<int>(each));
   else

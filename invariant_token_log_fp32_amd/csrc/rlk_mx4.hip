@@ -1055,8 +1055,7 @@ int32_t rlk_mx4_linear(const uint16_t* hidden, int64_t n_rows, int64_t d_model, 
   }
   const int64_t col_tiles = layout->vocab_padded / kRowsCols;
   const int64_t n_work = col_tiles * row_tiles(n_rows);
-  const int64_t blocks = (n_work + kRowsThreads / 64 - 1) / (kRowsThreads / 64);
-  if (blocks > INT32_MAX) return RLK_ERR_SHAPE;
+  const int64_t blocks = (n_work + kRowsThreads / 64 - 1) / (kRowsThreads / 64);  // at most 2^22 (beyond 32 rows: fewer than 512 column tiles)
   k_mx4_rows<<<dim3(static_cast<unsigned>(blocks)), dim3(kRowsThreads), 0, stream>>>(g, col_tiles, n_work, logits_out);
   return launched();
 }
