@@ -11,10 +11,12 @@
 //   k_draft_pick  a wave a sequence, finds the piece in which the running sum
 //                 passes sample_u times the whole, reads that piece's columns
 //                 again and writes the outputs.
-// 1024 sequences x 3 drafted tokens of 151936 columns: 464 MB in 114 to 124 us,
-// bound by the issue of 103 vector instructions a piece of a row (column by
-// column, without the table of weights, 335 us). 256 samples: 26 us, a sequence's
-// loads, table, sums and draw one after another. 1 x 4: 6 + 6 us, dependent loads.
+// 1024 sequences x 3 drafted tokens of 151936 columns: 464 MB in 114 to 124 us
+// (column by column, without the table of weights, 335 us). Vector issue takes 69
+// us of it (92 instructions a piece of a row, 41.7M counted), LDS 45 us, 29 of
+// them bank conflicts of the look-ups; the two overlap in part. 256 samples: 26
+// us, a sequence's loads, table, sums and draw one after another. 1 x 4: 6 + 6
+// us, dependent loads.
 // Piece sums are formed in one order whichever kernel forms them, so a
 // sequence's outputs do not depend on the batch.
 #include <hip/hip_runtime.h>

@@ -7,20 +7,25 @@
 //                    whose largest magnitude comes from packed 16-bit maxima
 //                    and two steps over the four lanes; the hardware's
 //                    conversion rounds to 4 bits (nearest even, saturating).
-//                    Bound by memory: 151936 x 4096 with values 2.8 GB in 0.53
-//                    ms, 5.4 TB/s, as fast as a large copy (4.8-5.1 TB/s).
+//                    Bound by memory: 151936 x 4096 with values 2.8 GB in 0.49
+//                    to 0.52 ms, 5.4 to 5.7 TB/s (a large copy 4.8-5.1), codes
+//                    and scales alone 1.6 GB in 0.29 ms.
 //   k_mx4_stream     up to 128 rows, d up to 4096: the projection streamed past
 //                    hidden states in registers. Bound by reading it: 332 MB of
 //                    the 151936 x 4096 head, 1 row 59 us (5.6 TB/s; a bare read
 //                    of as much takes 49 us), 48 rows 70 us, 128 rows 85 us.
-//   k_mx4_tiles      more rows: 256 x 256 tiles, operands through LDS. 8192
-//                    rows of the head 2.42 to 2.57 ms, 4.0 to 4.2 PFLOP/s: the bare scaled
-//                    matrix instructions run at 6.3 on all compute units, where
-//                    power holds the clock at 1.5 GHz.
-//   k_mx4_rows       up to 128 rows with a longer d: a wave takes 32 rows x 64
-//                    vocabulary columns and streams both operands from memory
-//                    straight into the matrix instructions' registers: the
-//                    packed layout holds, lane after lane, what one takes.
+//   k_mx4_tiles      more rows, and 33 to 128 rows of a longer d where the
+//                    vocabulary fills half the GPU with its tiles: 256 x 256
+//                    tiles, operands through LDS. 8192 rows of the head 2.42
+//                    to 2.57 ms, 4.0 to 4.2 PFLOP/s: the bare scaled matrix
+//                    instructions run at 6.3 on all compute units, where power
+//                    holds the clock at 1.5 GHz.
+//   k_mx4_rows       up to 32 rows of a longer d, up to 128 of a smaller
+//                    vocabulary: a wave takes 32 rows x 64 vocabulary columns
+//                    and streams both operands from memory straight into the
+//                    matrix instructions' registers: the packed layout holds,
+//                    lane after lane, what one takes. 1 row of 151936 x 8192
+//                    121 us, 32 rows 127 us (661 MB, 5.2 to 5.5 TB/s).
 // All of them add a logit's products in the same order (64 values of d an
 // instruction, the accumulator carried), so its bits do not depend on the kernel.
 #include <hip/hip_runtime.h>
@@ -217,10 +222,10 @@ __device__ __forceinline__ void stream_step(const Frag4& w, const Frag4 (&h)[NB]
 
 constexpr int kRowsThreads = 256;
 constexpr int kRowsCols = 64;  // columns of a wave
-// Up to 128 rows with d above 4096 (where k_mx4_stream's registers end) run on
+// Up to 128 rows with d above 4096 (where k_mx4_stream ends) run on
 // k_mx4_rows if they are one block of 32, or if the vocabulary has fewer than
 // 128 tiles of the wide kernel (half the compute units): 151936 x 8192, 32 rows
-// 131 us (wide 183), 64 rows 225 (wide 188); 20000 x 16384, 64 rows 71 us (wide 113).
+// 131 us (wide 183), 64 rows 225 (wide 188 to 197); 20000 x 16384, 64 rows 71 us (wide 113).
 constexpr int64_t kRowsMost = 128;
 constexpr int64_t kRowsTiles = 128;
 
@@ -294,7 +299,11 @@ __global__ __launch_bounds__(kRowsThreads) void k_mx4_rows(Geo g, int64_t col_ti
 // multiplied, so loads are always on their way. (With d always in four parts a
 // short d spends its time on turns: 77 x 1056 x 50021 21.7 us.)
 constexpr int kStreamBlocks = 4;    // blocks of 32 hidden rows, at most
-constexpr int kStreamSteps4 = 16;   // groups of 256 values of d, at most (d <= 4096): the registers' limit
+// Groups of 256 values of d, at most (d <= 4096): where the registers of four
+// blocks of rows end (a wave's four groups take 256 for the hidden states, 64 for
+// the projection and 64 for accumulators, of 512). One and two blocks would have
+// room for more; they end here too, and what a longer d would gain was not measured.
+constexpr int kStreamSteps4 = 16;
 
 // Waves of a workgroup, workgroups of a compute unit, groups of 256 values that
 // a wave holds at most and tiles that its registers hold ahead, by blocks of
