@@ -94,10 +94,10 @@ typedef struct rlk_scored_rows {
  * on either side; greedy rows' records are read for their status alone), a
  * drafted token's policy logprob is NaN, on either side, the drafted token is
  * outside [0, vocab_real), a random number is outside [0, 1) or there is
- * nothing to draw from (p has no mass, or no finite mass above q, where |z| of
- * 1e10 and more leaves lse_support too coarse; or p is nowhere above q and gives
- * the drafted token none), token_out is -1 and both logprobs are NaN at that place,
- * and the sequence ends there. */
+ * nothing to draw from (the weights' sum is 0 and there is no drafted token, or
+ * one whose policy logprob is -inf; or the sum is not finite: where |z| passes
+ * 1e10, lse_support is too coarse), token_out is -1 and both logprobs are NaN
+ * at that place, and the sequence ends there. */
 int32_t rlk_draft_verify(const rlk_scored_rows* target, const rlk_scored_rows* draft,
                          const rlk_vocab_layout* layout, int64_t n_seq, int64_t n_draft,
                          const int64_t* draft_start, const int64_t* draft_token, const double* accept_u,

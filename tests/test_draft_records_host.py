@@ -70,3 +70,12 @@ def test_sums_that_are_not_finite_are_not_drawn_from(kind, part, drawn):
         assert out[0] >= 0 and margin[0] < 1
     else:
         assert out[0] == -1 and np.isnan(policy[0]) and margin[0] == INF
+
+
+@pytest.mark.parametrize("logp,token", [(-900.0, 2), (-INF, -1)])
+def test_weights_that_sum_to_0_leave_the_drafted_token_if_it_has_a_logprob(logp, token):
+    x = np.random.default_rng(4).normal(0, 1, (2, 12))
+    t = scored(x, 1.0, [2, 0])
+    t = t._replace(lse_support=np.full(2, 1000.0, np.float32), policy=np.full(2, logp, np.float32))
+    out, accepted, policy, _, _ = OD.verify(t, None, 12, [0, 1], [2], [0.5], [0.5])
+    assert accepted[0] == 0 and out[0] == token and (policy[0] == logp if token >= 0 else np.isnan(policy[0]))

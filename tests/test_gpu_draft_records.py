@@ -135,3 +135,22 @@ def test_tiny_temperatures(counts):
     got = b.score().check()
     sharp = (b.t == np.float32(1e-4)) & (got[0] >= 0)
     assert sharp.any()
+
+
+@pytest.mark.parametrize("n", [4, 140])
+def test_weights_that_sum_to_0(n):
+    """An lse_support far above every logit: no weight is left, and a refused
+    drafted token comes out if it has a logprob."""
+    import torch
+    say(f"case: weights that sum to 0, {n} sequences")
+    b = Batch(np.random.default_rng(35), [1, 1, 1, 0] * (n // 4), 9000, 9024, (1.0,), 1.0, -1, "point").score()
+    b.accept_u[:] = 0.5
+    b.stats[3].view(torch.float32)[:, 0] = 1000.0
+    b.stats[0][:] = -900.0
+    b.stats[0][2::7] = float("-inf")     # the second sequence of four: rows 2 and 3 of seven
+    reread(b)
+    got = b.check()
+    for s in range(0, n, 4):
+        row = 7 * (s // 4)
+        assert got[0][row] == b.token[3 * (s // 4)] and got[0][row + 4] == b.token[3 * (s // 4) + 2]
+        assert (got[0][[row + 2, row + 6]] == -1).all() and np.isnan(got[2][[row + 2, row + 6]]).all()
