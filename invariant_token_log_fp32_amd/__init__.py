@@ -25,6 +25,7 @@ __all__ = [
     "logp_nucleus_noalloc", "NOALLOC_MAX_ROWS", "RlkError", "N_SHARDS",
     "mx4_bytes", "mx4_quantize", "mx4_linear", "mx4_linear_workspace_bytes",
     "draft_verify", "draft_workspace_bytes",
+    "linear_logp_backward", "linear_logp_backward_merge", "linear_logp_backward_workspace_bytes",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -35,6 +36,8 @@ HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "rlk_logp.h")
 HEADER_PATHS = [HEADER_PATH] + [os.path.join(os.path.dirname(_PKG), "include", n) for n in ("rlk_norm.h", "rlk_linear.h")]
 # The serving operators' headers (rollout and drafting).
 SERVING_HEADER_PATHS = [os.path.join(os.path.dirname(_PKG), "include", n) for n in ("rlk_mx4.h", "rlk_draft.h")]
+# The training head's operators.
+TRAINING_HEADER_PATHS = [os.path.join(os.path.dirname(_PKG), "include", n) for n in ("rlk_linear_grad.h",)]
 N_SHARDS = 8
 NORM_BIN_WORDS = 264  # uint64 words of rlk_norm_bins
 NOALLOC_MAX_ROWS = 32768  # RLK_NOALLOC_MAX_ROWS
@@ -145,6 +148,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rlk_draft_verify.restype = i32
     lib.rlk_draft_workspace_bytes.argtypes = [i64, lay]
     lib.rlk_draft_workspace_bytes.restype = sz
+    lib.rlk_linear_logp_backward.argtypes = [vp, i64, i64, i64, vp, i64, lay, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64,
+                                             i32, vp, i64, i32, vp, sz, vp]
+    lib.rlk_linear_logp_backward.restype = i32
+    lib.rlk_linear_logp_backward_workspace_bytes.argtypes = [i64, i64, lay]
+    lib.rlk_linear_logp_backward_workspace_bytes.restype = sz
+    lib.rlk_linear_logp_backward_merge.argtypes = [vp, i64, i32, i64, i64, vp, i64, i32, vp]
+    lib.rlk_linear_logp_backward_merge.restype = i32
     _lib = lib
     return lib
 
@@ -874,3 +884,135 @@ def draft_verify(logits, draft_token, draft_start, accept_u, sample_u, *, temper
          accept_u.data_ptr(), sample_u.data_ptr(), token_out.data_ptr(), accepted_out.data_ptr(), policy_out.data_ptr(),
          ref_out.data_ptr(), workspace.data_ptr() if workspace is not None else None, ws_bytes)
     return token_out, accepted_out, policy_out, ref_out
+
+
+# ---------------------------------------------------------------------------
+# gradient of the fused linear + logprob (include/rlk_linear_grad.h)
+# ---------------------------------------------------------------------------
+
+GRAD_BF16, GRAD_F32, GRAD_F32_ADD = 0, 1, 2  # RLK_GRAD_*
+
+
+@functools.lru_cache(maxsize=1024)
+def _backward_need(n_rows, d_model, vocab_padded, vocab_real, groups):
+    """The layout of a backward call, its reference and its bytes of workspace."""
+    lay = make_layout(vocab_padded, vocab_real, vocab_padded, groups)
+    ref = ctypes.byref(lay)
+    return lay, ref, int(load_library().rlk_linear_logp_backward_workspace_bytes(n_rows, d_model, ref))
+
+
+def linear_logp_backward_workspace_bytes(n_rows: int, d_model: int, vocab_padded: int, vocab_real: int,
+                                         groups: int = 1) -> int:
+    return _backward_need(int(n_rows), int(d_model), int(vocab_padded), int(vocab_real), int(groups))[2]
+
+
+def _grad_out(value, shape, dtype, device, name, f32_only=False):
+    """A caller-supplied gradient (BF16 or float32, rows contiguous, stride a multiple of 8), checked, or a new one."""
+    torch = _torch()
+    if value is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(value, torch.Tensor) or value.dtype not in ((torch.float32,) if f32_only else (torch.bfloat16, torch.float32)) \
+            or value.device != device or tuple(value.shape) != tuple(shape) or value.stride(1) != 1 or value.stride(0) % 8:
+        what = "float32" if f32_only else "bfloat16 or float32"
+        raise ValueError(f"{name} must be a {what} tensor of shape {tuple(shape)} on {device} with contiguous rows, row "
+                         f"stride a multiple of 8")
+    return value
+
+
+@_on_stream
+def linear_logp_backward(hidden, weight, temperature, target, *, vocab_padded: int, vocab_real: Optional[int] = None,
+                         ref_logp=None, lse=None, grad_ref=None, policy_logp=None, support_state=None, grad_policy=None,
+                         hidden_grad: bool = True, weight_grad: bool = True, grad_hidden=None, grad_weight=None,
+                         accumulate: bool = False, rank: int = 0, groups: int = 1, workspace=None):
+    """Gradients of sum_i (grad_ref[i] * ref_i + grad_policy[i] * policy_i) with
+    respect to ``hidden`` and ``weight``, the logits bf16(hidden . weight^T)
+    formed again in pieces (rlk_linear_logp_backward).
+
+    ``hidden`` [n_rows, d_model] and ``weight`` [vocab_real, d_model] are BF16;
+    ``ref_logp`` and ``lse`` come from linear_logp (``return_lse``) or logp_full /
+    logp_nucleus on linear's logits, ``policy_logp`` and ``support_state`` from
+    logp_nucleus; a term whose upstream gradient is None is absent. Rows whose
+    upstream gradients are 0 get zeros and add nothing, whatever they hold.
+    Returns (grad_hidden, grad_weight), bfloat16, None for one that is not
+    wanted (``hidden_grad`` / ``weight_grad`` False). A given ``grad_hidden`` or
+    ``grad_weight`` may be float32; with ``accumulate`` a given float32
+    ``grad_weight`` is added to.
+
+    ``groups`` G > 1: the part of ``rank`` in a vocabulary-parallel layout. ``weight``
+    holds its projection rows (columns [rank*C, (rank+1)*C) below ``vocab_real``, C =
+    vocab_padded / G), grad_hidden is float32 by default, for
+    linear_logp_backward_merge."""
+    torch = _torch()
+    ldh = _bf16_matrix(hidden, "hidden")
+    ldw = _bf16_matrix(weight, "weight")
+    n, d = hidden.shape
+    dev = hidden.device
+    rank, groups, vocab_padded = int(rank), int(groups), int(vocab_padded)
+    if vocab_real is None:
+        if groups != 1:
+            raise ValueError("vocab_real must be given for a part of the vocabulary")
+        vocab_real = weight.shape[0]
+    vocab_real = int(vocab_real)
+    if weight.shape[1] != d or weight.device != dev:
+        raise ValueError("hidden and weight must have the same d_model and device")
+    if groups in (1, 2, 4, 8):
+        cols = vocab_padded // groups
+        rows = max(0, min(cols, vocab_real - rank * cols))
+        if weight.shape[0] != rows:
+            raise ValueError(f"weight must hold the {rows} projection rows of rank {rank} of {groups}")
+    temperature = _per_row(temperature, n, torch.float32, dev, "temperature")
+    target = _per_row(target, n, torch.int64, dev, "target")
+    if grad_ref is not None:
+        grad_ref = _per_row(grad_ref, n, torch.float32, dev, "grad_ref")
+        _given(dev, (ref_logp, (n,), torch.float32, "ref_logp"), (lse, (n,), torch.float32, "lse"))
+    if grad_policy is not None:
+        grad_policy = _per_row(grad_policy, n, torch.float32, dev, "grad_policy")
+        _given(dev, (policy_logp, (n,), torch.float32, "policy_logp"), (support_state, (n, 4), torch.int32, "support_state"))
+    if accumulate and (grad_weight is None or not weight_grad):
+        raise ValueError("accumulate needs a given float32 grad_weight")
+    if hidden_grad:
+        grad_hidden = _grad_out(grad_hidden, (n, d), torch.bfloat16 if groups == 1 else torch.float32, dev, "grad_hidden")
+    if weight_grad:
+        grad_weight = _grad_out(grad_weight, (weight.shape[0], d), torch.bfloat16, dev, "grad_weight", f32_only=accumulate)
+    _, lay, need = _backward_need(n, d, vocab_padded, vocab_real, groups)
+    workspace, ws_bytes = _workspace(workspace, need, dev)
+
+    def ptr(t):
+        return t.data_ptr() if t is not None else None
+
+    def out(t, wanted, add=False):
+        if not wanted:
+            return None, 0, 0
+        kind = GRAD_BF16 if t.dtype == torch.bfloat16 else GRAD_F32_ADD if add else GRAD_F32
+        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), d), kind
+
+    spare = workspace.data_ptr() if workspace is not None else None
+    gh = out(grad_hidden, hidden_grad)
+    gw = out(grad_weight, weight_grad, accumulate)
+    # a side without rows has no memory of its own: any valid address stands for it
+    if hidden_grad and n == 0:
+        gh = (None, 0, 0) if weight_grad else (spare, d, gh[2])
+    if weight_grad and weight.shape[0] == 0:
+        gw = (None, 0, 0) if gh[0] else (spare, d, gw[2])
+    _run("rlk_linear_logp_backward", dev, ptr(hidden) or spare, n, d, ldh, ptr(weight) or spare, ldw, lay, rank,
+         temperature.data_ptr(), target.data_ptr(), ptr(ref_logp) if grad_ref is not None else None,
+         ptr(lse) if grad_ref is not None else None, ptr(grad_ref), ptr(policy_logp) if grad_policy is not None else None,
+         ptr(support_state) if grad_policy is not None else None, ptr(grad_policy), *gh, *gw, spare, ws_bytes)
+    return grad_hidden if hidden_grad else None, grad_weight if weight_grad else None
+
+
+@_on_stream
+def linear_logp_backward_merge(parts, *, out=None):
+    """grad_hidden [n_rows, d_model] from the ranks' float32 parts, stacked in rank
+    order as [groups, n_rows, d_model] (rlk_linear_logp_backward_merge); equals
+    linear_logp_backward's on the whole projection, byte for byte. BF16, or what a
+    given ``out`` holds."""
+    torch = _torch()
+    if parts.dim() != 3 or parts.dtype != torch.float32 or not parts.is_cuda or not parts[0].is_contiguous():
+        raise ValueError("parts must be a float32 device tensor [groups, n_rows, d_model] with contiguous parts")
+    groups, n, d = parts.shape
+    out = _grad_out(out, (n, d), torch.bfloat16, parts.device, "out")
+    _run("rlk_linear_logp_backward_merge", parts.device, parts.data_ptr(),
+         parts.stride(0) if groups > 1 else max(parts.stride(0), n * d), groups, n, d, out.data_ptr(),
+         out.stride(0) if n > 1 else max(out.stride(0), d), GRAD_BF16 if out.dtype == torch.bfloat16 else GRAD_F32)
+    return out

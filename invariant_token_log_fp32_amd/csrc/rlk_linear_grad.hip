@@ -1,0 +1,772 @@
+// Gradient of the fused linear + token logprob on gfx950, and the C ABI
+// declared in include/rlk_linear_grad.h.
+//
+// Passages: RL-Kernel page "H100 canonical CP backward validation", Change
+// section (the training step back-propagates through the logprobs), and page
+// "Reproduce and profile the Qwen3-8B TP4/CP2 experiment" (the linear-logp
+// backend; summaries per canonical vocabulary shard in fixed order).
+//
+// With G the gradient of the BF16 logits x = bf16(h w^T):
+//   grad_hidden = G w,  grad_weight = G^T h
+// three products of the same size, none of which keeps more of x or G than a
+// few canonical vocabulary shards (an eighth of the vocabulary each).
+//
+// Kernels, in order:
+//   k_rows     per row the coefficients of G (those of rlk_logp_backward); rows
+//              without a gradient are left out, the others numbered in order
+//              (one workgroup: a running count over 1024 rows at a time)
+//   k_gather   the hidden states of the rows that remain, side by side; zeros
+//              into grad_hidden of the others
+//   k_product  <kLogits> x of some shards (bit for bit rlk_linear's), turned
+//              into G in the accumulators and stored in BF16
+//              <kHidden> G times the projection's rows, a partial sum for each
+//              shard; <kWeight> G^T times the hidden states
+//   k_combine  a row's partial sums added in the fixed order
+// The products run on the tiles of mfma_tiles.hpp, one workgroup a compute unit
+// looping over its tiles. Both operands of kWeight and the projection in kHidden
+// run across K in memory; they are transposed on the way from LDS to registers,
+// so no transposed copy is written.
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "bf16_store.hpp"
+#include "logp_device.hpp"
+#include "mfma_tiles.hpp"
+#include "rlk_linear_grad.h"
+#include "rlk_logp.h"
+
+namespace rlk_lin_grad {
+
+using rlk::u32x4;
+using namespace rlk_tiles;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kShards = rlk::kShards;
+constexpr int64_t kMaxRows = int64_t(1) << 22;
+constexpr int64_t kMaxLd = int64_t(1) << 21;
+constexpr int64_t kMaxVocab = int64_t(1) << 22;  // 256 rows of a shard's G: byte offsets fit 31 bits
+constexpr int kMaxD = 65536;
+
+// What turns x of one row into G: G_j = s_r 2^(x_j c + a_r) + [x_j >= thr] s_p 2^(x_j c + a_p),
+// g_t in the target column.
+struct alignas(16) RowCoef {
+  float c, a_r, s_r, a_p;
+  float s_p, thr, g_t;
+  int32_t target;  // global column, -1: none
+};
+
+// The row's coefficients; false when the row has no gradient.
+__device__ __forceinline__ bool row_coef(int64_t row, int64_t vocab_real, const float* __restrict__ temperature,
+                                         const int64_t* __restrict__ target, const float* __restrict__ ref_logp,
+                                         const float* __restrict__ lse, const float* __restrict__ grad_ref,
+                                         const float* __restrict__ policy_logp,
+                                         const rlk_support_state* __restrict__ support,
+                                         const float* __restrict__ grad_policy, RowCoef& R) {
+  const float gr = grad_ref ? grad_ref[row] : 0.0f;
+  const float gp = grad_policy ? grad_policy[row] : 0.0f;
+  if (gr == 0.0f && gp == 0.0f) return false;
+  const float t = temperature[row];
+  const int64_t tg = target[row];
+  const float ref = grad_ref ? ref_logp[row] : 0.0f;
+  const int status = grad_policy ? support[row].status : 1;
+  const bool invalid = !rlk::temperature_valid(t) || tg < 0 || tg >= vocab_real || ref != ref || status == -2;
+  if (!invalid && t == 0.0f) return false;
+  R = RowCoef{0.0f, 0.0f, NAN, 0.0f, 0.0f, INFINITY, NAN, -1};  // NaN in every real column
+  if (invalid || (gp != 0.0f && status == -1)) return true;
+  R.c = rlk::kLog2e / t;
+  // without a reference term its power is 0 (a finite one could overflow beside s_r = 0)
+  R.a_r = gr != 0.0f ? static_cast<float>(-static_cast<double>(lse[row]) * 1.4426950408889634) : -INFINITY;
+  R.s_r = -gr / t;
+  const float gpe = status == 1 ? gp : 0.0f;
+  R.s_p = -gpe / t;
+  float tpol = 0.0f;
+  if (gpe != 0.0f) {
+    const rlk_support_state st = support[row];
+    R.a_p = static_cast<float>(-static_cast<double>(st.lse_support) * 1.4426950408889634);
+    R.thr = st.threshold;
+    tpol = gpe * -expm1f(policy_logp[row]);
+  }
+  const float tref = gr != 0.0f ? gr * -expm1f(ref) : 0.0f;
+  R.g_t = (tref + tpol) / t;
+  R.target = static_cast<int32_t>(tg);
+  return true;
+}
+
+constexpr int kRowThreads = 1024;
+
+// coef[p], row_of[p] for the p-th row with a gradient; place[row] = p or -1; *n_act.
+__global__ __launch_bounds__(kRowThreads) void k_rows(int64_t n_rows, int64_t vocab_real,
+                                                      const float* __restrict__ temperature,
+                                                      const int64_t* __restrict__ target,
+                                                      const float* __restrict__ ref_logp,
+                                                      const float* __restrict__ lse,
+                                                      const float* __restrict__ grad_ref,
+                                                      const float* __restrict__ policy_logp,
+                                                      const rlk_support_state* __restrict__ support,
+                                                      const float* __restrict__ grad_policy,
+                                                      RowCoef* __restrict__ coef, int32_t* __restrict__ row_of,
+                                                      int32_t* __restrict__ place, int32_t* __restrict__ n_act) {
+  __shared__ int count[2][kRowThreads / 64];
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  int before = 0;
+  int buf = 0;
+  for (int64_t at = 0; at < n_rows; at += kRowThreads, buf ^= 1) {  // uniform
+    const int64_t row = at + threadIdx.x;
+    RowCoef R;
+    const bool live = row < n_rows && row_coef(row, vocab_real, temperature, target, ref_logp, lse, grad_ref,
+                                               policy_logp, support, grad_policy, R);
+    const uint64_t mask = __ballot(live);
+    if (lane == 0) count[buf][wave] = __popcll(mask);
+    __syncthreads();  // the other buffer is written only after the next one
+    int p = before + __popcll(mask & ((uint64_t(1) << lane) - 1));
+    for (int w = 0; w < kRowThreads / 64; ++w) {
+      const int c = count[buf][w];
+      if (w < wave) p += c;
+      before += c;
+    }
+    if (live) {
+      coef[p] = R;
+      row_of[p] = static_cast<int32_t>(row);
+    }
+    if (row < n_rows) place[row] = live ? p : -1;
+  }
+  if (threadIdx.x == 0) *n_act = before;
+}
+
+// One wave a row: a row with a gradient is copied to its place, another one's
+// grad_hidden (when wanted; `bytes` a row) is set to zeros.
+__global__ __launch_bounds__(256) void k_gather(const uint16_t* __restrict__ h, int64_t n_rows, int d, int64_t ldh,
+                                                const int32_t* __restrict__ place, uint16_t* __restrict__ to,
+                                                uint8_t* __restrict__ gh, int64_t gh_stride_bytes, int gh_bytes) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (row >= n_rows) return;  // uniform across the wave
+  const int p = place[row];
+  if (p >= 0) {
+    const u32x4* __restrict__ src = reinterpret_cast<const u32x4*>(h + row * ldh);
+    u32x4* __restrict__ dst = reinterpret_cast<u32x4*>(to + static_cast<int64_t>(p) * d);
+    for (int v = lane; v < d / 8; v += 64) dst[v] = src[v];
+  } else if (gh) {
+    u32x4* __restrict__ dst = reinterpret_cast<u32x4*>(gh + row * gh_stride_bytes);
+    for (int v = lane; v < gh_bytes / 16; v += 64) dst[v] = u32x4{0u, 0u, 0u, 0u};
+  }
+}
+
+enum Pass { kLogits = 0, kHidden = 1, kWeight = 2 };
+
+// Where sums of grad_hidden go: the buffers `add` in order in front of them, then
+// float32 sums of the rows with a gradient, or (row_of given) the output's rows.
+struct HiddenOut {
+  const float* add[3];  // [rows with a gradient x d]
+  int n_add;
+  int type;
+  void* out;
+  int64_t ldo;
+  int64_t shard_step;   // values between the shards of a launch
+  const int32_t* row_of;
+};
+
+struct Args {
+  const uint16_t* h;   // gathered hidden states [n_act x d]
+  const uint16_t* w;   // projection rows of the launch's first shard
+  uint16_t* g;         // G [shard of the launch][n_cap x ldg]
+  int64_t ldw;
+  int64_t ldg;
+  int64_t g_step;      // values between shards of G
+  const int32_t* n_act;
+  const RowCoef* coef;
+  int64_t col0;        // first (global) column of the launch
+  int64_t cols;        // its real columns
+  int width;           // columns of a shard
+  int shards;          // shards of the launch
+  int d;
+  HiddenOut hid;
+  void* gw;            // grad_weight at the launch's first column
+  int64_t ldgw;
+};
+
+// Shard, tile and sizes of tile u of a launch.
+struct Where {
+  int shard, m, n, cols;
+};
+
+template <Pass kPass>
+__device__ __forceinline__ int tile_count(const Args& a, int n_act) {
+  const int mt = (n_act + BM - 1) / BM;
+  const int dt = (a.d + BN - 1) / BN;
+  const int64_t full = a.cols / a.width;
+  const int rest = static_cast<int>(a.cols - full * a.width);
+  const int per = (a.width + BN - 1) / BN, last = (rest + BN - 1) / BN;
+  if (kPass == kLogits) return static_cast<int>(mt * (full * per + last));
+  if (kPass == kWeight) return static_cast<int>(dt * (full * per + last));
+  return mt * dt * a.shards;  // a shard without real columns has its (empty) sums all the same
+}
+
+template <Pass kPass>
+__device__ __forceinline__ Where where_is(const Args& a, int n_act, int u) {
+  const int mt = (n_act + BM - 1) / BM;
+  const int dt = (a.d + BN - 1) / BN;
+  const int per = (a.width + BN - 1) / BN;
+  const int each = kPass == kHidden ? mt * dt : (kPass == kLogits ? mt : dt) * per;
+  Where w;
+  w.shard = u / each;
+  const int64_t left = a.cols - static_cast<int64_t>(w.shard) * a.width;
+  w.cols = static_cast<int>(left < 0 ? 0 : (left < a.width ? left : a.width));
+  const int v = u - w.shard * each;
+  const int vt = (w.cols + BN - 1) / BN;
+  if (kPass == kLogits) tile_at(v, mt, vt, w.m, w.n);
+  if (kPass == kHidden) tile_at(v, mt, dt, w.m, w.n);
+  if (kPass == kWeight) tile_at(v, vt, dt, w.m, w.n);
+  return w;
+}
+
+template <Pass kPass>
+__device__ __forceinline__ TileIn tile_in(const Args& a, int n_act, const Where& w) {
+  TileIn t;
+  const uint16_t* wp = a.w + static_cast<int64_t>(w.shard) * a.width * a.ldw;
+  const uint16_t* gp = a.g + w.shard * a.g_step;
+  const int rows = n_act - w.m * BM < BM ? n_act - w.m * BM : BM;
+  if (kPass == kLogits) {
+    const int vr = w.cols - w.n * BN < BN ? w.cols - w.n * BN : BN;
+    t.k_end = a.d;
+    t.a = panel_rows(a.h + static_cast<int64_t>(w.m) * BM * a.d, rows, a.d, a.d);
+    t.b = panel_rows(wp + static_cast<int64_t>(w.n) * BN * a.ldw, vr, static_cast<int>(a.ldw), a.d);
+  } else if (kPass == kHidden) {
+    t.k_end = w.cols;
+    t.a = panel_rows(gp + static_cast<int64_t>(w.m) * BM * a.ldg, rows, static_cast<int>(a.ldg), w.cols);
+    t.b = panel_cols(wp + w.n * BN, a.d - w.n * BN);
+  } else {
+    t.k_end = n_act;
+    t.a = panel_cols(gp + w.m * BM, a.ldg - w.m * BM);
+    t.b = panel_cols(a.h + w.n * BN, a.d - w.n * BN);
+  }
+  return t;
+}
+
+// G of the tile from its sums: BF16 logits (rounded to nearest even), the
+// gradient formula, BF16 again. Columns past the shard's real ones hold zeros.
+__device__ __forceinline__ void store_g(const Args& a, int n_act, const Where& w, Acc& acc) {
+  const int lane = threadIdx.x & 63;
+  const int h = lane >> 5;
+  const int wave = threadIdx.x >> 6;
+  const int wm = wave & 1;
+  const int wn = wave >> 1;
+  const int cw = w.n * BN + wn * kWaveN;  // first column of the wave's part in the shard
+  const bool whole = cw + kWaveN <= w.cols;
+  const int64_t col = a.col0 + static_cast<int64_t>(w.shard) * a.width + cw;
+  uint16_t* __restrict__ g = a.g + w.shard * a.g_step;
+#pragma unroll
+  for (int i = 0; i < kMB; ++i) {
+    const int gr = w.m * BM + wm * kWaveM + i * 32 + (lane & 31);
+    const RowCoef R = a.coef[gr < n_act ? gr : 0];
+#pragma unroll
+    for (int j = 0; j < kNB; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float x = __uint_as_float(static_cast<uint32_t>(__builtin_bit_cast(
+                                            uint16_t, static_cast<__bf16>(acc[i][j][e]))) << 16);
+        acc[i][j][e] = x;
+      }
+    const bool policy = __any(R.s_p != 0.0f);
+    if (policy) {
+#pragma unroll
+      for (int j = 0; j < kNB; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float x = acc[i][j][e];
+          const float q = x >= R.thr ? __builtin_amdgcn_exp2f(fmaf(x, R.c, R.a_p)) : 0.0f;
+          acc[i][j][e] = R.s_r * __builtin_amdgcn_exp2f(fmaf(x, R.c, R.a_r)) + R.s_p * q;
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kNB; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          acc[i][j][e] = R.s_r * __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], R.c, R.a_r));
+    }
+    const int64_t lc = R.target - col;
+    const bool tin = R.target >= 0 && lc >= 0 && lc < kWaveN;
+    if (__any(tin)) {
+      const int lci = static_cast<int>(tin ? lc : 0);
+      const int kt = tin && ((lci >> 2) & 1) == h ? (lci >> 5) * 16 + ((lci >> 3) & 3) * 4 + (lci & 3) : -1;
+#pragma unroll
+      for (int k = 0; k < 64; ++k) acc[i][k >> 4][k & 15] = k == kt ? R.g_t : acc[i][k >> 4][k & 15];
+    }
+    if (!whole) {
+      const int lim = w.cols - cw - 4 * h;  // this lane's column 32 j + 8 q + e is real iff below lim
+#pragma unroll
+      for (int k = 0; k < 64; ++k)
+        acc[i][k >> 4][k & 15] = 32 * (k >> 4) + 8 * ((k >> 2) & 3) + (k & 3) < lim ? acc[i][k >> 4][k & 15] : 0.0f;
+    }
+    u32x4* dst = reinterpret_cast<u32x4*>(g + static_cast<int64_t>(gr) * a.ldg + cw + 16 * h);
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) {
+      uint32_t v[8];
+      rlk::block_words(acc[i][j], v);
+      if (gr < n_act) {  // ldg is a multiple of 256: the tile's columns all exist
+        dst[4 * j] = u32x4{v[0], v[1], v[2], v[3]};
+        dst[4 * j + 1] = u32x4{v[4], v[5], v[6], v[7]};
+      }
+    }
+  }
+}
+
+// Stores a 32 x 32 block whose row of this lane starts at out + at: 16 BF16
+// values after an exchange between the wave's halves, or float32 quads as they lie.
+template <int kType>
+__device__ __forceinline__ void store_block(const f32x16& v, bool ok, void* __restrict__ out, int64_t at, int h) {
+  if (kType == RLK_GRAD_BF16) {
+    uint32_t o[8];
+    rlk::block_words(v, o);
+    if (ok) {
+      u32x4* dst = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + at + 16 * h);
+      dst[0] = u32x4{o[0], o[1], o[2], o[3]};
+      dst[1] = u32x4{o[4], o[5], o[6], o[7]};
+    }
+  } else if (ok) {
+    f32x4* dst = reinterpret_cast<f32x4*>(static_cast<float*>(out) + at + 4 * h);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      f32x4 o = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      if (kType == RLK_GRAD_F32_ADD) o = dst[2 * q] + o;
+      dst[2 * q] = o;
+    }
+  }
+}
+
+template <int kType>
+__device__ __forceinline__ void store_hidden(const Args& a, int n_act, const Where& w, Acc& acc) {
+  const int lane = threadIdx.x & 63;
+  const int h = lane >> 5;
+  const int wave = threadIdx.x >> 6;
+  const int wm = wave & 1;
+  const int wn = wave >> 1;
+  const int cw = w.n * BN + wn * kWaveN;
+#pragma unroll
+  for (int i = 0; i < kMB; ++i) {
+    const int gr = w.m * BM + wm * kWaveM + i * 32 + (lane & 31);
+    for (int k = 0; k < a.hid.n_add; ++k) {
+      const float* from = a.hid.add[k] + static_cast<int64_t>(gr) * a.d + cw + 4 * h;
+#pragma unroll
+      for (int j = 0; j < kNB; ++j)
+        if (gr < n_act && cw + 32 * j < a.d) {  // d is a multiple of 64
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(from + 32 * j + 8 * q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] = v[e] + acc[i][j][4 * q + e];
+          }
+        }
+    }
+    const int64_t row = a.hid.row_of && gr < n_act ? a.hid.row_of[gr] : gr;
+    const int64_t at = row * a.hid.ldo + w.shard * a.hid.shard_step + cw;
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) store_block<kType>(acc[i][j], gr < n_act && cw + 32 * j < a.d, a.hid.out, at + 32 * j, h);
+  }
+}
+
+template <int kType>
+__device__ __forceinline__ void store_weight(const Args& a, const Where& w, Acc& acc) {
+  const int lane = threadIdx.x & 63;
+  const int h = lane >> 5;
+  const int wave = threadIdx.x >> 6;
+  const int wm = wave & 1;
+  const int wn = wave >> 1;
+  const int cw = w.n * BN + wn * kWaveN;
+  const int64_t first = static_cast<int64_t>(w.shard) * a.width;
+#pragma unroll
+  for (int i = 0; i < kMB; ++i) {
+    const int v = w.m * BM + wm * kWaveM + i * 32 + (lane & 31);
+    const int64_t at = (first + v) * a.ldgw + cw;
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) store_block<kType>(acc[i][j], v < w.cols && cw + 32 * j < a.d, a.gw, at + 32 * j, h);
+  }
+}
+
+template <Pass kPass, int kType>
+__global__ __launch_bounds__(kThreads) void k_product(Args a) {
+  constexpr bool kTA = kPass == kWeight;
+  constexpr bool kTB = kPass != kLogits;
+  __shared__ __attribute__((aligned(16))) uint16_t smem[kSmem];
+  const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
+  const int n_tiles = tile_count<kPass>(a, n_act);
+  const int grid = static_cast<int>(gridDim.x);
+  int u = first_tile();
+  if (u >= n_tiles) return;  // uniform across the workgroup
+  const int lda = kPass == kLogits ? a.d : static_cast<int>(a.ldg);
+  const int ldb = kPass == kWeight ? a.d : static_cast<int>(a.ldw);
+  const Offsets oa = offsets_for<kTA>(lda);
+  const Offsets ob = offsets_for<kTB>(ldb);
+  const int wm = (threadIdx.x >> 6) & 1;
+  const int wn = threadIdx.x >> 7;
+  Where w = where_is<kPass>(a, n_act, u);
+  TileIn t = tile_in<kPass>(a, n_act, w);
+  bf16x8 fa[kSteps][kMB], fb[kSteps][kNB];
+  int par = 0;
+  prefetch_tile<kTA, kTB>(t, lda, ldb, oa, ob, par, smem);
+  // stage 0 landed: all but the last 16 panel loads (stage 1) are done
+  asm volatile("s_waitcnt vmcnt(16)\n\ts_barrier" ::: "memory");
+  FragAt pa = frag_at<kTA>(smem, wm);
+  FragAt pb = frag_at<kTB>(smem + 2 * kStage, wn);
+  load_frags<kTA, kTB>(pa, pb, 0, fa[0], fb[0]);
+  load_frags<kTA, kTB>(pa, pb, 1, fa[1], fb[1]);
+  while (true) {
+    const bool more = u + grid < n_tiles;
+    Where w2 = w;
+    TileIn t2 = t;
+    if (more) {
+      w2 = where_is<kPass>(a, n_act, u + grid);
+      t2 = tile_in<kPass>(a, n_act, w2);
+    }
+    Acc acc;
+    tile_sums<kTA, kTB>(t, t2, more, lda, ldb, oa, ob, par, pa, pb, smem, acc, fa, fb);
+    if (kPass == kLogits) store_g(a, n_act, w, acc);
+    if (kPass == kHidden) store_hidden<kType>(a, n_act, w, acc);
+    if (kPass == kWeight) store_weight<kType>(a, w, acc);
+    if (!more) break;
+    const int kt_n = stages_of(t.k_end);
+    par = (par + kt_n) & 1;
+    u += grid;
+    w = w2;
+    t = t2;
+    if (kt_n == 1) {
+      // a one-stage tile could not load the next one in its loop
+      prefetch_tile<kTA, kTB>(t, lda, ldb, oa, ob, par, smem);
+      asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+      load_frags<kTA, kTB>(pa, pb, 0, fa[0], fb[0]);
+      load_frags<kTA, kTB>(pa, pb, 1, fa[1], fb[1]);
+    }
+  }
+}
+
+// The fixed sum of `count` (1, 2, 4 or 8) partial sums, neighbours first.
+template <typename F>
+__device__ __forceinline__ f32x4 tree(int count, const F& part) {
+  f32x4 v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k < count) v[k] = part(k);
+#pragma unroll
+  for (int s = 1; s < 8; s *= 2)
+#pragma unroll
+    for (int k = 0; k + s < 8; k += 2 * s)
+      if (s < count && k < count) v[k] = v[k] + v[k + s];
+  return v[0];
+}
+
+__device__ __forceinline__ void store4(void* out, int type, int64_t at, const f32x4& v) {
+  if (type == RLK_GRAD_BF16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(rlk::pack_bf16(v.x, v.y),
+                                                                            rlk::pack_bf16(v.z, v.w));
+  else
+    *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) = v;
+}
+
+// Row r of the rows with a gradient: `count` partial sums of this launch, then
+// the earlier ones.
+__global__ __launch_bounds__(256) void k_combine(const float* __restrict__ parts, int64_t step, int count,
+                                                 HiddenOut o, const int32_t* __restrict__ n_act, int d) {
+  const int n = *n_act;
+  const int64_t vecs = static_cast<int64_t>(n) * (d / 4);
+  for (int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; v < vecs;
+       v += static_cast<int64_t>(gridDim.x) * 256) {
+    f32x4 s = tree(count, [&](int k) { return *reinterpret_cast<const f32x4*>(parts + k * step + v * 4); });
+    for (int k = 0; k < o.n_add; ++k) s = *reinterpret_cast<const f32x4*>(o.add[k] + v * 4) + s;
+    const int64_t r = v / (d / 4);
+    const int64_t c = (v - r * (d / 4)) * 4;
+    store4(o.out, o.type, (o.row_of ? o.row_of[r] : r) * o.ldo + c, s);
+  }
+}
+
+__global__ __launch_bounds__(256) void k_merge(const float* __restrict__ parts, int64_t step, int count,
+                                               int64_t n_rows, int d, void* __restrict__ out, int64_t ldo, int type) {
+  const int64_t vecs = n_rows * (d / 4);
+  for (int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; v < vecs;
+       v += static_cast<int64_t>(gridDim.x) * 256) {
+    const f32x4 s = tree(count, [&](int k) { return *reinterpret_cast<const f32x4*>(parts + k * step + v * 4); });
+    const int64_t r = v / (d / 4);
+    store4(out, type, r * ldo + (v - r * (d / 4)) * 4, s);
+  }
+}
+
+// ----------------------------------------------------------------------------
+// Host side
+// ----------------------------------------------------------------------------
+
+static bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+static int32_t launched() { return hipGetLastError() == hipSuccess ? RLK_OK : RLK_ERR_HIP; }
+
+static int32_t check_shapes(int64_t n_rows, int64_t d, const rlk_vocab_layout* L) {
+  if (L == nullptr) return RLK_ERR_NULL;
+  if (n_rows < 0 || n_rows > kMaxRows) return RLK_ERR_SHAPE;
+  if (L->n_shards != kShards) return RLK_ERR_SHAPE;
+  if (L->vocab_padded < 64 || L->vocab_padded > kMaxVocab || L->vocab_padded % 64 != 0) return RLK_ERR_SHAPE;
+  if (L->vocab_real < 1 || L->vocab_real > L->vocab_padded) return RLK_ERR_SHAPE;
+  if (L->row_stride < L->vocab_padded || L->row_stride % 8 != 0) return RLK_ERR_SHAPE;
+  if (!(L->groups == 1 || L->groups == 2 || L->groups == 4 || L->groups == 8)) return RLK_ERR_GROUPS;
+  if (d < 64 || d > kMaxD || d % BK != 0) return RLK_ERR_SHAPE;
+  return RLK_OK;
+}
+
+static bool stride_ok(int64_t ld, int64_t d) { return ld >= d && ld % 8 == 0 && ld <= kMaxLd; }
+
+// The workspace and how many shards of G it holds at a time.
+struct Plan {
+  int width;        // columns of a shard
+  int local;        // the rank's shards
+  int at_once;      // shards of a launch (1, 2, 4 or 8)
+  int64_t ldg;
+  int64_t g_step;
+  int64_t part_step;
+  int n_parts;      // partial sums of grad_hidden, and of earlier launches
+  size_t n_act, coef, row_of, place, h, g, parts, bytes;
+};
+
+// G of one launch may take this much when it takes more than one shard.
+constexpr int64_t kGBudget = int64_t(640) << 20;
+
+static Plan plan_for(int64_t n_rows, int64_t d, const rlk_vocab_layout* L) {
+  Plan p;
+  p.width = static_cast<int>(L->vocab_padded / kShards);
+  p.local = kShards / L->groups;
+  p.ldg = (static_cast<int64_t>(p.width) + BN - 1) / BN * BN;
+  p.g_step = n_rows * p.ldg;
+  p.part_step = n_rows * d;
+  p.at_once = p.local;
+  while (p.at_once > 1 && p.at_once * p.g_step * 2 > kGBudget) p.at_once /= 2;
+  int levels = 0;  // sums of earlier launches that wait for their neighbours
+  for (int k = p.local / p.at_once; k > 1; k /= 2) ++levels;
+  p.n_parts = (p.at_once > 1 ? p.at_once : 0) + levels;
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  p.n_act = take(sizeof(int32_t));
+  p.coef = take(static_cast<size_t>(n_rows) * sizeof(RowCoef));
+  p.row_of = take(static_cast<size_t>(n_rows) * sizeof(int32_t));
+  p.place = take(static_cast<size_t>(n_rows) * sizeof(int32_t));
+  p.h = take(static_cast<size_t>(n_rows) * d * 2);
+  p.g = take(static_cast<size_t>(p.at_once) * p.g_step * 2);
+  p.parts = take(static_cast<size_t>(p.n_parts) * p.part_step * 4);
+  p.bytes = at;
+  return p;
+}
+
+// Bytes for n_rows rows and for any fewer: where a launch takes fewer shards from
+// some row count on, the rows just below it need more.
+static size_t bytes_for(int64_t n_rows, int64_t d, const rlk_vocab_layout* L) {
+  size_t most = plan_for(n_rows, d, L).bytes;
+  const int64_t ldg = plan_for(0, d, L).ldg;
+  for (int a = kShards / L->groups; a > 1; a /= 2) {
+    const int64_t n = kGBudget / (a * ldg * 2);  // the most rows with `a` shards at once
+    if (n < n_rows) {
+      const size_t b = plan_for(n, d, L).bytes;
+      most = b > most ? b : most;
+    }
+  }
+  return most;
+}
+
+// Compute units of the current device (cached per device), a multiple of 8.
+static int cu_count() {
+  static std::atomic<int> cache[64];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 256;
+  if (dev < 64) {
+    const int c = cache[dev].load(std::memory_order_relaxed);
+    if (c > 0) return c;
+  }
+  int n = 0;
+  if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) return 256;
+  n = (n + kXcds - 1) / kXcds * kXcds;
+  if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+static unsigned grid_for(int64_t tiles) {
+  const int64_t cap = cu_count();
+  const int64_t want = (tiles + kXcds - 1) / kXcds * kXcds;
+  return static_cast<unsigned>(want < cap ? want : cap);
+}
+
+static unsigned vec_grid(int64_t vecs) {
+  const int64_t blocks = (vecs + 255) / 256;
+  return static_cast<unsigned>(blocks < 1 ? 1 : (blocks < 16384 ? blocks : 16384));
+}
+
+}  // namespace rlk_lin_grad
+
+extern "C" {
+
+size_t rlk_linear_logp_backward_workspace_bytes(int64_t n_rows, int64_t d_model, const rlk_vocab_layout* layout) {
+  using namespace rlk_lin_grad;
+  if (check_shapes(n_rows, d_model, layout) != RLK_OK) return 0;
+  return bytes_for(n_rows, d_model, layout);
+}
+
+int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t d_model, int64_t hidden_stride,
+                                 const uint16_t* weight, int64_t weight_stride, const rlk_vocab_layout* layout,
+                                 int32_t rank, const float* temperature, const int64_t* target,
+                                 const float* ref_logp, const float* lse, const float* grad_ref,
+                                 const float* policy_logp, const rlk_support_state* support,
+                                 const float* grad_policy, void* grad_hidden, int64_t grad_hidden_stride,
+                                 int32_t grad_hidden_type, void* grad_weight, int64_t grad_weight_stride,
+                                 int32_t grad_weight_type, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream) {
+  using namespace rlk_lin_grad;
+  int32_t st = check_shapes(n_rows, d_model, layout);
+  if (st != RLK_OK) return st;
+  const int64_t d = d_model;
+  if (!stride_ok(hidden_stride, d) || !stride_ok(weight_stride, d)) return RLK_ERR_SHAPE;
+  if (rank < 0 || rank >= layout->groups) return RLK_ERR_SHAPE;
+  if (!grad_hidden && !grad_weight) return RLK_ERR_NULL;
+  if (grad_hidden && (!stride_ok(grad_hidden_stride, d) ||
+                      !(grad_hidden_type == RLK_GRAD_BF16 || grad_hidden_type == RLK_GRAD_F32)))
+    return RLK_ERR_SHAPE;
+  if (grad_weight && (!stride_ok(grad_weight_stride, d) || grad_weight_type < RLK_GRAD_BF16 ||
+                      grad_weight_type > RLK_GRAD_F32_ADD))
+    return RLK_ERR_SHAPE;
+  if (n_rows > 0) {
+    if (!hidden || !weight || !temperature || !target) return RLK_ERR_NULL;
+    if (!grad_ref && !grad_policy) return RLK_ERR_NULL;
+    if (grad_ref && (!ref_logp || !lse)) return RLK_ERR_NULL;
+    if (grad_policy && (!policy_logp || !support)) return RLK_ERR_NULL;
+    if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(temperature, 4) || !aligned(target, 8) ||
+        !aligned(ref_logp, 4) || !aligned(lse, 4) || !aligned(grad_ref, 4) || !aligned(policy_logp, 4) ||
+        !aligned(support, 4) || !aligned(grad_policy, 4))
+      return RLK_ERR_ALIGN;
+  }
+  if (!workspace) return RLK_ERR_NULL;
+  if (!aligned(workspace, 16) || !aligned(grad_hidden, 16) || !aligned(grad_weight, 16)) return RLK_ERR_ALIGN;
+  if (workspace_bytes < bytes_for(n_rows, d, layout)) return RLK_ERR_WORKSPACE;
+  const Plan p = plan_for(n_rows, d, layout);
+
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int32_t* n_act = reinterpret_cast<int32_t*>(ws + p.n_act);
+  RowCoef* coef = reinterpret_cast<RowCoef*>(ws + p.coef);
+  int32_t* row_of = reinterpret_cast<int32_t*>(ws + p.row_of);
+  int32_t* place = reinterpret_cast<int32_t*>(ws + p.place);
+  uint16_t* h = reinterpret_cast<uint16_t*>(ws + p.h);
+  float* parts = reinterpret_cast<float*>(ws + p.parts);
+  if (n_rows == 0 && (!grad_weight || grad_weight_type == RLK_GRAD_F32_ADD)) return RLK_OK;
+  k_rows<<<dim3(1), dim3(kRowThreads), 0, stream>>>(n_rows, layout->vocab_real, temperature, target, ref_logp, lse,
+                                                     grad_ref, policy_logp, support, grad_policy, coef, row_of, place,
+                                                     n_act);
+  if ((st = launched()) != RLK_OK) return st;
+  if (n_rows > 0) {
+    const int size = grad_hidden_type == RLK_GRAD_BF16 ? 2 : 4;
+    k_gather<<<dim3(static_cast<unsigned>((n_rows + 3) / 4)), dim3(256), 0, stream>>>(
+        hidden, n_rows, static_cast<int>(d), hidden_stride, place, h, static_cast<uint8_t*>(grad_hidden),
+        grad_hidden_stride * size, static_cast<int>(d) * size);
+    if ((st = launched()) != RLK_OK) return st;
+  }
+
+  const int64_t m_tiles = (n_rows + BM - 1) / BM;
+  const int64_t d_tiles = (d + BN - 1) / BN;
+  const int64_t v_tiles = (static_cast<int64_t>(p.width) + BN - 1) / BN * p.at_once;
+  const int64_t first = static_cast<int64_t>(rank) * p.local * p.width;  // the rank's first column
+  Args a{};
+  a.h = h;
+  a.g = reinterpret_cast<uint16_t*>(ws + p.g);
+  a.ldw = weight_stride;
+  a.ldg = p.ldg;
+  a.g_step = p.g_step;
+  a.n_act = n_act;
+  a.coef = coef;
+  a.width = p.width;
+  a.shards = p.at_once;
+  a.d = static_cast<int>(d);
+  a.ldgw = grad_weight_stride;
+  float* waiting = parts + static_cast<int64_t>(p.at_once > 1 ? p.at_once : 0) * p.part_step;
+  for (int s = 0; s < p.local; s += p.at_once) {
+    const int64_t c0 = static_cast<int64_t>(s) * p.width;  // columns counted from the rank's first
+    const int64_t left = layout->vocab_real - first - c0;
+    const int64_t most = static_cast<int64_t>(p.at_once) * p.width;
+    a.col0 = first + c0;
+    a.cols = left < 0 ? 0 : (left < most ? left : most);
+    a.w = n_rows > 0 && a.cols > 0 ? weight + c0 * weight_stride : weight;
+    if (m_tiles > 0 && a.cols > 0) {
+      k_product<kLogits, RLK_GRAD_BF16><<<dim3(grid_for(m_tiles * v_tiles)), dim3(kThreads), 0, stream>>>(a);
+      if ((st = launched()) != RLK_OK) return st;
+    }
+    if (grad_hidden && m_tiles > 0) {
+      // sums of whole pairs, fours, eights of launches are added as they end
+      const int k = s / p.at_once;
+      HiddenOut o{};
+      int level = 0;
+      for (; (k >> level) & 1; ++level) o.add[level] = waiting + level * p.part_step;
+      o.n_add = level;
+      if (s + p.at_once == p.local) {
+        o.out = grad_hidden;
+        o.ldo = grad_hidden_stride;
+        o.type = grad_hidden_type;
+        o.row_of = row_of;
+      } else {
+        o.out = waiting + level * p.part_step;
+        o.ldo = d;
+        o.type = RLK_GRAD_F32;
+      }
+      a.hid = o;
+      if (p.at_once > 1) {
+        a.hid = HiddenOut{};
+        a.hid.out = parts;
+        a.hid.ldo = d;
+        a.hid.type = RLK_GRAD_F32;
+        a.hid.shard_step = p.part_step;
+      }
+      const dim3 grid(grid_for(m_tiles * d_tiles * p.at_once));
+      if (a.hid.type == RLK_GRAD_BF16)
+        k_product<kHidden, RLK_GRAD_BF16><<<grid, dim3(kThreads), 0, stream>>>(a);
+      else
+        k_product<kHidden, RLK_GRAD_F32><<<grid, dim3(kThreads), 0, stream>>>(a);
+      if ((st = launched()) != RLK_OK) return st;
+      if (p.at_once > 1) {
+        k_combine<<<dim3(vec_grid(n_rows * (d / 4))), dim3(256), 0, stream>>>(parts, p.part_step, p.at_once, o, n_act,
+                                                                              static_cast<int>(d));
+        if ((st = launched()) != RLK_OK) return st;
+      }
+    }
+    if (grad_weight && a.cols > 0) {
+      const int64_t size = grad_weight_type == RLK_GRAD_BF16 ? 2 : 4;
+      a.gw = static_cast<uint8_t*>(grad_weight) + c0 * grad_weight_stride * size;
+      const dim3 grid(grid_for(v_tiles * d_tiles));
+      if (grad_weight_type == RLK_GRAD_BF16)
+        k_product<kWeight, RLK_GRAD_BF16><<<grid, dim3(kThreads), 0, stream>>>(a);
+      else if (grad_weight_type == RLK_GRAD_F32)
+        k_product<kWeight, RLK_GRAD_F32><<<grid, dim3(kThreads), 0, stream>>>(a);
+      else
+        k_product<kWeight, RLK_GRAD_F32_ADD><<<grid, dim3(kThreads), 0, stream>>>(a);
+      if ((st = launched()) != RLK_OK) return st;
+    }
+  }
+  return RLK_OK;
+}
+
+int32_t rlk_linear_logp_backward_merge(const float* parts, int64_t part_stride, int32_t groups, int64_t n_rows,
+                                       int64_t d_model, void* grad_hidden, int64_t grad_hidden_stride,
+                                       int32_t grad_hidden_type, hipStream_t stream) {
+  using namespace rlk_lin_grad;
+  if (!(groups == 1 || groups == 2 || groups == 4 || groups == 8)) return RLK_ERR_GROUPS;
+  if (n_rows < 0 || n_rows > kMaxRows || d_model < 64 || d_model > kMaxD || d_model % BK != 0) return RLK_ERR_SHAPE;
+  if (part_stride < n_rows * d_model || part_stride % 4 != 0 || part_stride > INT64_MAX / 64) return RLK_ERR_SHAPE;
+  if (!stride_ok(grad_hidden_stride, d_model) ||
+      !(grad_hidden_type == RLK_GRAD_BF16 || grad_hidden_type == RLK_GRAD_F32))
+    return RLK_ERR_SHAPE;
+  if (n_rows == 0) return RLK_OK;
+  if (!parts || !grad_hidden) return RLK_ERR_NULL;
+  if (!aligned(parts, 16) || !aligned(grad_hidden, 16)) return RLK_ERR_ALIGN;
+  k_merge<<<dim3(vec_grid(n_rows * (d_model / 4))), dim3(256), 0, stream>>>(
+      parts, part_stride, groups, n_rows, static_cast<int>(d_model), grad_hidden, grad_hidden_stride,
+      grad_hidden_type);
+  return launched();
+}
+
+}  // extern "C"
