@@ -26,6 +26,7 @@ __all__ = [
     "mx4_bytes", "mx4_quantize", "mx4_linear", "mx4_linear_workspace_bytes",
     "draft_verify", "draft_workspace_bytes",
     "linear_logp_backward", "linear_logp_backward_merge", "linear_logp_backward_workspace_bytes",
+    "layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_bytes",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -37,7 +38,7 @@ HEADER_PATHS = [HEADER_PATH] + [os.path.join(os.path.dirname(_PKG), "include", n
 # The serving operators' headers (rollout and drafting).
 SERVING_HEADER_PATHS = [os.path.join(os.path.dirname(_PKG), "include", n) for n in ("rlk_mx4.h", "rlk_draft.h")]
 # The training head's operators.
-TRAINING_HEADER_PATHS = [os.path.join(os.path.dirname(_PKG), "include", n) for n in ("rlk_linear_grad.h",)]
+TRAINING_HEADER_PATHS = [os.path.join(os.path.dirname(_PKG), "include", n) for n in ("rlk_linear_grad.h", "rlk_layer_norm.h")]
 N_SHARDS = 8
 NORM_BIN_WORDS = 264  # uint64 words of rlk_norm_bins
 NOALLOC_MAX_ROWS = 32768  # RLK_NOALLOC_MAX_ROWS
@@ -155,6 +156,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rlk_linear_logp_backward_workspace_bytes.restype = sz
     lib.rlk_linear_logp_backward_merge.argtypes = [vp, i64, i32, i64, i64, vp, i64, i32, vp]
     lib.rlk_linear_logp_backward_merge.restype = i32
+    f32 = ctypes.c_float
+    lib.rlk_layer_norm.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, i32, f32, vp, i64, vp, vp, vp]
+    lib.rlk_layer_norm.restype = i32
+    lib.rlk_layer_norm_backward.argtypes = [vp, i64, vp, i32, i64, i64, i64, vp, i32, i32, vp, vp, vp, i64, vp, vp, i32, vp, sz, vp]
+    lib.rlk_layer_norm_backward.restype = i32
+    lib.rlk_layer_norm_backward_workspace_bytes.argtypes = [i64, i64]
+    lib.rlk_layer_norm_backward_workspace_bytes.restype = sz
     _lib = lib
     return lib
 
@@ -1016,3 +1024,114 @@ def linear_logp_backward_merge(parts, *, out=None):
          parts.stride(0) if groups > 1 else max(parts.stride(0), n * d), groups, n, d, out.data_ptr(),
          out.stride(0) if n > 1 else max(out.stride(0), d), GRAD_BF16 if out.dtype == torch.bfloat16 else GRAD_F32)
     return out
+
+
+# ---------------------------------------------------------------------------
+# layer norm in front of the head, and its backward (include/rlk_layer_norm.h)
+# ---------------------------------------------------------------------------
+
+NORM_LAYER, NORM_RMS = 0, 1  # RLK_NORM_*
+TYPE_BF16, TYPE_F32 = 0, 1   # RLK_TYPE_*
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_need(n_rows, d):
+    return int(load_library().rlk_layer_norm_backward_workspace_bytes(n_rows, d))
+
+
+def layer_norm_backward_workspace_bytes(n_rows: int, d: int) -> int:
+    return _norm_need(int(n_rows), int(d))
+
+
+def _matrix(x, name, device=None, shape=None, f32_too=True):
+    """(row stride, RLK_TYPE_*) of a 2-D device tensor of BF16 (or float32) values with contiguous rows."""
+    torch = _torch()
+    types = (torch.bfloat16, torch.float32) if f32_too else (torch.bfloat16,)
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in types or x.is_cpu or x.stride(1) != 1 or \
+            (device is not None and x.device != device) or (shape is not None and x.shape != shape):
+        raise ValueError(f"{name} must be a 2-D device tensor of {' or '.join(str(t) for t in types)} values with contiguous "
+                         f"rows" + (f", of shape {tuple(shape)} on {device}" if shape is not None else ""))
+    stride = x.stride(0) if x.shape[0] > 1 else max((x.stride(0) + 7) // 8 * 8, (x.shape[1] + 7) // 8 * 8)
+    return stride, TYPE_BF16 if x.dtype is torch.bfloat16 else TYPE_F32
+
+
+def _norm_weight(weight, bias, d, device):
+    torch = _torch()
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("weight must be a bfloat16 or float32 tensor")
+    _given(device, (weight, (d,), weight.dtype, "weight"))
+    if bias is not None:
+        _given(device, (bias, (d,), weight.dtype, "bias"))
+    return TYPE_BF16 if weight.dtype is torch.bfloat16 else TYPE_F32
+
+
+@_on_stream
+def layer_norm(x, weight, bias=None, *, rms: bool = False, eps: float = 1e-6, return_stats: bool = False, out=None,
+               mean_out=None, rstd_out=None):
+    """BF16 hidden states bf16((x - mean) * rstd * weight + bias) of the rows of ``x``
+    (rlk_layer_norm); with ``rms`` the mean is left out. ``x`` is a BF16 or float32
+    [n_rows, d] device tensor, d a multiple of 8 up to 16384, row stride a
+    multiple of 8; ``weight`` and ``bias`` are BF16 or float32 [d]. ``out`` may be
+    ``x`` (BF16). Returns the hidden states, or with ``return_stats`` (hidden
+    states, mean, rstd), float32 [n_rows] (mean None with ``rms``)."""
+    torch = _torch()
+    ldx, xt = _matrix(x, "x")
+    n, d = x.shape
+    dev = x.device
+    wt = _norm_weight(weight, bias, d, dev)
+    if out is None:
+        out = torch.empty((n, d), dtype=torch.bfloat16, device=dev)
+    ldo = _matrix(out, "out", dev, x.shape, f32_too=False)[0]
+    if mean_out is not None or (return_stats and not rms):
+        mean_out = _out(mean_out, (n,), torch.float32, dev, "mean_out")
+    if rstd_out is not None or return_stats:
+        rstd_out = _out(rstd_out, (n,), torch.float32, dev, "rstd_out")
+    _run("rlk_layer_norm", dev, x.data_ptr(), xt, n, d, ldx, weight.data_ptr(), bias.data_ptr() if bias is not None else None, wt,
+         NORM_RMS if rms else NORM_LAYER, eps, out.data_ptr(), ldo, mean_out.data_ptr() if mean_out is not None else None,
+         rstd_out.data_ptr() if rstd_out is not None else None)
+    return (out, mean_out, rstd_out) if return_stats else out
+
+
+@_on_stream
+def layer_norm_backward(grad_out, x, weight, mean, rstd, *, rms: bool = False, x_grad: bool = True, weight_grad: bool = True,
+                        bias_grad: bool = False, grad_x=None, grad_weight=None, grad_bias=None, accumulate: bool = False,
+                        workspace=None):
+    """Gradients of layer_norm's inputs from that of its output, ``grad_out`` BF16
+    [n_rows, d] (rlk_layer_norm_backward). ``mean`` (None with ``rms``) and ``rstd``
+    are the forward's. Returns (grad_x of x's type, grad_weight, grad_bias float32
+    [d]), None for one that is not wanted; with ``accumulate`` the given
+    ``grad_weight`` and ``grad_bias`` are added to. Rows whose grad_out is 0 get zeros
+    and add nothing."""
+    torch = _torch()
+    f32 = torch.float32
+    lddy = _matrix(grad_out, "grad_out", f32_too=False)[0]
+    dev = grad_out.device
+    ldx, xt = _matrix(x, "x", dev, grad_out.shape)
+    n, d = x.shape
+    wt = _norm_weight(weight, None, d, dev)
+    _given(dev, (rstd, (n,), f32, "rstd"))
+    if not rms:
+        _given(dev, (mean, (n,), f32, "mean"))
+    if accumulate and ((weight_grad and grad_weight is None) or (bias_grad and grad_bias is None)):
+        raise ValueError("accumulate needs given gradients")
+    dx, lddx = None, d
+    if x_grad:
+        grad_x = torch.empty((n, d), dtype=x.dtype, device=dev) if grad_x is None else grad_x
+        lddx, gt = _matrix(grad_x, "grad_x", dev, x.shape)
+        if gt != xt:
+            raise ValueError("grad_x must have x's type")
+        dx = grad_x.data_ptr()
+    dw = db = None
+    if weight_grad:
+        grad_weight = _out(grad_weight, (d,), f32, dev, "grad_weight")
+        dw = grad_weight.data_ptr()
+    if bias_grad:
+        grad_bias = _out(grad_bias, (d,), f32, dev, "grad_bias")
+        db = grad_bias.data_ptr()
+    ws, ws_bytes = _workspace(workspace, _norm_need(n, d), dev) if weight_grad or bias_grad else (None, 0)
+    if n == 0 and dw is None and db is None:
+        return grad_x if x_grad else None, None, None
+    _run("rlk_layer_norm_backward", dev, grad_out.data_ptr(), lddy, x.data_ptr(), xt, n, d, ldx, weight.data_ptr(), wt,
+         NORM_RMS if rms else NORM_LAYER, None if rms else mean.data_ptr(), rstd.data_ptr(), dx, lddx, dw, db, int(bool(accumulate)),
+         ws.data_ptr() if ws is not None else None, ws_bytes)
+    return grad_x if x_grad else None, grad_weight if weight_grad else None, grad_bias if bias_grad else None

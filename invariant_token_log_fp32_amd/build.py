@@ -5,7 +5,8 @@ Produces ``librlk_logp.so`` next to this file from ``csrc/rlk_logp.hip``
 ``csrc/rlk_linear.hip`` (LM-head linear, fused linear + logprob),
 ``csrc/rlk_mx4.hip`` (4-bit microscaled quantisation and LM-head linear),
 ``csrc/rlk_draft.hip`` (verification of drafted tokens),
-``csrc/rlk_linear_grad.hip`` (gradient of the fused linear + logprob):
+``csrc/rlk_linear_grad.hip`` (gradient of the fused linear + logprob) and
+``csrc/rlk_layer_norm.hip`` (layer norm and its backward):
     python -m invariant_token_log_fp32_amd.build
 """
 from __future__ import annotations
@@ -18,7 +19,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", n) for n in ("rlk_logp.hip", "rlk_norm.hip", "rlk_linear.hip", "rlk_mx4.hip",
-                                              "rlk_draft.hip", "rlk_linear_grad.hip")]
+                                              "rlk_draft.hip", "rlk_linear_grad.hip", "rlk_layer_norm.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "librlk_logp.so")
 ARCH = "gfx950"

@@ -1,0 +1,289 @@
+"""GPU parity of the layer norm / RMS norm and its backward pass against the
+float64 oracle (oracle/layer_norm.py), and the properties that the header states.
+
+Tolerances, with u = 2^-24 (half a float32 step). A sum over a row is a tree at
+most 26 additions deep (4 in a thread, 6 in the wave, up to 15 over the waves, one
+division): off by at most 32 u of the mean magnitude. The mean is therefore off by
+dm = 32 u mean|x|; the variance by 32 u of itself, 4 u for its squares, and dm^2;
+the square root and the quotient add 2 u: rstd is off by 40 u + (dm rstd)^2 of
+itself (half of each, rounded up). y adds three roundings to that and dm rstd |w|
+for the mean, and 2^-8 for BF16. In the backward pass m and r are given: xhat is
+off by 2 u, each sum by 36 u of its mean magnitude, dx by the sum of both and 4
+more roundings. dweight and dbias add n terms, each off by 3 u, in chains of at
+most n / 1024 + 70 additions; n + 80 u of the sum of the magnitudes is above that.
+"""
+import numpy as np
+import pytest
+
+import datagen
+import invariant_token_log_fp32_amd as rlk
+from oracle import layer_norm as LN
+
+from gpu_util import say, to_host
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+SIZES = [(1, 8), (1, 4096), (3, 40), (5, 520), (37, 1000), (64, 1024), (7, 1032), (2, 2048), (19, 2080), (9, 4104), (4, 8192),
+         (3, 8200), (2, 16384), (1300, 64), (3000, 264)]
+
+
+def make(rng, n, d, f32, pad=0, scale=1.0, offset=0.0):
+    """(device [n, d] out of a wider buffer of NaN, its float64 values)."""
+    import torch
+    t = torch.float32 if f32 else torch.bfloat16
+    v = torch.from_numpy((rng.normal(0, 1, (n, d)) * scale + offset).astype(np.float32)).to(t)
+    buf = torch.full((n, d + pad), float("nan"), dtype=t)
+    buf[:, :d] = v
+    return buf.to("cuda:0")[:, :d], v.double().numpy()
+
+
+def vector(rng, d, f32, mean=1.0):
+    import torch
+    v = torch.from_numpy(rng.normal(mean, 0.3, d).astype(np.float32)).to(torch.float32 if f32 else torch.bfloat16)
+    return v.to("cuda:0"), v.double().numpy()
+
+
+def check(got, want, tol, what):
+    got = to_host(got.double())
+    assert got.shape == want.shape
+    off = np.abs(got - want)
+    bad = ~(off <= tol)
+    assert not bad.any(), f"{what}: off by {off[bad].max():.3e}, allowed {np.broadcast_to(tol, off.shape)[bad].min():.3e}, " \
+                          f"{bad.sum()} of {bad.size}, first at {np.argwhere(bad)[0].tolist()}"
+
+
+def check_forward(y, mean, rstd, x, w, b, eps, rms):
+    want, m, r = LN.forward(x, w, b, eps, rms)
+    dm = np.zeros(len(m)) if rms else 32 * U * np.abs(x).mean(1)
+    dr = 40 * U + (dm * r) ** 2
+    if not rms:
+        check(mean, m, dm + 1e-45, "mean")
+    check(rstd, r, dr * r, "rstd")
+    v = np.abs(want - (0 if b is None else b))
+    tol = 2.0 ** -8 * np.abs(want) + v * (dr + 4 * U)[:, None] + (dm * r)[:, None] * np.abs(w) + 2 * U * np.abs(want) + 1e-40
+    check(y, want, tol, "y")
+
+
+@pytest.mark.parametrize("n,d", SIZES)
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("x32,w32", [(False, False), (True, True), (True, False), (False, True)])
+def test_forward_matches_the_oracle(n, d, rms, x32, w32):
+    import torch
+    say(f"case: forward {n} x {d}, rms {rms}, x32 {x32}, w32 {w32}")
+    rng = np.random.default_rng(n + d)
+    x, xv = make(rng, n, d, x32, pad=8 * (n % 3), scale=np.exp2(rng.integers(-6, 7, (n, 1))), offset=0.5)
+    w, wv = vector(rng, d, w32)
+    b, bv = vector(rng, d, w32, 0.0) if n % 2 else (None, None)
+    out = torch.full((n + 1, d + 8), 7.0, dtype=torch.bfloat16, device="cuda:0")
+    y, mean, rstd = rlk.layer_norm(x, w, b, rms=rms, eps=1e-5, return_stats=True, out=out[:n, :d])
+    assert y.data_ptr() == out.data_ptr() and (mean is None) == rms
+    check_forward(y, mean, rstd, xv, wv, bv, 1e-5, rms)
+    assert bool((out[n:] == 7.0).all()) and bool((out[:, d:] == 7.0).all()), "written outside the hidden states"
+
+
+@pytest.mark.parametrize("n,d", SIZES)
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("x32,w32", [(False, False), (True, True), (True, False), (False, True)])
+def test_backward_matches_the_oracle(n, d, rms, x32, w32):
+    import torch
+    say(f"case: backward {n} x {d}, rms {rms}, x32 {x32}, w32 {w32}")
+    rng = np.random.default_rng(2 * n + d)
+    x, xv = make(rng, n, d, x32, pad=8 * (n % 3), scale=np.exp2(rng.integers(-3, 4, (n, 1))), offset=0.5)
+    w, wv = vector(rng, d, w32)
+    dy, dyv = make(rng, n, d, False, pad=16 * (n % 2))
+    _, m, r = LN.forward(xv, wv, None, 1e-5, rms)
+    mean, rstd = (torch.from_numpy(v.astype(np.float32)).to("cuda:0") for v in (m, r))
+    m, r = to_host(mean).astype(np.float64), to_host(rstd).astype(np.float64)
+    dx, dw, db = rlk.layer_norm_backward(dy, x, w, None if rms else mean, rstd, rms=rms, bias_grad=True)
+    want_dx, want_dw, want_db = LN.backward(dyv, xv, wv, m, r, rms)
+    hat = (xv - (0 if rms else m[:, None])) * r[:, None]
+    g = np.abs(dyv * wv)
+    c1 = 0 if rms else g.mean(1, keepdims=True)
+    c2 = (g * np.abs(hat)).mean(1, keepdims=True)
+    tol = r[:, None] * U * (8 * g + 44 * c1 + 48 * np.abs(hat) * c2) + (2 * U if x32 else 2.0 ** -8) * np.abs(want_dx) + 1e-40
+    check(dx, want_dx, tol, "dx")
+    assert dx.dtype == x.dtype
+    check(dw, want_dw, (n + 80) * U * np.abs(dyv * hat).sum(0) + 1e-45, "dweight")
+    check(db, want_db, (n + 80) * U * np.abs(dyv).sum(0) + 1e-45, "dbias")
+    # without the bias: the same kernel without its sums
+    dx2, dw2, none = rlk.layer_norm_backward(dy, x, w, None if rms else mean, rstd, rms=rms)
+    assert none is None and torch.equal(dx2, dx) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("rms", [False, True])
+def test_a_long_batch(rms):
+    """More rows than workgroups, a walk whose last turn is short."""
+    import torch
+    say("case: 20001 x 72")
+    rng = np.random.default_rng(8)
+    n, d = 20001, 72
+    x, xv = make(rng, n, d, False, pad=8)
+    w, wv = vector(rng, d, False)
+    b, bv = vector(rng, d, False, 0.0)
+    dy, dyv = make(rng, n, d, False)
+    y, mean, rstd = rlk.layer_norm(x, w, b, rms=rms, return_stats=True)
+    check_forward(y, mean, rstd, xv, wv, bv, 1e-6, rms)
+    _, dw, db = rlk.layer_norm_backward(dy, x, w, mean, rstd, rms=rms, bias_grad=True, x_grad=False)
+    m = 0 if rms else to_host(mean).astype(np.float64)[:, None]
+    hat = (xv - m) * to_host(rstd).astype(np.float64)[:, None]
+    check(dw, (dyv * hat).sum(0), (n / 1024 + 80) * U * np.abs(dyv * hat).sum(0), "dweight")
+    check(db, dyv.sum(0), (n / 1024 + 80) * U * np.abs(dyv).sum(0), "dbias")
+
+
+def test_offsets_and_constant_rows():
+    """A row far from zero (no cancellation in the variance), a constant row, zeros, an infinity, NaN."""
+    import torch
+    say("case: special rows")
+    d = 512
+    rng = np.random.default_rng(1)
+    v = np.zeros((6, d), np.float32)
+    v[0] = 4096 + rng.normal(0, 1, d)
+    v[1] = 3.0
+    v[3, 7] = np.inf
+    v[4, 9] = np.nan
+    v[5] = rng.normal(0, 1e-20, d)
+    x = torch.from_numpy(v).to("cuda:0")
+    w, wv = vector(rng, d, True)
+    y, mean, rstd = rlk.layer_norm(x, w, eps=1e-6, return_stats=True)
+    rows = [0, 1, 2, 5]
+    check_forward(y[rows], mean[rows], rstd[rows], v[rows].astype(np.float64), wv, None, 1e-6, False)
+    assert bool(y[3].isnan().all()) and bool(y[4].isnan().all()) and bool((y[1:3] == 0).all())
+    y0 = rlk.layer_norm(x[2:3], w, eps=0.0, rms=True)
+    assert bool(y0.isnan().all())  # 0 / 0
+
+
+def test_rows_without_a_gradient_add_nothing():
+    import torch
+    say("case: padding rows that hold NaN")
+    rng = np.random.default_rng(2)
+    n, d = 90, 1032
+    x, _ = make(rng, n, d, False)
+    w, _ = vector(rng, d, False)
+    dy, dyv = make(rng, n, d, False)
+    mean, rstd = torch.rand(n, device="cuda:0"), torch.rand(n, device="cuda:0") + 0.5
+    off = torch.from_numpy(rng.random(n) < 0.5).to("cuda:0")
+    dy[off] = 0
+    dy[off, 5] = -0.0
+    dx, dw, db = rlk.layer_norm_backward(dy, x, w, mean, rstd, bias_grad=True)
+    for v in (x, mean, rstd):
+        v[off] = float("nan")
+    dx2, dw2, db2 = rlk.layer_norm_backward(dy, x, w, mean, rstd, bias_grad=True)
+    assert torch.equal(dx[~off], dx2[~off]) and torch.equal(dw, dw2) and torch.equal(db, db2)
+    assert not dx2[off].any()
+    last = torch.zeros_like(dy)
+    last[3, 1031] = 1  # one value of one row, in the last wave
+    dx3, _, _ = rlk.layer_norm_backward(last, torch.nan_to_num(x), w, torch.zeros_like(mean), torch.ones_like(rstd))
+    assert bool(dx3[3].any()) and not torch.cat([dx3[:3], dx3[4:]]).any()
+
+
+def test_bytes_do_not_depend_on_the_batch():
+    import torch
+    say("case: batches")
+    rng = np.random.default_rng(3)
+    for n, d in ((2500, 1032), (40, 4096)):
+        x, _ = make(rng, n, d, True)
+        w, _ = vector(rng, d, False)
+        dy, _ = make(rng, n, d, False)
+        y, mean, rstd = rlk.layer_norm(x, w, return_stats=True)
+        dx = rlk.layer_norm_backward(dy, x, w, mean, rstd)[0]
+        for rows in (slice(0, 1), slice(7, 30), slice(n - 3, n)):
+            y2, m2, r2 = rlk.layer_norm(x[rows], w, return_stats=True)
+            assert torch.equal(y2, y[rows]) and torch.equal(m2, mean[rows]) and torch.equal(r2, rstd[rows])
+            assert torch.equal(rlk.layer_norm_backward(dy[rows], x[rows], w, m2, r2)[0], dx[rows])
+
+
+def test_in_place_and_accumulated():
+    import torch
+    say("case: in place, accumulate")
+    rng = np.random.default_rng(4)
+    n, d = 700, 264
+    x, _ = make(rng, n, d, False, pad=8)
+    w, _ = vector(rng, d, True)
+    dy, _ = make(rng, n, d, False)
+    y, mean, rstd = rlk.layer_norm(x, w, return_stats=True)
+    dx, dw, db = rlk.layer_norm_backward(dy, x, w, mean, rstd, bias_grad=True)
+    a, b = torch.randn(d, device="cuda:0"), torch.randn(d, device="cuda:0")
+    wa, wb = a + dw, b + db
+    dy2 = dy.clone()
+    got = rlk.layer_norm_backward(dy2, x, w, mean, rstd, bias_grad=True, grad_x=dy2, grad_weight=a, grad_bias=b, accumulate=True)
+    assert got[0] is dy2 and torch.equal(dy2, dx) and torch.equal(a, wa) and torch.equal(b, wb)
+    x2 = x.clone()
+    rlk.layer_norm_backward(dy, x2, w, mean, rstd, grad_x=x2)
+    assert torch.equal(x2, dx)
+    out = rlk.layer_norm(x, w, out=x)
+    assert out is x and torch.equal(x, y)
+
+
+def test_no_rows():
+    import torch
+    say("case: no rows")
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda:0")
+    w, stat = torch.ones(64, device="cuda:0"), torch.empty(0, device="cuda:0")
+    assert rlk.layer_norm(x, w).shape == (0, 64)
+    dw, db = torch.ones(64, device="cuda:0"), torch.ones(64, device="cuda:0")
+    rlk.layer_norm_backward(x, x, w, stat, stat, grad_weight=dw, grad_bias=db, bias_grad=True, accumulate=True)
+    assert bool((dw == 1).all()) and bool((db == 1).all())
+    rlk.layer_norm_backward(x, x, w, stat, stat, grad_weight=dw, grad_bias=db, bias_grad=True)
+    assert not dw.any() and not db.any()
+
+
+def test_against_differences():
+    import torch
+    say("case: differences")
+    rng = np.random.default_rng(5)
+    n, d = 5, 200
+    x, xv = make(rng, n, d, True)
+    w, wv = vector(rng, d, True)
+    dy, dyv = make(rng, n, d, False)
+    for rms in (False, True):
+        _, m, r = LN.forward(xv, wv, None, 1e-6, rms)
+        mean, rstd = (torch.from_numpy(v.astype(np.float32)).to("cuda:0") for v in (m, r))
+        dx, dw, _ = rlk.layer_norm_backward(dy, x, w, mean, rstd, rms=rms)
+        for _ in range(4):
+            ax, aw = rng.normal(0, 1, (n, d)), rng.normal(0, 1, d)
+            e = 1e-6
+
+            def loss(s, t):
+                return (LN.forward(xv + s * ax, wv + t * aw, None, 1e-6, rms)[0] * dyv).sum()
+
+            # float32 gradients (1e-5 of the sum of 1000 terms of about 1) and the differences' 1e-8
+            assert abs((loss(e, 0) - loss(-e, 0)) / (2 * e) - (to_host(dx.double()) * ax).sum()) < 1e-3
+            assert abs((loss(0, e) - loss(0, -e)) / (2 * e) - (to_host(dw.double()) * aw).sum()) < 1e-3
+
+
+def test_streams_and_graphs():
+    import torch
+    say("case: side streams, graphs")
+    rng = np.random.default_rng(6)
+    n, d = 333, 520
+    x, _ = make(rng, n, d, False)
+    w, _ = vector(rng, d, False)
+    dy, _ = make(rng, n, d, False)
+    y, mean, rstd = rlk.layer_norm(x, w, return_stats=True)
+    want = rlk.layer_norm_backward(dy, x, w, mean, rstd, bias_grad=True)
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    got = [rlk.layer_norm_backward(dy, x, w, mean, rstd, bias_grad=True, stream=s) for s in sides]
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))
+    outs = [torch.empty_like(v) for v in (y, mean, rstd)]
+    grads = [torch.empty_like(v) for v in want]
+    ws = torch.empty(rlk.layer_norm_backward_workspace_bytes(n, d), dtype=torch.uint8, device="cuda:0")
+    s = sides[0]
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            rlk.layer_norm(x, w, return_stats=True, out=outs[0], mean_out=outs[1], rstd_out=outs[2])
+            rlk.layer_norm_backward(dy, x, w, outs[1], outs[2], bias_grad=True, grad_x=grads[0], grad_weight=grads[1], grad_bias=grads[2],
+                                    workspace=ws)
+    for step in range(3):
+        x.copy_(torch.randn(n, d, device="cuda:0").to(torch.bfloat16))
+        y, mean, rstd = rlk.layer_norm(x, w, return_stats=True)
+        want = rlk.layer_norm_backward(dy, x, w, mean, rstd, bias_grad=True)
+        for v in outs + grads:
+            v.fill_(9)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs + grads, [y, mean, rstd, *want])), step
