@@ -1,25 +1,32 @@
-// 256 x 256 tiles of a BF16 product on the matrix cores, operands in either
-// memory order: a workgroup of 4 waves (one per SIMD), each 128 x 128 as 4 x 4
-// blocks of v_mfma_f32_32x32x16_bf16, K in 64-wide stages through
-// double-buffered LDS, panels loaded from global memory straight into LDS.
+// Tiles of a BF16 product on the matrix cores, operands in either memory order.
 //
 //   out[m][n] = sum_k A[m][k] * B[n][k],  A = a[m * lda + k] (K contiguous) or
 //   a[k * lda + m] (K across rows); the same for B.
 //
-// Operand with K contiguous: an LDS stage is 256 rows of 64 values (128
-// bytes), the 16-byte chunks of row r permuted by an XOR with swz(r); one
-// ds_read_b128 gives a lane its 8 values of a K step.
+// A workgroup of 4 waves takes a tile of BM x BN; a wave's part is cut into 32 x
+// 32 blocks of v_mfma_f32_32x32x16_bf16. K runs in slices of 32 (two steps of 16)
+// through a ring of LDS buffers; panels go from global memory straight into LDS.
 //
-// Operand with K across rows: a stage is 64 rows (k) of 256 values (512
-// bytes), read with ds_read_b64_tr_b16: 16 lanes take a 4 (k) x 16 block, and
-// lane t receives column t's 4 values; two of them are a K step's 8. The four
-// rows of a block lie 512 bytes apart, in the same banks, so the 32-byte
-// pieces of row k are permuted by an XOR with 2 (k % 4): the 32 lanes that
-// read together then cover all 64 banks once.
+// Operand with K contiguous: a slice is BM rows of 32 values (64 bytes), the
+// four 16-byte chunks of row r permuted by an XOR; one ds_read_b128 gives a lane
+// its 8 values of a step.
+//
+// Operand with K across rows: a slice is 32 rows (k) of BM values, read with
+// ds_read_b64_tr_b16: 16 lanes take a 4 (k) x 16 block, and lane t receives
+// column t's 4 values; two of them are a step's 8. The four rows of a block lie in
+// the same banks, so the chunks of row k are permuted by an XOR with a function
+// of k % 4: the 32 lanes that read together cover all 64 banks once.
+//
+// Pipeline, in slices: while slice s is multiplied, the fragments of s + 1 are
+// read into registers and the loads of s + kRing are issued, spread over the
+// slice, into the buffer that s came from (its fragments were read in s - 1, and
+// a barrier has passed). The barrier at the end of a slice waits until s + 2 has
+// landed and leaves the younger loads in flight, so a load has (kRing - 2) slices
+// to come. The ring runs on from tile to tile.
 //
 // Order of a sum: increasing k, 16 a matrix instruction, the accumulator
 // carried, the second operand's fragment (B) first: bit for bit that of
-// rlk_linear for the same values.
+// rlk_linear for the same values, whatever the tile's shape.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -32,256 +39,341 @@ namespace rlk_tiles {
 
 using rlk::f32x16;
 
-constexpr int BM = 256;
-constexpr int BN = 256;
-constexpr int BK = 64;                  // K per LDS stage
-constexpr int kThreads = 256;           // 4 waves, 2 x 2
-constexpr int kWaveM = 128;
-constexpr int kWaveN = 128;
-constexpr int kMB = kWaveM / 32;        // 32 x 32 blocks per wave
-constexpr int kNB = kWaveN / 32;
-constexpr int kSteps = BK / 16;         // K steps per stage
-constexpr int kStage = BM * BK;         // values per operand and stage
-constexpr int kSmem = 4 * kStage;       // two stages of both operands: 128 KB
+constexpr int kThreads = 256;
+constexpr int kSlice = 32;              // K of a slice: two matrix instructions deep
 constexpr int kXcds = 8;
 // Tiles of an XCD's 32 compute units: 4 x 8, so that its L2 serves each panel
 // to several of them (as in rlk_linear).
 constexpr int kGM = 4;
 constexpr int kGN = 8;
 
-static_assert(BM == BN && kSteps == 4 && kMB == 4 && kNB == 4, "the step below is written out for this shape");
-
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef f32x16 Acc[kMB][kNB];
 typedef __attribute__((address_space(3))) void* LdsPtr;
+typedef __attribute__((address_space(3))) s16x4* LdsTr;
+typedef __attribute__((address_space(3))) const bf16x8* LdsFrag;
 
 constexpr int kRsrcWord3 = 0x00020000;  // gfx9 raw buffer: 32-bit data format, no swizzle
 
-__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6); }
-
-__host__ __device__ __forceinline__ constexpr int swz(int r) { return (((r >> 1) & 3) << 1) | ((r >> 3) & 1); }
-
-// One operand of one tile: where its first stage begins and what may be read.
-struct Panel {
-  const uint16_t* p;
-  int lim;  // K contiguous: bytes from p to the end of the last row's K; K across rows: bytes of a row from p on
+// Shape of a workgroup's tile: WM x WN waves; kRing LDS buffers of a slice.
+template <int BM_, int BN_, int WM_, int WN_, int kRing_>
+struct Shape {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kRing = kRing_;
+  static constexpr int MB = BM / WM / 32, NB = BN / WN / 32;  // blocks of a wave
+  static constexpr int kLoadsA = BM / 64, kLoadsB = BN / 64;  // 1 KB loads a wave and slice
+  static constexpr int kLoads = kLoadsA + kLoadsB;
+  static constexpr int kBytesA = BM * kSlice * 2, kBytes = (BM + BN) * kSlice * 2;  // of a buffer
+  static constexpr int kLds = kRing * kBytes;
+  static_assert(WM * WN * 64 == kThreads && BM % 64 == 0 && BN % 64 == 0, "four waves, whole loads");
+  static_assert(kRing >= 3 && (kRing - 2) * kLoads < 64, "the wait counter has 6 bits");
 };
 
-// K contiguous: `rows` valid rows from p on, k values each.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6); }
+
+// Permutations of a row's 16-byte chunks. K contiguous, 4 chunks a row, 4 rows in
+// the 256 bytes of the banks: 16 rows at one chunk, and rows 0-7 at two
+// neighbouring chunks, lie in different banks.
+__device__ __forceinline__ int swz_rows(int r) { return (((r >> 2) & 1) << 1) | ((r >> 3) & 1); }
+// K across rows, `width` values a row.
+template <int kWidth>
+__device__ __forceinline__ int swz_k(int k) {
+  return kWidth >= 128 ? 4 * (k & 3) : 4 * ((k >> 1) & 1);
+}
+
+// One operand of one tile: where its first slice begins and what may be read.
+// K contiguous: lim = bytes from p to the end of the last row's K. K across rows:
+// lim = bytes of a row from p on, k_end rows.
+struct Panel {
+  const uint16_t* p;
+  int lim;
+};
+
 __device__ __forceinline__ Panel panel_rows(const uint16_t* p, int rows, int ld, int k) {
   return Panel{p, (rows > 0 && k > 0) ? ((rows - 1) * ld + k) * 2 : 0};
 }
 
-// K across rows: `cols` valid columns from p on (at least one).
-__device__ __forceinline__ Panel panel_cols(const uint16_t* p, int64_t cols) {
-  return Panel{p, static_cast<int>(cols < BN ? cols : BN) * 2};
+__device__ __forceinline__ Panel panel_cols(const uint16_t* p, int64_t cols, int most) {
+  return Panel{p, static_cast<int>(cols < most ? cols : most) * 2};
 }
 
-// Stage st of a panel as a buffer resource whose range check returns zeros for
-// rows past the operand's end, and for k past `k_end` where K runs across rows;
-// with `any` false one that loads nothing.
+// The slices of a panel one after another, as buffer resources whose range check
+// returns zeros for rows past the operand's end, and for k past k_end.
 template <bool kAcross>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t stage_of(const Panel& q, int ld, int k_end, int st, bool any) {
-  const int64_t skip = kAcross ? static_cast<int64_t>(st) * BK * ld : st * BK;
-  int rec;
-  if (kAcross) {
-    const int left = k_end - st * BK;
-    const int rows = left < BK ? left : BK;
-    rec = rows > 0 ? (rows - 1) * ld * 2 + q.lim : 0;
-  } else {
-    rec = q.lim - st * BK * 2;
-  }
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(q.p + skip), 0, any && rec > 0 ? rec : 0, kRsrcWord3);
-}
+struct Stream {
+  const uint16_t* p;
+  int rec;         // K contiguous: bytes left from p; across: of a whole slice
+  int rest, tail;  // across: rows left, bytes of the last slice when it is not whole
 
-// This lane's byte offsets into a stage for the 8 loads that fill it: loads 0
-// and 1, and the distance between loads i and i + 2. Load i of wave w fills
-// 1 KB of LDS in lane order, from 1 KB * (8 w + i) on.
-struct Offsets {
-  int at[2];
-  int step;
+  __device__ __forceinline__ void begin(const Panel& t, int ld, int k_end) {
+    p = t.p;
+    rec = kAcross ? (kSlice - 1) * ld * 2 + t.lim : t.lim;
+    rest = k_end;
+    tail = (k_end % kSlice - 1) * ld * 2 + t.lim;  // looked at only where a row is left
+  }
+  __device__ __forceinline__ void none() {
+    rec = 0;
+    rest = 0;
+  }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t next(int ld) {
+    const int now = kAcross ? (rest >= kSlice ? rec : (rest > 0 ? tail : 0)) : (rec > 0 ? rec : 0);
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, __builtin_amdgcn_readfirstlane(now), kRsrcWord3);
+    if (kAcross) {
+      p += static_cast<int64_t>(ld) * kSlice;
+      rest -= kSlice;
+    } else {
+      p += kSlice;
+      rec -= kSlice * 2;
+    }
+    return r;
+  }
 };
 
-template <bool kAcross>
-__device__ __forceinline__ Offsets offsets_for(int ld) {
+// This lane's byte offsets into a slice for its wave's loads. Load i of wave w
+// fills 1 KB of LDS in lane order, from 1 KB * (kLoads w + i) of the operand's part on.
+template <int kLoads>
+struct Offsets {
+  int at[kLoads];
+};
+
+template <bool kAcross, int kWidth>
+__device__ __forceinline__ Offsets<kWidth / 64> offsets_for(int ld) {
+  constexpr int kLoads = kWidth / 64;
   const int l = static_cast<int>(threadIdx.x) & 63;
   const int w = static_cast<int>(threadIdx.x) >> 6;
-  Offsets o;
+  Offsets<kLoads> o;
 #pragma unroll
-  for (int par = 0; par < 2; ++par) {
-    if (kAcross) {  // rows k = 16 w + 2 i and the next, 32 chunks each
-      const int k = 16 * w + 2 * par + (l >> 5);
-      const int c = (l & 31) ^ (4 * (k & 3));
-      o.at[par] = k * ld * 2 + c * 16;
-    } else {        // rows 64 w + 8 i .. + 7, 8 chunks each
-      const int r = 64 * w + 8 * par + (l >> 3);
-      const int c = (l & 7) ^ swz(r);
-      o.at[par] = r * ld * 2 + c * 16;
+  for (int i = 0; i < kLoads; ++i) {
+    if (kAcross) {  // kWidth / 8 chunks a row
+      constexpr int kChunks = kWidth / 8;
+      const int k = (w * kLoads + i) * (64 / kChunks) + l / kChunks;
+      o.at[i] = k * ld * 2 + ((l % kChunks) ^ swz_k<kWidth>(k)) * 16;
+    } else {        // 16 rows of 4 chunks
+      const int r = (w * kLoads + i) * 16 + (l >> 2);
+      o.at[i] = r * ld * 2 + ((l & 3) ^ swz_rows(r)) * 16;
     }
+    asm volatile("" : "+v"(o.at[i]));  // kept, not formed again for every load
   }
-  o.step = (kAcross ? 4 : 16) * ld * 2;
-  // without this the offsets of all loads are kept apart, and spilled
-  asm volatile("" : "+v"(o.at[0]), "+v"(o.at[1]));
   return o;
 }
 
-__device__ __forceinline__ void load_one(__amdgpu_buffer_rsrc_t r, const Offsets& o, uint16_t* __restrict__ s, int i) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsPtr)(s + (8 * wave_id() + i) * 512), 16,
-                                           o.at[i & 1] + (i >> 1) * o.step, 0, 0, 0);
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, int off, uint8_t* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsPtr)(lds), 16, off, 0, 0, 0);
 }
 
-__device__ __forceinline__ void load_stage(__amdgpu_buffer_rsrc_t r, const Offsets& o, uint16_t* __restrict__ s) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) load_one(r, o, s, i);
-}
-
-// Waits for this wave's LDS operations and panel loads, then for the workgroup.
-__device__ __forceinline__ void stage_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
-// LDS addresses of a wave's fragments in one operand's current stage: lane l
-// takes row or column 32 i + l % 32 of block i, k = 16 kk + 8 (l / 32) .. + 7 in K
-// step kk. The chunk permutations make four of them: one a K step where K is
-// contiguous (blocks lie 4 KB apart), one a block where it runs across rows (K
-// steps lie 8 KB apart).
+// LDS addresses of a wave's fragments in the buffer that is read next: lane l
+// takes row or column 32 n + l % 32 of block n, k = 16 kk + 8 (l / 32) .. + 7 in
+// step kk. The chunk permutations make one address a step where K is contiguous
+// (blocks lie 2 KB apart), one a block where it runs across rows.
+template <bool kAcross, int kBlocks>
 struct FragAt {
-  uint32_t at[4];
+  static constexpr int kCount = kAcross ? kBlocks : 2;
+  uint32_t at[kCount];
 };
 
-constexpr uint32_t kStageBytes = kStage * 2;
-
-template <bool kAcross>
-__device__ __forceinline__ FragAt frag_at(const uint16_t* stage, int w) {
+template <bool kAcross, int kBlocks, int kWidth>
+__device__ __forceinline__ FragAt<kAcross, kBlocks> frag_at(uint32_t base, int w) {
   const int lane = threadIdx.x & 63;
-  const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((LdsPtr)(const_cast<uint16_t*>(stage))));
-  FragAt f;
+  FragAt<kAcross, kBlocks> f;
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
+  for (int n = 0; n < f.kCount; ++n) {
     if (kAcross) {
-      const int q = (lane >> 2) & 3;  // row of the 4 x 16 block that this lane's address names
-      f.at[n] = base + ((8 * (lane >> 5) + q) * BN + (w * 8 + ((lane >> 4) & 1) + (n ^ q) * 2) * 16 + (lane & 3) * 4) * 2;
+      const int k = 8 * (lane >> 5) + ((lane >> 2) & 3);  // row that this lane's address names
+      const int chunk = (w * kBlocks + n) * 4 + ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1);
+      f.at[n] = base + k * kWidth * 2 + (chunk ^ swz_k<kWidth>(k)) * 16 + (lane & 1) * 8;
     } else {
-      const int fr = lane & 31;
-      f.at[n] = base + ((w * kWaveM + fr) * BK + ((2 * n + (lane >> 5)) ^ swz(fr)) * 8) * 2;
+      const int r = w * kBlocks * 32 + (lane & 31);
+      f.at[n] = base + r * kSlice * 2 + ((2 * n + (lane >> 5)) ^ swz_rows(r)) * 16;
     }
-    asm volatile("" : "+v"(f.at[n]));  // kept in registers, not formed again for every read
+    asm volatile("" : "+v"(f.at[n]));
   }
   return f;
 }
 
-typedef __attribute__((address_space(3))) s16x4* LdsTr;
-typedef __attribute__((address_space(3))) const bf16x8* LdsFrag;
-
-template <bool kAcross>
-__device__ __forceinline__ bf16x8 read_frag(const FragAt& f, int i, int kk) {
-  if (kAcross) {
-    const uint32_t p = f.at[i] + kk * 16 * BN * 2;
+template <bool kAcross, int kBlocks, int kWidth>
+__device__ __forceinline__ bf16x8 read_frag(const FragAt<kAcross, kBlocks>& f, int n, int kk) {
+  if constexpr (kAcross) {
+    const uint32_t p = f.at[n] + kk * 16 * kWidth * 2;
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(p));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(p + 4 * BN * 2));
-    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(p + 4 * kWidth * 2));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-  }
-  return *(LdsFrag)(f.at[kk] + i * 32 * BK * 2);
-}
-
-template <bool kTA, bool kTB>
-__device__ __forceinline__ void load_frags(const FragAt& pa, const FragAt& pb, int kk, bf16x8 (&a)[kMB],
-                                           bf16x8 (&b)[kNB]) {
-#pragma unroll
-  for (int i = 0; i < kMB; ++i) a[i] = read_frag<kTA>(pa, i, kk);
-#pragma unroll
-  for (int j = 0; j < kNB; ++j) b[j] = read_frag<kTB>(pb, j, kk);
-}
-
-// One K step: 16 matrix instructions, with the fragments of the step after
-// next read between them, and, in steps that carry panel loads, one of the 8
-// loads of a panel after every other instruction.
-template <bool kLoads, bool kTA, bool kTB>
-__device__ __forceinline__ void mma_step(const bf16x8 (&a)[kMB], const bf16x8 (&b)[kNB], Acc& acc, const FragAt& pa,
-                                         const FragAt& pb, int kk, bf16x8 (&na)[kMB], bf16x8 (&nb)[kNB],
-                                         __amdgpu_buffer_rsrc_t rs, const Offsets& o, uint16_t* __restrict__ ld_to) {
-#pragma unroll
-  for (int t = 0; t < kMB * kNB; ++t) {
-    const int i = t / kNB;
-    const int j = t % kNB;
-    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
-    if (t < kMB)
-      na[t] = read_frag<kTA>(pa, t, kk);
-    else if (t < kMB + kNB)
-      nb[t - kMB] = read_frag<kTB>(pb, t - kMB, kk);
-    if (kLoads && (t & 1) == 0) load_one(rs, o, ld_to, t >> 1);
-    __builtin_amdgcn_sched_barrier(0);
+  } else {
+    return *(LdsFrag)(f.at[kk] + n * 32 * kSlice * 2);
   }
 }
 
-// A tile's product: panels, the operands' strides and the end of K.
+// A tile's product: panels and the end of K.
 struct TileIn {
   Panel a, b;
   int k_end;
 };
 
-__device__ __forceinline__ int stages_of(int k_end) {
-  const int n = (k_end + BK - 1) / BK;
-  return n > 0 ? n : 1;  // an empty sum still goes through one stage, of zeros
+__device__ __forceinline__ int slices_of(int k_end) {
+  const int n = (k_end + 2 * kSlice - 1) / (2 * kSlice);
+  return 2 * (n > 0 ? n : 1);  // an empty sum still goes through two slices, of zeros
 }
 
-// Stages 0 and 1 of a tile into LDS buffers par and par ^ 1.
-template <bool kTA, bool kTB>
-__device__ __forceinline__ void prefetch_tile(const TileIn& t, int lda, int ldb, const Offsets& oa, const Offsets& ob,
-                                              int par, uint16_t* __restrict__ smem) {
-  const bool two = stages_of(t.k_end) > 1;
-  load_stage(stage_of<kTA>(t.a, lda, t.k_end, 0, true), oa, smem + par * kStage);
-  load_stage(stage_of<kTB>(t.b, ldb, t.k_end, 0, true), ob, smem + (2 + par) * kStage);
-  load_stage(stage_of<kTA>(t.a, lda, t.k_end, 1, two), oa, smem + (par ^ 1) * kStage);
-  load_stage(stage_of<kTB>(t.b, ldb, t.k_end, 1, two), ob, smem + (2 + (par ^ 1)) * kStage);
-}
+// The pipeline of a workgroup: operands' strides, where loads and fragments lie,
+// the ring's position, and the fragments in registers.
+template <class S, bool kTA, bool kTB>
+struct Tiles {
+  typedef f32x16 Acc[S::MB][S::NB];
 
-// The sums of one tile into acc. Stage kt lives in LDS buffer (kt + par) & 1,
-// which pa, pb point into on entry; stages 0 and 1 are loaded or in flight then
-// and the fragments of steps 0 and 1 in fa[0..1], fb[0..1]. Fragments are read
-// two steps ahead, so a stage's buffer is free after step 1: one barrier there,
-// after the next stage's loads have landed; steps 2 and 3 then load the stage
-// after next (in the last two stages: stages 0 and 1 of the next tile, when there
-// is one) into the freed buffer. Block (i, j): element 4 q + e of lane l is row
-// 32 i + l % 32, column 32 j + 8 q + 4 (l / 32) + e of the wave's part.
-template <bool kTA, bool kTB>
-__device__ __forceinline__ void tile_sums(const TileIn& t, const TileIn& tn, bool next, int lda, int ldb,
-                                          const Offsets& oa, const Offsets& ob, int par, FragAt& pa, FragAt& pb,
-                                          uint16_t* __restrict__ smem, Acc& acc, bf16x8 (&fa)[kSteps][kMB],
-                                          bf16x8 (&fb)[kSteps][kNB]) {
-#pragma unroll
-  for (int i = 0; i < kMB; ++i)
-#pragma unroll
-    for (int j = 0; j < kNB; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  const int kt_n = stages_of(t.k_end);
-  const bool ahead = next && kt_n >= 2;
-  for (int kt = 0; kt < kt_n; ++kt) {
-    const int cur = (kt + par) & 1;
-    uint16_t* ca = smem + cur * kStage;
-    const bool own = kt + 2 < kt_n;
-    const int st = own ? kt + 2 : kt + 2 - kt_n;
-    const Panel qa = {own ? t.a.p : tn.a.p, own ? t.a.lim : tn.a.lim};
-    const Panel qb = {own ? t.b.p : tn.b.p, own ? t.b.lim : tn.b.lim};
-    const int k_end = own ? t.k_end : tn.k_end;
-    const __amdgpu_buffer_rsrc_t ra = stage_of<kTA>(qa, lda, k_end, st, own || ahead);
-    const __amdgpu_buffer_rsrc_t rb = stage_of<kTB>(qb, ldb, k_end, st, own || ahead);
-    mma_step<false, kTA, kTB>(fa[0], fb[0], acc, pa, pb, 2, fa[2], fb[2], ra, oa, ca);
-    mma_step<false, kTA, kTB>(fa[1], fb[1], acc, pa, pb, 3, fa[3], fb[3], ra, oa, ca);
-    stage_barrier();
-    const uint32_t turn = cur ? 0u - kStageBytes : kStageBytes;
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      pa.at[n] += turn;
-      pb.at[n] += turn;
-    }
-    mma_step<true, kTA, kTB>(fa[2], fb[2], acc, pa, pb, 0, fa[0], fb[0], ra, oa, ca);
-    mma_step<true, kTA, kTB>(fa[3], fb[3], acc, pa, pb, 1, fa[1], fb[1], rb, ob, ca + 2 * kStage);
+  int lda, ldb;
+  uint8_t* ring;
+  int buf;        // byte offset of the buffer that the slice at hand came from
+  Offsets<S::kLoadsA> oa;
+  Offsets<S::kLoadsB> ob;
+  Stream<kTA> sa;  // slices still to be loaded
+  Stream<kTB> sb;
+  FragAt<kTA, S::MB> pa;  // in the buffer of the next slice
+  FragAt<kTB, S::NB> pb;
+  bf16x8 fa[4][S::MB], fb[4][S::NB];
+
+  __device__ __forceinline__ void init(uint8_t* smem, int lda_, int ldb_) {
+    lda = lda_;
+    ldb = ldb_;
+    ring = smem;
+    oa = offsets_for<kTA, S::BM>(lda);
+    ob = offsets_for<kTB, S::BN>(ldb);
   }
-}
+
+  __device__ __forceinline__ void load_a(__amdgpu_buffer_rsrc_t r, uint8_t* to, int j) {
+    load_to_lds(r, oa.at[j], to + (wave_id() * S::kLoadsA + j) * 1024);
+  }
+  __device__ __forceinline__ void load_b(__amdgpu_buffer_rsrc_t r, uint8_t* to, int j) {
+    load_to_lds(r, ob.at[j], to + S::kBytesA + (wave_id() * S::kLoadsB + j) * 1024);
+  }
+
+  __device__ __forceinline__ void streams(const TileIn& t) {
+    sa.begin(t.a, lda, t.k_end);
+    sb.begin(t.b, ldb, t.k_end);
+  }
+
+  // Fills the ring with a tile's first slices and reads the first one's fragments.
+  __device__ __forceinline__ void start(const TileIn& t) {
+    streams(t);
+#pragma unroll
+    for (int q = 0; q < S::kRing; ++q) {
+      const __amdgpu_buffer_rsrc_t ra = sa.next(lda);
+      const __amdgpu_buffer_rsrc_t rb = sb.next(ldb);
+#pragma unroll
+      for (int j = 0; j < S::kLoadsA; ++j) load_a(ra, ring + q * S::kBytes, j);
+#pragma unroll
+      for (int j = 0; j < S::kLoadsB; ++j) load_b(rb, ring + q * S::kBytes, j);
+    }
+    landed();
+    buf = 0;
+    const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((LdsPtr)(ring)));
+    pa = frag_at<kTA, S::MB, S::BM>(lds, wave_m());
+    pb = frag_at<kTB, S::NB, S::BN>(lds + S::kBytesA, wave_n());
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+      for (int i = 0; i < S::MB; ++i) fa[kk][i] = read_frag<kTA, S::MB, S::BM>(pa, i, kk);
+#pragma unroll
+      for (int j = 0; j < S::NB; ++j) fb[kk][j] = read_frag<kTB, S::NB, S::BN>(pb, j, kk);
+    }
+    turn(S::kBytes);
+  }
+
+  __device__ __forceinline__ static int wave_m() { return (threadIdx.x >> 6) % S::WM; }
+  __device__ __forceinline__ static int wave_n() { return (threadIdx.x >> 6) / S::WM; }
+
+  __device__ __forceinline__ void turn(int by) {
+#pragma unroll
+    for (int n = 0; n < pa.kCount; ++n) pa.at[n] += by;
+#pragma unroll
+    for (int n = 0; n < pb.kCount; ++n) pb.at[n] += by;
+  }
+
+  // The wave's LDS reads, the loads of the slice after next, then the workgroup.
+  __device__ __forceinline__ static void landed() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"((S::kRing - 2) * S::kLoads) : "memory");
+  }
+
+  // One slice: its matrix instructions, with the fragments of the next slice read
+  // and a slice's loads issued between them (A's in the first step, B's in the
+  // second), into the buffer `to`. sched_barrier keeps each group of instructions
+  // where it is written; without restrict every fragment read waits for all loads.
+  template <int kHalf>
+  __device__ __forceinline__ void slice(Acc& acc, uint8_t* __restrict__ to) {
+    constexpr int kSlots = S::MB * S::NB;
+    constexpr int kTurnAt = S::MB + S::NB < kSlots ? S::MB + S::NB : kSlots - 1;
+    __amdgpu_buffer_rsrc_t ra, rb;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      constexpr int kAt[2] = {2 * kHalf, 2 * kHalf + 1};
+      const int from = kAt[kk], into = kAt[kk] ^ 2;
+#pragma unroll
+      for (int t = 0; t < kSlots; ++t) {
+        const int i = t / S::NB;
+        const int j = t % S::NB;
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[from][j], fa[from][i], acc[i][j], 0, 0, 0);
+#pragma unroll
+        for (int n = t; n < S::MB + S::NB; n += kSlots) {
+          if (n < S::MB)
+            fa[into][n] = read_frag<kTA, S::MB, S::BM>(pa, n, kk);
+          else
+            fb[into][n - S::MB] = read_frag<kTB, S::NB, S::BN>(pb, n - S::MB, kk);
+        }
+        if (kk == 0) {
+          if (t == 0) ra = sa.next(lda);
+#pragma unroll
+          for (int n = 0; n < S::kLoadsA; ++n)
+            if (t == 1 + n * (kSlots - 1) / S::kLoadsA) load_a(ra, to, n);
+          if (t == kSlots - 1) rb = sb.next(ldb);
+        } else {
+#pragma unroll
+          for (int n = 0; n < S::kLoadsB; ++n)
+            if (t == n * kSlots / S::kLoadsB) load_b(rb, to, n);
+          if (t == kTurnAt) {
+            // the buffer that was read becomes the one at hand
+            buf = buf + S::kBytes == S::kLds ? 0 : buf + S::kBytes;
+            turn(buf + S::kBytes == S::kLds ? S::kBytes - S::kLds : S::kBytes);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    landed();
+  }
+
+  // The sums of tile t into acc; `tn` follows it in the ring when `next`. Element
+  // 4 q + e of block (i, j) in lane l is row 32 i + l % 32, column 32 j + 8 q +
+  // 4 (l / 32) + e of the wave's part. Returns whether the ring holds the next
+  // tile's first slices (a tile shorter than the ring ends it: start again).
+  __device__ __forceinline__ bool sums(Acc& acc, const TileIn& t, const TileIn& tn, bool next) {
+#pragma unroll
+    for (int i = 0; i < S::MB; ++i)
+#pragma unroll
+      for (int j = 0; j < S::NB; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    const int n_slices = slices_of(t.k_end);
+    const bool going = n_slices >= S::kRing;
+    int until = n_slices - S::kRing;  // slices until the loads go on to the next tile
+    for (int s = 0; s < n_slices; s += 2) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (until == half) {  // uniform
+          if (next) {
+            streams(tn);
+          } else {
+            sa.none();
+            sb.none();
+          }
+        }
+        if (half == 0)
+          slice<0>(acc, ring + buf);
+        else
+          slice<1>(acc, ring + buf);
+      }
+      until -= 2;
+    }
+    return going;
+  }
+};
 
 // Tile u of m_tiles x n_tiles, every index a tile: bands of kGN tiles along n,
 // in a band groups of kGM x kGN, in a group m first.

@@ -157,6 +157,12 @@ __global__ __launch_bounds__(256) void k_gather(const uint16_t* __restrict__ h, 
   }
 }
 
+// One workgroup a compute unit: the largest wave part that the 512 registers
+// hold (the fewest LDS reads for a multiplication), five slices in 160 KB of LDS.
+using Large = Shape<256, 256, 2, 2, 5>;
+
+constexpr int kTile = 256;  // rows of G are padded to whole tiles
+
 enum Pass { kLogits = 0, kHidden = 1, kWeight = 2 };
 
 // Where sums of grad_hidden go: the buffers `add` in order in front of them, then
@@ -195,77 +201,78 @@ struct Where {
   int shard, m, n, cols;
 };
 
-template <Pass kPass>
+template <class S, Pass kPass>
 __device__ __forceinline__ int tile_count(const Args& a, int n_act) {
-  const int mt = (n_act + BM - 1) / BM;
-  const int dt = (a.d + BN - 1) / BN;
+  const int mt = (n_act + S::BM - 1) / S::BM;
+  const int dt = (a.d + S::BN - 1) / S::BN;
   const int64_t full = a.cols / a.width;
   const int rest = static_cast<int>(a.cols - full * a.width);
-  const int per = (a.width + BN - 1) / BN, last = (rest + BN - 1) / BN;
+  const int per = (a.width + S::BN - 1) / S::BN, last = (rest + S::BN - 1) / S::BN;
   if (kPass == kLogits) return static_cast<int>(mt * (full * per + last));
   if (kPass == kWeight) return static_cast<int>(dt * (full * per + last));
   return mt * dt * a.shards;  // a shard without real columns has its (empty) sums all the same
 }
 
-template <Pass kPass>
+template <class S, Pass kPass>
 __device__ __forceinline__ Where where_is(const Args& a, int n_act, int u) {
-  const int mt = (n_act + BM - 1) / BM;
-  const int dt = (a.d + BN - 1) / BN;
-  const int per = (a.width + BN - 1) / BN;
+  const int mt = (n_act + S::BM - 1) / S::BM;
+  const int dt = (a.d + S::BN - 1) / S::BN;
+  const int per = (a.width + S::BN - 1) / S::BN;
   const int each = kPass == kHidden ? mt * dt : (kPass == kLogits ? mt : dt) * per;
   Where w;
   w.shard = u / each;
   const int64_t left = a.cols - static_cast<int64_t>(w.shard) * a.width;
   w.cols = static_cast<int>(left < 0 ? 0 : (left < a.width ? left : a.width));
   const int v = u - w.shard * each;
-  const int vt = (w.cols + BN - 1) / BN;
+  const int vt = (w.cols + S::BN - 1) / S::BN;
   if (kPass == kLogits) tile_at(v, mt, vt, w.m, w.n);
   if (kPass == kHidden) tile_at(v, mt, dt, w.m, w.n);
   if (kPass == kWeight) tile_at(v, vt, dt, w.m, w.n);
   return w;
 }
 
-template <Pass kPass>
+template <class S, Pass kPass>
 __device__ __forceinline__ TileIn tile_in(const Args& a, int n_act, const Where& w) {
   TileIn t;
   const uint16_t* wp = a.w + static_cast<int64_t>(w.shard) * a.width * a.ldw;
   const uint16_t* gp = a.g + w.shard * a.g_step;
-  const int rows = n_act - w.m * BM < BM ? n_act - w.m * BM : BM;
+  const int rows = n_act - w.m * S::BM < S::BM ? n_act - w.m * S::BM : S::BM;
   if (kPass == kLogits) {
-    const int vr = w.cols - w.n * BN < BN ? w.cols - w.n * BN : BN;
+    const int vr = w.cols - w.n * S::BN < S::BN ? w.cols - w.n * S::BN : S::BN;
     t.k_end = a.d;
-    t.a = panel_rows(a.h + static_cast<int64_t>(w.m) * BM * a.d, rows, a.d, a.d);
-    t.b = panel_rows(wp + static_cast<int64_t>(w.n) * BN * a.ldw, vr, static_cast<int>(a.ldw), a.d);
+    t.a = panel_rows(a.h + static_cast<int64_t>(w.m) * S::BM * a.d, rows, a.d, a.d);
+    t.b = panel_rows(wp + static_cast<int64_t>(w.n) * S::BN * a.ldw, vr, static_cast<int>(a.ldw), a.d);
   } else if (kPass == kHidden) {
     t.k_end = w.cols;
-    t.a = panel_rows(gp + static_cast<int64_t>(w.m) * BM * a.ldg, rows, static_cast<int>(a.ldg), w.cols);
-    t.b = panel_cols(wp + w.n * BN, a.d - w.n * BN);
+    t.a = panel_rows(gp + static_cast<int64_t>(w.m) * S::BM * a.ldg, rows, static_cast<int>(a.ldg), w.cols);
+    t.b = panel_cols(wp + w.n * S::BN, a.d - w.n * S::BN, S::BN);
   } else {
     t.k_end = n_act;
-    t.a = panel_cols(gp + w.m * BM, a.ldg - w.m * BM);
-    t.b = panel_cols(a.h + w.n * BN, a.d - w.n * BN);
+    t.a = panel_cols(gp + w.m * S::BM, a.ldg - w.m * S::BM, S::BM);
+    t.b = panel_cols(a.h + w.n * S::BN, a.d - w.n * S::BN, S::BN);
   }
   return t;
 }
 
 // G of the tile from its sums: BF16 logits (rounded to nearest even), the
 // gradient formula, BF16 again. Columns past the shard's real ones hold zeros.
-__device__ __forceinline__ void store_g(const Args& a, int n_act, const Where& w, Acc& acc) {
+template <class S>
+__device__ __forceinline__ void store_g(const Args& a, int n_act, const Where& w, f32x16 (&acc)[S::MB][S::NB]) {
   const int lane = threadIdx.x & 63;
   const int h = lane >> 5;
   const int wave = threadIdx.x >> 6;
-  const int wm = wave & 1;
-  const int wn = wave >> 1;
-  const int cw = w.n * BN + wn * kWaveN;  // first column of the wave's part in the shard
-  const bool whole = cw + kWaveN <= w.cols;
+  const int wm = wave % S::WM;
+  const int wn = wave / S::WM;
+  const int cw = w.n * S::BN + wn * (S::NB * 32);  // first column of the wave's part in the shard
+  const bool whole = cw + (S::NB * 32) <= w.cols;
   const int64_t col = a.col0 + static_cast<int64_t>(w.shard) * a.width + cw;
   uint16_t* __restrict__ g = a.g + w.shard * a.g_step;
 #pragma unroll
-  for (int i = 0; i < kMB; ++i) {
-    const int gr = w.m * BM + wm * kWaveM + i * 32 + (lane & 31);
+  for (int i = 0; i < S::MB; ++i) {
+    const int gr = w.m * S::BM + wm * (S::MB * 32) + i * 32 + (lane & 31);
     const RowCoef R = a.coef[gr < n_act ? gr : 0];
 #pragma unroll
-    for (int j = 0; j < kNB; ++j)
+    for (int j = 0; j < S::NB; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const float x = __uint_as_float(static_cast<uint32_t>(__builtin_bit_cast(
@@ -275,7 +282,7 @@ __device__ __forceinline__ void store_g(const Args& a, int n_act, const Where& w
     const bool policy = __any(R.s_p != 0.0f);
     if (policy) {
 #pragma unroll
-      for (int j = 0; j < kNB; ++j)
+      for (int j = 0; j < S::NB; ++j)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float x = acc[i][j][e];
@@ -284,28 +291,28 @@ __device__ __forceinline__ void store_g(const Args& a, int n_act, const Where& w
         }
     } else {
 #pragma unroll
-      for (int j = 0; j < kNB; ++j)
+      for (int j = 0; j < S::NB; ++j)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           acc[i][j][e] = R.s_r * __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], R.c, R.a_r));
     }
     const int64_t lc = R.target - col;
-    const bool tin = R.target >= 0 && lc >= 0 && lc < kWaveN;
+    const bool tin = R.target >= 0 && lc >= 0 && lc < (S::NB * 32);
     if (__any(tin)) {
       const int lci = static_cast<int>(tin ? lc : 0);
       const int kt = tin && ((lci >> 2) & 1) == h ? (lci >> 5) * 16 + ((lci >> 3) & 3) * 4 + (lci & 3) : -1;
 #pragma unroll
-      for (int k = 0; k < 64; ++k) acc[i][k >> 4][k & 15] = k == kt ? R.g_t : acc[i][k >> 4][k & 15];
+      for (int k = 0; k < 16 * S::NB; ++k) acc[i][k >> 4][k & 15] = k == kt ? R.g_t : acc[i][k >> 4][k & 15];
     }
     if (!whole) {
       const int lim = w.cols - cw - 4 * h;  // this lane's column 32 j + 8 q + e is real iff below lim
 #pragma unroll
-      for (int k = 0; k < 64; ++k)
+      for (int k = 0; k < 16 * S::NB; ++k)
         acc[i][k >> 4][k & 15] = 32 * (k >> 4) + 8 * ((k >> 2) & 3) + (k & 3) < lim ? acc[i][k >> 4][k & 15] : 0.0f;
     }
     u32x4* dst = reinterpret_cast<u32x4*>(g + static_cast<int64_t>(gr) * a.ldg + cw + 16 * h);
 #pragma unroll
-    for (int j = 0; j < kNB; ++j) {
+    for (int j = 0; j < S::NB; ++j) {
       uint32_t v[8];
       rlk::block_words(acc[i][j], v);
       if (gr < n_act) {  // ldg is a multiple of 256: the tile's columns all exist
@@ -339,21 +346,21 @@ __device__ __forceinline__ void store_block(const f32x16& v, bool ok, void* __re
   }
 }
 
-template <int kType>
-__device__ __forceinline__ void store_hidden(const Args& a, int n_act, const Where& w, Acc& acc) {
+template <class S, int kType>
+__device__ __forceinline__ void store_hidden(const Args& a, int n_act, const Where& w, f32x16 (&acc)[S::MB][S::NB]) {
   const int lane = threadIdx.x & 63;
   const int h = lane >> 5;
   const int wave = threadIdx.x >> 6;
-  const int wm = wave & 1;
-  const int wn = wave >> 1;
-  const int cw = w.n * BN + wn * kWaveN;
+  const int wm = wave % S::WM;
+  const int wn = wave / S::WM;
+  const int cw = w.n * S::BN + wn * (S::NB * 32);
 #pragma unroll
-  for (int i = 0; i < kMB; ++i) {
-    const int gr = w.m * BM + wm * kWaveM + i * 32 + (lane & 31);
+  for (int i = 0; i < S::MB; ++i) {
+    const int gr = w.m * S::BM + wm * (S::MB * 32) + i * 32 + (lane & 31);
     for (int k = 0; k < a.hid.n_add; ++k) {
       const float* from = a.hid.add[k] + static_cast<int64_t>(gr) * a.d + cw + 4 * h;
 #pragma unroll
-      for (int j = 0; j < kNB; ++j)
+      for (int j = 0; j < S::NB; ++j)
         if (gr < n_act && cw + 32 * j < a.d) {  // d is a multiple of 64
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -366,83 +373,63 @@ __device__ __forceinline__ void store_hidden(const Args& a, int n_act, const Whe
     const int64_t row = a.hid.row_of && gr < n_act ? a.hid.row_of[gr] : gr;
     const int64_t at = row * a.hid.ldo + w.shard * a.hid.shard_step + cw;
 #pragma unroll
-    for (int j = 0; j < kNB; ++j) store_block<kType>(acc[i][j], gr < n_act && cw + 32 * j < a.d, a.hid.out, at + 32 * j, h);
+    for (int j = 0; j < S::NB; ++j) store_block<kType>(acc[i][j], gr < n_act && cw + 32 * j < a.d, a.hid.out, at + 32 * j, h);
   }
 }
 
-template <int kType>
-__device__ __forceinline__ void store_weight(const Args& a, const Where& w, Acc& acc) {
+template <class S, int kType>
+__device__ __forceinline__ void store_weight(const Args& a, const Where& w, f32x16 (&acc)[S::MB][S::NB]) {
   const int lane = threadIdx.x & 63;
   const int h = lane >> 5;
   const int wave = threadIdx.x >> 6;
-  const int wm = wave & 1;
-  const int wn = wave >> 1;
-  const int cw = w.n * BN + wn * kWaveN;
+  const int wm = wave % S::WM;
+  const int wn = wave / S::WM;
+  const int cw = w.n * S::BN + wn * (S::NB * 32);
   const int64_t first = static_cast<int64_t>(w.shard) * a.width;
 #pragma unroll
-  for (int i = 0; i < kMB; ++i) {
-    const int v = w.m * BM + wm * kWaveM + i * 32 + (lane & 31);
+  for (int i = 0; i < S::MB; ++i) {
+    const int v = w.m * S::BM + wm * (S::MB * 32) + i * 32 + (lane & 31);
     const int64_t at = (first + v) * a.ldgw + cw;
 #pragma unroll
-    for (int j = 0; j < kNB; ++j) store_block<kType>(acc[i][j], v < w.cols && cw + 32 * j < a.d, a.gw, at + 32 * j, h);
+    for (int j = 0; j < S::NB; ++j) store_block<kType>(acc[i][j], v < w.cols && cw + 32 * j < a.d, a.gw, at + 32 * j, h);
   }
 }
 
-template <Pass kPass, int kType>
+template <class S, Pass kPass, int kType>
 __global__ __launch_bounds__(kThreads) void k_product(Args a) {
-  constexpr bool kTA = kPass == kWeight;
-  constexpr bool kTB = kPass != kLogits;
-  __shared__ __attribute__((aligned(16))) uint16_t smem[kSmem];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[S::kLds];
   const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
-  const int n_tiles = tile_count<kPass>(a, n_act);
+  const int n_tiles = tile_count<S, kPass>(a, n_act);
   const int grid = static_cast<int>(gridDim.x);
   int u = first_tile();
   if (u >= n_tiles) return;  // uniform across the workgroup
-  const int lda = kPass == kLogits ? a.d : static_cast<int>(a.ldg);
-  const int ldb = kPass == kWeight ? a.d : static_cast<int>(a.ldw);
-  const Offsets oa = offsets_for<kTA>(lda);
-  const Offsets ob = offsets_for<kTB>(ldb);
-  const int wm = (threadIdx.x >> 6) & 1;
-  const int wn = threadIdx.x >> 7;
-  Where w = where_is<kPass>(a, n_act, u);
-  TileIn t = tile_in<kPass>(a, n_act, w);
-  bf16x8 fa[kSteps][kMB], fb[kSteps][kNB];
-  int par = 0;
-  prefetch_tile<kTA, kTB>(t, lda, ldb, oa, ob, par, smem);
-  // stage 0 landed: all but the last 16 panel loads (stage 1) are done
-  asm volatile("s_waitcnt vmcnt(16)\n\ts_barrier" ::: "memory");
-  FragAt pa = frag_at<kTA>(smem, wm);
-  FragAt pb = frag_at<kTB>(smem + 2 * kStage, wn);
-  load_frags<kTA, kTB>(pa, pb, 0, fa[0], fb[0]);
-  load_frags<kTA, kTB>(pa, pb, 1, fa[1], fb[1]);
+  Where w = where_is<S, kPass>(a, n_act, u);
+  TileIn t = tile_in<S, kPass>(a, n_act, w);
+  Tiles<S, kPass == kWeight, kPass != kLogits> tiles;
+  tiles.init(smem, kPass == kLogits ? a.d : static_cast<int>(a.ldg),
+             kPass == kWeight ? a.d : static_cast<int>(a.ldw));
+  tiles.start(t);
   while (true) {
     const bool more = u + grid < n_tiles;
     Where w2 = w;
     TileIn t2 = t;
     if (more) {
-      w2 = where_is<kPass>(a, n_act, u + grid);
-      t2 = tile_in<kPass>(a, n_act, w2);
+      w2 = where_is<S, kPass>(a, n_act, u + grid);
+      t2 = tile_in<S, kPass>(a, n_act, w2);
     }
-    Acc acc;
-    tile_sums<kTA, kTB>(t, t2, more, lda, ldb, oa, ob, par, pa, pb, smem, acc, fa, fb);
-    if (kPass == kLogits) store_g(a, n_act, w, acc);
-    if (kPass == kHidden) store_hidden<kType>(a, n_act, w, acc);
-    if (kPass == kWeight) store_weight<kType>(a, w, acc);
+    f32x16 acc[S::MB][S::NB];
+    const bool going = tiles.sums(acc, t, t2, more);
+    if (kPass == kLogits) store_g<S>(a, n_act, w, acc);
+    if (kPass == kHidden) store_hidden<S, kType>(a, n_act, w, acc);
+    if (kPass == kWeight) store_weight<S, kType>(a, w, acc);
     if (!more) break;
-    const int kt_n = stages_of(t.k_end);
-    par = (par + kt_n) & 1;
     u += grid;
     w = w2;
     t = t2;
-    if (kt_n == 1) {
-      // a one-stage tile could not load the next one in its loop
-      prefetch_tile<kTA, kTB>(t, lda, ldb, oa, ob, par, smem);
-      asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-      load_frags<kTA, kTB>(pa, pb, 0, fa[0], fb[0]);
-      load_frags<kTA, kTB>(pa, pb, 1, fa[1], fb[1]);
-    }
+    if (!going) tiles.start(t);
   }
 }
+
 
 // The fixed sum of `count` (1, 2, 4 or 8) partial sums, neighbours first.
 template <typename F>
@@ -510,7 +497,7 @@ static int32_t check_shapes(int64_t n_rows, int64_t d, const rlk_vocab_layout* L
   if (L->vocab_real < 1 || L->vocab_real > L->vocab_padded) return RLK_ERR_SHAPE;
   if (L->row_stride < L->vocab_padded || L->row_stride % 8 != 0) return RLK_ERR_SHAPE;
   if (!(L->groups == 1 || L->groups == 2 || L->groups == 4 || L->groups == 8)) return RLK_ERR_GROUPS;
-  if (d < 64 || d > kMaxD || d % BK != 0) return RLK_ERR_SHAPE;
+  if (d < 64 || d > kMaxD || d % 64 != 0) return RLK_ERR_SHAPE;
   return RLK_OK;
 }
 
@@ -535,7 +522,7 @@ static Plan plan_for(int64_t n_rows, int64_t d, const rlk_vocab_layout* L) {
   Plan p;
   p.width = static_cast<int>(L->vocab_padded / kShards);
   p.local = kShards / L->groups;
-  p.ldg = (static_cast<int64_t>(p.width) + BN - 1) / BN * BN;
+  p.ldg = (static_cast<int64_t>(p.width) + kTile - 1) / kTile * kTile;
   p.g_step = n_rows * p.ldg;
   p.part_step = n_rows * d;
   p.at_once = p.local;
@@ -669,9 +656,9 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
     if ((st = launched()) != RLK_OK) return st;
   }
 
-  const int64_t m_tiles = (n_rows + BM - 1) / BM;
-  const int64_t d_tiles = (d + BN - 1) / BN;
-  const int64_t v_tiles = (static_cast<int64_t>(p.width) + BN - 1) / BN * p.at_once;
+  const int64_t m_tiles = (n_rows + Large::BM - 1) / Large::BM;
+  const int64_t d_tiles = (d + Large::BN - 1) / Large::BN;
+  const int64_t v_tiles = (static_cast<int64_t>(p.width) + Large::BN - 1) / Large::BN * p.at_once;
   const int64_t first = static_cast<int64_t>(rank) * p.local * p.width;  // the rank's first column
   Args a{};
   a.h = h;
@@ -694,7 +681,7 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
     a.cols = left < 0 ? 0 : (left < most ? left : most);
     a.w = n_rows > 0 && a.cols > 0 ? weight + c0 * weight_stride : weight;
     if (m_tiles > 0 && a.cols > 0) {
-      k_product<kLogits, RLK_GRAD_BF16><<<dim3(grid_for(m_tiles * v_tiles)), dim3(kThreads), 0, stream>>>(a);
+      k_product<Large, kLogits, RLK_GRAD_BF16><<<dim3(grid_for(m_tiles * v_tiles)), dim3(kThreads), 0, stream>>>(a);
       if ((st = launched()) != RLK_OK) return st;
     }
     if (grad_hidden && m_tiles > 0) {
@@ -724,9 +711,9 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
       }
       const dim3 grid(grid_for(m_tiles * d_tiles * p.at_once));
       if (a.hid.type == RLK_GRAD_BF16)
-        k_product<kHidden, RLK_GRAD_BF16><<<grid, dim3(kThreads), 0, stream>>>(a);
+        k_product<Large, kHidden, RLK_GRAD_BF16><<<grid, dim3(kThreads), 0, stream>>>(a);
       else
-        k_product<kHidden, RLK_GRAD_F32><<<grid, dim3(kThreads), 0, stream>>>(a);
+        k_product<Large, kHidden, RLK_GRAD_F32><<<grid, dim3(kThreads), 0, stream>>>(a);
       if ((st = launched()) != RLK_OK) return st;
       if (p.at_once > 1) {
         k_combine<<<dim3(vec_grid(n_rows * (d / 4))), dim3(256), 0, stream>>>(parts, p.part_step, p.at_once, o, n_act,
@@ -739,11 +726,11 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
       a.gw = static_cast<uint8_t*>(grad_weight) + c0 * grad_weight_stride * size;
       const dim3 grid(grid_for(v_tiles * d_tiles));
       if (grad_weight_type == RLK_GRAD_BF16)
-        k_product<kWeight, RLK_GRAD_BF16><<<grid, dim3(kThreads), 0, stream>>>(a);
+        k_product<Large, kWeight, RLK_GRAD_BF16><<<grid, dim3(kThreads), 0, stream>>>(a);
       else if (grad_weight_type == RLK_GRAD_F32)
-        k_product<kWeight, RLK_GRAD_F32><<<grid, dim3(kThreads), 0, stream>>>(a);
+        k_product<Large, kWeight, RLK_GRAD_F32><<<grid, dim3(kThreads), 0, stream>>>(a);
       else
-        k_product<kWeight, RLK_GRAD_F32_ADD><<<grid, dim3(kThreads), 0, stream>>>(a);
+        k_product<Large, kWeight, RLK_GRAD_F32_ADD><<<grid, dim3(kThreads), 0, stream>>>(a);
       if ((st = launched()) != RLK_OK) return st;
     }
   }
@@ -755,7 +742,7 @@ int32_t rlk_linear_logp_backward_merge(const float* parts, int64_t part_stride, 
                                        int32_t grad_hidden_type, hipStream_t stream) {
   using namespace rlk_lin_grad;
   if (!(groups == 1 || groups == 2 || groups == 4 || groups == 8)) return RLK_ERR_GROUPS;
-  if (n_rows < 0 || n_rows > kMaxRows || d_model < 64 || d_model > kMaxD || d_model % BK != 0) return RLK_ERR_SHAPE;
+  if (n_rows < 0 || n_rows > kMaxRows || d_model < 64 || d_model > kMaxD || d_model % 64 != 0) return RLK_ERR_SHAPE;
   if (part_stride < n_rows * d_model || part_stride % 4 != 0 || part_stride > INT64_MAX / 64) return RLK_ERR_SHAPE;
   if (!stride_ok(grad_hidden_stride, d_model) ||
       !(grad_hidden_type == RLK_GRAD_BF16 || grad_hidden_type == RLK_GRAD_F32))
