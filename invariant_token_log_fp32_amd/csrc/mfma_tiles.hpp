@@ -3,19 +3,22 @@
 //   out[m][n] = sum_k A[m][k] * B[n][k],  A = a[m * lda + k] (K contiguous) or
 //   a[k * lda + m] (K across rows); the same for B.
 //
-// A workgroup of 4 waves takes a tile of BM x BN; a wave's part is cut into 32 x
-// 32 blocks of v_mfma_f32_32x32x16_bf16. K runs in slices of 32 (two steps of 16)
-// through a ring of LDS buffers; panels go from global memory straight into LDS.
+// A workgroup of 4 waves takes a tile of BM x BN; a wave's part is cut into 16 x
+// 16 blocks of v_mfma_f32_16x16x32_bf16. K runs in slices of 32, one matrix
+// instruction deep, through a ring of LDS buffers; panels go from global memory
+// straight into LDS. Large products are bound by power here: bare 16x16x32
+// instructions on random values run at 2.06 PFLOP/s on all compute units,
+// 32x32x16, which move the accumulators twice as often, at 1.81.
 //
 // Operand with K contiguous: a slice is BM rows of 32 values (64 bytes), the
 // four 16-byte chunks of row r permuted by an XOR; one ds_read_b128 gives a lane
-// its 8 values of a step.
+// its 8 values.
 //
 // Operand with K across rows: a slice is 32 rows (k) of BM values, read with
 // ds_read_b64_tr_b16: 16 lanes take a 4 (k) x 16 block, and lane t receives
-// column t's 4 values; two of them are a step's 8. The four rows of a block lie in
-// the same banks, so the chunks of row k are permuted by an XOR with a function
-// of k % 4: the 32 lanes that read together cover all 64 banks once.
+// column t's 4 values; two of them are a lane's 8. The rows that are read together
+// lie in the same banks, so the chunks of row k are permuted by an XOR with a
+// function of k: the 32 lanes that read together cover all 64 banks once.
 //
 // Pipeline, in slices: while slice s is multiplied, the fragments of s + 1 are
 // read into registers and the loads of s + kRing are issued, spread over the
@@ -24,23 +27,24 @@
 // landed and leaves the younger loads in flight, so a load has (kRing - 2) slices
 // to come. The ring runs on from tile to tile.
 //
-// Order of a sum: increasing k, 16 a matrix instruction, the accumulator
-// carried, the second operand's fragment (B) first: bit for bit that of
-// rlk_linear for the same values, whatever the tile's shape.
+// Order of a sum: increasing k, the accumulator carried from instruction to
+// instruction, whatever the tile's shape. 16x16x32 gives the bits of two
+// 32x32x16 in a row, so the sums are bit for bit those of rlk_linear.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
+#include <utility>
 
 #include "bf16_store.hpp"
 #include "logp_device.hpp"
 
 namespace rlk_tiles {
 
-using rlk::f32x16;
-
 constexpr int kThreads = 256;
-constexpr int kSlice = 32;              // K of a slice: two matrix instructions deep
+constexpr int kSlice = 32;              // K of a slice: one matrix instruction deep
 constexpr int kXcds = 8;
 // Tiles of an XCD's 32 compute units: 4 x 8, so that its L2 serves each panel
 // to several of them (as in rlk_linear).
@@ -49,17 +53,31 @@ constexpr int kGN = 8;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* LdsPtr;
 typedef __attribute__((address_space(3))) s16x4* LdsTr;
 typedef __attribute__((address_space(3))) const bf16x8* LdsFrag;
 
 constexpr int kRsrcWord3 = 0x00020000;  // gfx9 raw buffer: 32-bit data format, no swizzle
 
+// f(0), f(1) .. f(n - 1) with constants, written out.
+template <typename F, int... kI>
+__device__ __forceinline__ void each(const F& f, std::integer_sequence<int, kI...>) {
+  (f(std::integral_constant<int, kI>()), ...);
+}
+
+// The n below `count` whose turn first + n * span / count is t, or -1.
+constexpr int at_slot(int t, int count, int first, int span) {
+  for (int n = 0; n < count; ++n)
+    if (first + n * span / count == t) return n;
+  return -1;
+}
+
 // Shape of a workgroup's tile: WM x WN waves; kRing LDS buffers of a slice.
 template <int BM_, int BN_, int WM_, int WN_, int kRing_>
 struct Shape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kRing = kRing_;
-  static constexpr int MB = BM / WM / 32, NB = BN / WN / 32;  // blocks of a wave
+  static constexpr int MB = BM / WM / 16, NB = BN / WN / 16;  // blocks of a wave
   static constexpr int kLoadsA = BM / 64, kLoadsB = BN / 64;  // 1 KB loads a wave and slice
   static constexpr int kLoads = kLoadsA + kLoadsB;
   static constexpr int kBytesA = BM * kSlice * 2, kBytes = (BM + BN) * kSlice * 2;  // of a buffer
@@ -71,13 +89,19 @@ struct Shape {
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6); }
 
 // Permutations of a row's 16-byte chunks. K contiguous, 4 chunks a row, 4 rows in
-// the 256 bytes of the banks: 16 rows at one chunk, and rows 0-7 at two
-// neighbouring chunks, lie in different banks.
-__device__ __forceinline__ int swz_rows(int r) { return (((r >> 2) & 1) << 1) | ((r >> 3) & 1); }
-// K across rows, `width` values a row.
+// the 256 bytes of the banks: a ds_read_b128 is served for lanes 0-3, 12-15 and
+// 20-27 together (then 4-11, 16-19 and 28-31, and the same of the upper half), so
+// with lane l at row l % 16, chunk l / 16, rows q = r / 4 of 0 and 3 meet rows of 1
+// and 2 one chunk on; 0, 2, 3, 1 for q = 0 .. 3 keeps them apart (counted: none).
+__device__ __forceinline__ int swz_rows(int r) {
+  const int q = (r >> 2) & 3;
+  return (((q ^ (q >> 1)) & 1) << 1) | (q >> 1);
+}
+// K across rows, kWidth values a row: rows 0-3 and 8-11 (the blocks of 32 lanes) at
+// one 32-byte piece lie in different banks.
 template <int kWidth>
 __device__ __forceinline__ int swz_k(int k) {
-  return kWidth >= 128 ? 4 * (k & 3) : 4 * ((k >> 1) & 1);
+  return (kWidth >= 128 ? 4 * (k & 3) : 4 * ((k >> 1) & 1)) + 2 * ((k >> 3) & 1);
 }
 
 // One operand of one tile: where its first slice begins and what may be read.
@@ -106,13 +130,18 @@ struct Stream {
 
   __device__ __forceinline__ void begin(const Panel& t, int ld, int k_end) {
     p = t.p;
-    rec = kAcross ? (kSlice - 1) * ld * 2 + t.lim : t.lim;
+    rec = kAcross ? (kSlice - 1) * ld * 2 + t.lim : (k_end > 0 ? t.lim : 0);
     rest = k_end;
     tail = (k_end % kSlice - 1) * ld * 2 + t.lim;  // looked at only where a row is left
   }
-  __device__ __forceinline__ void none() {
-    rec = 0;
-    rest = 0;
+  // Goes on with another panel's slices, without a branch.
+  __device__ __forceinline__ void switch_to(const Stream& o, bool now) {
+    p = now ? o.p : p;
+    rec = now ? o.rec : rec;
+    if (kAcross) {
+      rest = now ? o.rest : rest;
+      tail = now ? o.tail : tail;
+    }
   }
   __device__ __forceinline__ __amdgpu_buffer_rsrc_t next(int ld) {
     const int now = kAcross ? (rest >= kSlice ? rec : (rest > 0 ? tail : 0)) : (rec > 0 ? rec : 0);
@@ -162,12 +191,12 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, int off, u
 }
 
 // LDS addresses of a wave's fragments in the buffer that is read next: lane l
-// takes row or column 32 n + l % 32 of block n, k = 16 kk + 8 (l / 32) .. + 7 in
-// step kk. The chunk permutations make one address a step where K is contiguous
-// (blocks lie 2 KB apart), one a block where it runs across rows.
+// takes row or column 16 n + l % 16 of block n, k = 8 (l / 16) .. + 7. Where K is
+// contiguous blocks lie 1 KB apart; where it runs across rows the chunk
+// permutation makes an address for each block.
 template <bool kAcross, int kBlocks>
 struct FragAt {
-  static constexpr int kCount = kAcross ? kBlocks : 2;
+  static constexpr int kCount = kAcross ? kBlocks : 1;
   uint32_t at[kCount];
 };
 
@@ -178,12 +207,12 @@ __device__ __forceinline__ FragAt<kAcross, kBlocks> frag_at(uint32_t base, int w
 #pragma unroll
   for (int n = 0; n < f.kCount; ++n) {
     if (kAcross) {
-      const int k = 8 * (lane >> 5) + ((lane >> 2) & 3);  // row that this lane's address names
-      const int chunk = (w * kBlocks + n) * 4 + ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1);
+      const int k = 8 * (lane >> 4) + ((lane >> 2) & 3);  // row that this lane's address names
+      const int chunk = (w * kBlocks + n) * 2 + ((lane >> 1) & 1);
       f.at[n] = base + k * kWidth * 2 + (chunk ^ swz_k<kWidth>(k)) * 16 + (lane & 1) * 8;
     } else {
-      const int r = w * kBlocks * 32 + (lane & 31);
-      f.at[n] = base + r * kSlice * 2 + ((2 * n + (lane >> 5)) ^ swz_rows(r)) * 16;
+      const int r = w * kBlocks * 16 + (lane & 15);
+      f.at[n] = base + r * kSlice * 2 + ((lane >> 4) ^ swz_rows(r)) * 16;
     }
     asm volatile("" : "+v"(f.at[n]));
   }
@@ -191,15 +220,34 @@ __device__ __forceinline__ FragAt<kAcross, kBlocks> frag_at(uint32_t base, int w
 }
 
 template <bool kAcross, int kBlocks, int kWidth>
-__device__ __forceinline__ bf16x8 read_frag(const FragAt<kAcross, kBlocks>& f, int n, int kk) {
+__device__ __forceinline__ bf16x8 read_frag(const FragAt<kAcross, kBlocks>& f, int n) {
   if constexpr (kAcross) {
-    const uint32_t p = f.at[n] + kk * 16 * kWidth * 2;
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(p));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(p + 4 * kWidth * 2));
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(f.at[n]));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(f.at[n] + 4 * kWidth * 2));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   } else {
-    return *(LdsFrag)(f.at[kk] + n * 32 * kSlice * 2);
+    return *(LdsFrag)(f.at[0] + n * 16 * kSlice * 2);
   }
+}
+
+// One matrix instruction, the accumulator where it is. (Of the builtin the compiler
+// makes forms with another destination, and moves accumulators in the loop.) The
+// compiler does not know that this is one: what it needs is waited for by settle().
+__device__ __forceinline__ void mma(f32x4& c, const bf16x8& b, const bf16x8& a) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
+}
+
+// Between writes of the accumulators by ordinary instructions and mma (2 wait
+// states), and between mma and their reads (11 for this instruction): 32. The
+// accumulators pass through, so that nothing is done with them before.
+template <int kM, int kN>
+__device__ __forceinline__ void settle(f32x4 (&acc)[kM][kN]) {
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < kM; ++i)
+#pragma unroll
+    for (int j = 0; j < kN; j += 4)
+      asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]), "+a"(acc[i][j + 2]), "+a"(acc[i][j + 3]));
 }
 
 // A tile's product: panels and the end of K.
@@ -217,7 +265,7 @@ __device__ __forceinline__ int slices_of(int k_end) {
 // the ring's position, and the fragments in registers.
 template <class S, bool kTA, bool kTB>
 struct Tiles {
-  typedef f32x16 Acc[S::MB][S::NB];
+  typedef f32x4 Acc[S::MB][S::NB];
 
   int lda, ldb;
   uint8_t* ring;
@@ -228,7 +276,7 @@ struct Tiles {
   Stream<kTB> sb;
   FragAt<kTA, S::MB> pa;  // in the buffer of the next slice
   FragAt<kTB, S::NB> pb;
-  bf16x8 fa[4][S::MB], fb[4][S::NB];
+  bf16x8 fa[2][S::MB], fb[2][S::NB];  // of the slice at hand and of the next, in turn
 
   __device__ __forceinline__ void init(uint8_t* smem, int lda_, int ldb_) {
     lda = lda_;
@@ -268,12 +316,9 @@ struct Tiles {
     pa = frag_at<kTA, S::MB, S::BM>(lds, wave_m());
     pb = frag_at<kTB, S::NB, S::BN>(lds + S::kBytesA, wave_n());
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
+    for (int i = 0; i < S::MB; ++i) fa[0][i] = read_frag<kTA, S::MB, S::BM>(pa, i);
 #pragma unroll
-      for (int i = 0; i < S::MB; ++i) fa[kk][i] = read_frag<kTA, S::MB, S::BM>(pa, i, kk);
-#pragma unroll
-      for (int j = 0; j < S::NB; ++j) fb[kk][j] = read_frag<kTB, S::NB, S::BN>(pb, j, kk);
-    }
+    for (int j = 0; j < S::NB; ++j) fb[0][j] = read_frag<kTB, S::NB, S::BN>(pb, j);
     turn(S::kBytes);
   }
 
@@ -293,55 +338,43 @@ struct Tiles {
   }
 
   // One slice: its matrix instructions, with the fragments of the next slice read
-  // and a slice's loads issued between them (A's in the first step, B's in the
-  // second), into the buffer `to`. sched_barrier keeps each group of instructions
-  // where it is written; without restrict every fragment read waits for all loads.
+  // (in the first three quarters, so that none is waited for at the barrier) and a
+  // slice's loads issued between them, into the buffer `to`. sched_barrier keeps
+  // each group of instructions where it is written; without restrict every
+  // fragment read waits for all loads.
   template <int kHalf>
   __device__ __forceinline__ void slice(Acc& acc, uint8_t* __restrict__ to) {
-    constexpr int kSlots = S::MB * S::NB;
-    constexpr int kTurnAt = S::MB + S::NB < kSlots ? S::MB + S::NB : kSlots - 1;
+    constexpr int kSlots = S::MB * S::NB, kReads = S::MB + S::NB, kLater = kSlots / 2;
+    constexpr int kTurnAt = (kReads - 1) * (kSlots * 3 / 4) / kReads + 1;
+    static_assert(kReads * 4 <= kSlots * 3 && S::kLoadsA < kLater && S::kLoadsB <= kSlots - kLater, "one of each a slot");
     __amdgpu_buffer_rsrc_t ra, rb;
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      constexpr int kAt[2] = {2 * kHalf, 2 * kHalf + 1};
-      const int from = kAt[kk], into = kAt[kk] ^ 2;
-#pragma unroll
-      for (int t = 0; t < kSlots; ++t) {
-        const int i = t / S::NB;
-        const int j = t % S::NB;
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[from][j], fa[from][i], acc[i][j], 0, 0, 0);
-#pragma unroll
-        for (int n = t; n < S::MB + S::NB; n += kSlots) {
-          if (n < S::MB)
-            fa[into][n] = read_frag<kTA, S::MB, S::BM>(pa, n, kk);
-          else
-            fb[into][n - S::MB] = read_frag<kTB, S::NB, S::BN>(pb, n - S::MB, kk);
-        }
-        if (kk == 0) {
-          if (t == 0) ra = sa.next(lda);
-#pragma unroll
-          for (int n = 0; n < S::kLoadsA; ++n)
-            if (t == 1 + n * (kSlots - 1) / S::kLoadsA) load_a(ra, to, n);
-          if (t == kSlots - 1) rb = sb.next(ldb);
-        } else {
-#pragma unroll
-          for (int n = 0; n < S::kLoadsB; ++n)
-            if (t == n * kSlots / S::kLoadsB) load_b(rb, to, n);
-          if (t == kTurnAt) {
-            // the buffer that was read becomes the one at hand
-            buf = buf + S::kBytes == S::kLds ? 0 : buf + S::kBytes;
-            turn(buf + S::kBytes == S::kLds ? S::kBytes - S::kLds : S::kBytes);
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
+    each([&](auto slot) __attribute__((always_inline)) {
+      constexpr int t = slot, i = t / S::NB, j = t % S::NB;
+      mma(acc[i][j], fb[kHalf][j], fa[kHalf][i]);
+      constexpr int read = at_slot(t, kReads, 0, kSlots * 3 / 4);
+      if constexpr (read >= 0 && read < S::MB)
+        fa[kHalf ^ 1][read] = read_frag<kTA, S::MB, S::BM>(pa, read);
+      else if constexpr (read >= 0)
+        fb[kHalf ^ 1][read - S::MB] = read_frag<kTB, S::NB, S::BN>(pb, read - S::MB);
+      if constexpr (t == 0) ra = sa.next(lda);
+      constexpr int la = at_slot(t, S::kLoadsA, 1, kLater - 1);
+      if constexpr (la >= 0) load_a(ra, to, la);
+      if constexpr (t == kLater - 1) rb = sb.next(ldb);
+      constexpr int lb = at_slot(t, S::kLoadsB, kLater, kSlots - kLater);
+      if constexpr (lb >= 0) load_b(rb, to, lb);
+      if constexpr (t == kTurnAt) {
+        // the buffer that was read becomes the one at hand
+        buf = buf + S::kBytes == S::kLds ? 0 : buf + S::kBytes;
+        turn(buf + S::kBytes == S::kLds ? S::kBytes - S::kLds : S::kBytes);
       }
-    }
+      __builtin_amdgcn_sched_barrier(0);
+    }, std::make_integer_sequence<int, kSlots>());
     landed();
   }
 
-  // The sums of tile t into acc; `tn` follows it in the ring when `next`. Element
-  // 4 q + e of block (i, j) in lane l is row 32 i + l % 32, column 32 j + 8 q +
-  // 4 (l / 32) + e of the wave's part. Returns whether the ring holds the next
+  // The sums of tile t into acc; `tn` follows it in the ring when `next`. Element e
+  // of block (i, j) in lane l is row 16 i + l % 16, column 16 j + 4 (l / 16) + e of
+  // the wave's part (B's fragment is the first operand). Returns whether the ring holds the next
   // tile's first slices (a tile shorter than the ring ends it: start again).
   __device__ __forceinline__ bool sums(Acc& acc, const TileIn& t, const TileIn& tn, bool next) {
 #pragma unroll
@@ -349,28 +382,27 @@ struct Tiles {
 #pragma unroll
       for (int j = 0; j < S::NB; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
+    settle(acc);
     const int n_slices = slices_of(t.k_end);
     const bool going = n_slices >= S::kRing;
     int until = n_slices - S::kRing;  // slices until the loads go on to the next tile
-    for (int s = 0; s < n_slices; s += 2) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (until == half) {  // uniform
-          if (next) {
-            streams(tn);
-          } else {
-            sa.none();
-            sb.none();
-          }
-        }
-        if (half == 0)
-          slice<0>(acc, ring + buf);
-        else
-          slice<1>(acc, ring + buf);
-      }
+    Stream<kTA> na;
+    Stream<kTB> nb;
+    na.begin(tn.a, lda, next ? tn.k_end : 0);
+    nb.begin(tn.b, ldb, next ? tn.k_end : 0);
+    int s = 0;
+    do {  // at least once
+      sa.switch_to(na, until == 0);
+      sb.switch_to(nb, until == 0);
+      slice<0>(acc, ring + buf);
+      sa.switch_to(na, until == 1);
+      sb.switch_to(nb, until == 1);
+      slice<1>(acc, ring + buf);
       until -= 2;
-    }
+      s += 2;
+    } while (s < n_slices);
+    settle(acc);
     return going;
   }
 };

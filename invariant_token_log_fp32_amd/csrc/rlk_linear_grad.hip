@@ -43,8 +43,6 @@ namespace rlk_lin_grad {
 using rlk::u32x4;
 using namespace rlk_tiles;
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
 constexpr int kShards = rlk::kShards;
 constexpr int64_t kMaxRows = int64_t(1) << 22;
 constexpr int64_t kMaxLd = int64_t(1) << 21;
@@ -254,144 +252,144 @@ __device__ __forceinline__ TileIn tile_in(const Args& a, int n_act, const Where&
   return t;
 }
 
+// Two neighbouring blocks' 32 columns of a row in BF16: this lane's 8, at column
+// 16 (h % 2) + 8 (h / 2) of the pair, h = lane / 16 (the even quarters of the wave
+// give their part of the second block for the odd ones' part of the first).
+__device__ __forceinline__ u32x4 pair_words(const f32x4& x, const f32x4& y) {
+  const auto lo = __builtin_amdgcn_permlane16_swap(rlk::pack_bf16(x.x, x.y), rlk::pack_bf16(y.x, y.y), false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(rlk::pack_bf16(x.z, x.w), rlk::pack_bf16(y.z, y.w), false, false);
+  return u32x4{lo[0], hi[0], lo[1], hi[1]};
+}
+__device__ __forceinline__ int pair_column(int h) { return 16 * (h & 1) + 8 * (h >> 1); }
+
+// The lane, formed where it stands: what is derived from it in an epilogue is not
+// kept in registers through the tile's loop.
+__device__ __forceinline__ int lane_here() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
 // G of the tile from its sums: BF16 logits (rounded to nearest even), the
 // gradient formula, BF16 again. Columns past the shard's real ones hold zeros.
 template <class S>
-__device__ __forceinline__ void store_g(const Args& a, int n_act, const Where& w, f32x16 (&acc)[S::MB][S::NB]) {
-  const int lane = threadIdx.x & 63;
-  const int h = lane >> 5;
+__device__ __forceinline__ void store_g(const Args& a, int n_act, const Where& w, f32x4 (&acc)[S::MB][S::NB]) {
+  constexpr int kCols = S::NB * 16;       // of a wave
+  const int lane = lane_here();
+  const int h = lane >> 4;
   const int wave = threadIdx.x >> 6;
   const int wm = wave % S::WM;
   const int wn = wave / S::WM;
-  const int cw = w.n * S::BN + wn * (S::NB * 32);  // first column of the wave's part in the shard
-  const bool whole = cw + (S::NB * 32) <= w.cols;
+  const int cw = w.n * S::BN + wn * kCols;  // first column of the wave's part in the shard
+  const bool whole = cw + kCols <= w.cols;
   const int64_t col = a.col0 + static_cast<int64_t>(w.shard) * a.width + cw;
   uint16_t* __restrict__ g = a.g + w.shard * a.g_step;
 #pragma unroll
   for (int i = 0; i < S::MB; ++i) {
-    const int gr = w.m * S::BM + wm * (S::MB * 32) + i * 32 + (lane & 31);
+    const int gr = w.m * S::BM + (wm * S::MB + i) * 16 + (lane & 15);
     const RowCoef R = a.coef[gr < n_act ? gr : 0];
+    const bool policy = __any(R.s_p != 0.0f);
 #pragma unroll
     for (int j = 0; j < S::NB; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
+      for (int e = 0; e < 4; ++e) {
         const float x = __uint_as_float(static_cast<uint32_t>(__builtin_bit_cast(
                                             uint16_t, static_cast<__bf16>(acc[i][j][e]))) << 16);
-        acc[i][j][e] = x;
-      }
-    const bool policy = __any(R.s_p != 0.0f);
-    if (policy) {
-#pragma unroll
-      for (int j = 0; j < S::NB; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float x = acc[i][j][e];
+        float v = R.s_r * __builtin_amdgcn_exp2f(fmaf(x, R.c, R.a_r));
+        if (policy) {  // uniform
           const float q = x >= R.thr ? __builtin_amdgcn_exp2f(fmaf(x, R.c, R.a_p)) : 0.0f;
-          acc[i][j][e] = R.s_r * __builtin_amdgcn_exp2f(fmaf(x, R.c, R.a_r)) + R.s_p * q;
+          v = v + R.s_p * q;
         }
-    } else {
-#pragma unroll
-      for (int j = 0; j < S::NB; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          acc[i][j][e] = R.s_r * __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], R.c, R.a_r));
-    }
+        acc[i][j][e] = v;
+      }
     const int64_t lc = R.target - col;
-    const bool tin = R.target >= 0 && lc >= 0 && lc < (S::NB * 32);
+    const bool tin = R.target >= 0 && lc >= 0 && lc < kCols;
     if (__any(tin)) {
       const int lci = static_cast<int>(tin ? lc : 0);
-      const int kt = tin && ((lci >> 2) & 1) == h ? (lci >> 5) * 16 + ((lci >> 3) & 3) * 4 + (lci & 3) : -1;
+      const int kt = tin && ((lci >> 2) & 3) == h ? (lci >> 4) * 4 + (lci & 3) : -1;
 #pragma unroll
-      for (int k = 0; k < 16 * S::NB; ++k) acc[i][k >> 4][k & 15] = k == kt ? R.g_t : acc[i][k >> 4][k & 15];
+      for (int k = 0; k < 4 * S::NB; ++k) acc[i][k >> 2][k & 3] = k == kt ? R.g_t : acc[i][k >> 2][k & 3];
     }
     if (!whole) {
-      const int lim = w.cols - cw - 4 * h;  // this lane's column 32 j + 8 q + e is real iff below lim
+      const int lim = w.cols - cw - 4 * h;  // this lane's column 16 j + e is real iff below lim
 #pragma unroll
-      for (int k = 0; k < 16 * S::NB; ++k)
-        acc[i][k >> 4][k & 15] = 32 * (k >> 4) + 8 * ((k >> 2) & 3) + (k & 3) < lim ? acc[i][k >> 4][k & 15] : 0.0f;
+      for (int k = 0; k < 4 * S::NB; ++k)
+        acc[i][k >> 2][k & 3] = 16 * (k >> 2) + (k & 3) < lim ? acc[i][k >> 2][k & 3] : 0.0f;
     }
-    u32x4* dst = reinterpret_cast<u32x4*>(g + static_cast<int64_t>(gr) * a.ldg + cw + 16 * h);
+    uint16_t* dst = g + static_cast<int64_t>(gr) * a.ldg + cw + pair_column(h);
 #pragma unroll
-    for (int j = 0; j < S::NB; ++j) {
-      uint32_t v[8];
-      rlk::block_words(acc[i][j], v);
-      if (gr < n_act) {  // ldg is a multiple of 256: the tile's columns all exist
-        dst[4 * j] = u32x4{v[0], v[1], v[2], v[3]};
-        dst[4 * j + 1] = u32x4{v[4], v[5], v[6], v[7]};
-      }
+    for (int j = 0; j < S::NB; j += 2) {
+      const u32x4 v = pair_words(acc[i][j], acc[i][j + 1]);
+      if (gr < n_act) *reinterpret_cast<u32x4*>(dst + 16 * j) = v;  // ldg is a multiple of 256: the tile's columns exist
     }
   }
 }
 
-// Stores a 32 x 32 block whose row of this lane starts at out + at: 16 BF16
-// values after an exchange between the wave's halves, or float32 quads as they lie.
+// Stores blocks (i, j) and (i, j + 1), the lane's row of which starts at out + at.
 template <int kType>
-__device__ __forceinline__ void store_block(const f32x16& v, bool ok, void* __restrict__ out, int64_t at, int h) {
+__device__ __forceinline__ void store_pair(const f32x4& x, const f32x4& y, bool ok, void* __restrict__ out, int64_t at,
+                                           int h) {
   if (kType == RLK_GRAD_BF16) {
-    uint32_t o[8];
-    rlk::block_words(v, o);
-    if (ok) {
-      u32x4* dst = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + at + 16 * h);
-      dst[0] = u32x4{o[0], o[1], o[2], o[3]};
-      dst[1] = u32x4{o[4], o[5], o[6], o[7]};
-    }
+    const u32x4 v = pair_words(x, y);
+    if (ok) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + at + pair_column(h)) = v;
   } else if (ok) {
     f32x4* dst = reinterpret_cast<f32x4*>(static_cast<float*>(out) + at + 4 * h);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      f32x4 o = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-      if (kType == RLK_GRAD_F32_ADD) o = dst[2 * q] + o;
-      dst[2 * q] = o;
-    }
+    dst[0] = kType == RLK_GRAD_F32_ADD ? dst[0] + x : x;
+    dst[4] = kType == RLK_GRAD_F32_ADD ? dst[4] + y : y;
   }
 }
 
 template <class S, int kType>
-__device__ __forceinline__ void store_hidden(const Args& a, int n_act, const Where& w, f32x16 (&acc)[S::MB][S::NB]) {
-  const int lane = threadIdx.x & 63;
-  const int h = lane >> 5;
+__device__ __forceinline__ void store_hidden(const Args& a, int n_act, const Where& w, const f32x4 (&acc)[S::MB][S::NB]) {
+  const int lane = lane_here();
+  const int h = lane >> 4;
   const int wave = threadIdx.x >> 6;
   const int wm = wave % S::WM;
   const int wn = wave / S::WM;
-  const int cw = w.n * S::BN + wn * (S::NB * 32);
+  const int cw = w.n * S::BN + wn * S::NB * 16;
 #pragma unroll
   for (int i = 0; i < S::MB; ++i) {
-    const int gr = w.m * S::BM + wm * (S::MB * 32) + i * 32 + (lane & 31);
+    const int gr = w.m * S::BM + (wm * S::MB + i) * 16 + (lane & 15);
+    f32x4 v[S::NB];  // (sums added to here leave the accumulators in their registers)
+#pragma unroll
+    for (int j = 0; j < S::NB; ++j) v[j] = acc[i][j];
+    __builtin_amdgcn_sched_barrier(0);
     for (int k = 0; k < a.hid.n_add; ++k) {
       const float* from = a.hid.add[k] + static_cast<int64_t>(gr) * a.d + cw + 4 * h;
+      f32x4 o[S::NB];
 #pragma unroll
-      for (int j = 0; j < S::NB; ++j)
-        if (gr < n_act && cw + 32 * j < a.d) {  // d is a multiple of 64
+      for (int j = 0; j < S::NB; ++j) {
+        o[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (gr < n_act && cw + 16 * j < a.d) o[j] = *reinterpret_cast<const f32x4*>(from + 16 * j);  // d is a multiple of 64
+      }
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const f32x4 v = *reinterpret_cast<const f32x4*>(from + 32 * j + 8 * q);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] = v[e] + acc[i][j][4 * q + e];
-          }
-        }
+      for (int j = 0; j < S::NB; ++j) v[j] = o[j] + v[j];
     }
+    __builtin_amdgcn_sched_barrier(0);
     const int64_t row = a.hid.row_of && gr < n_act ? a.hid.row_of[gr] : gr;
     const int64_t at = row * a.hid.ldo + w.shard * a.hid.shard_step + cw;
 #pragma unroll
-    for (int j = 0; j < S::NB; ++j) store_block<kType>(acc[i][j], gr < n_act && cw + 32 * j < a.d, a.hid.out, at + 32 * j, h);
+    for (int j = 0; j < S::NB; j += 2)
+      store_pair<kType>(v[j], v[j + 1], gr < n_act && cw + 16 * j < a.d, a.hid.out, at + 16 * j, h);
   }
 }
 
 template <class S, int kType>
-__device__ __forceinline__ void store_weight(const Args& a, const Where& w, f32x16 (&acc)[S::MB][S::NB]) {
-  const int lane = threadIdx.x & 63;
-  const int h = lane >> 5;
+__device__ __forceinline__ void store_weight(const Args& a, const Where& w, const f32x4 (&acc)[S::MB][S::NB]) {
+  const int lane = lane_here();
+  const int h = lane >> 4;
   const int wave = threadIdx.x >> 6;
   const int wm = wave % S::WM;
   const int wn = wave / S::WM;
-  const int cw = w.n * S::BN + wn * (S::NB * 32);
+  const int cw = w.n * S::BN + wn * S::NB * 16;
   const int64_t first = static_cast<int64_t>(w.shard) * a.width;
 #pragma unroll
   for (int i = 0; i < S::MB; ++i) {
-    const int v = w.m * S::BM + wm * (S::MB * 32) + i * 32 + (lane & 31);
+    const int v = w.m * S::BM + (wm * S::MB + i) * 16 + (lane & 15);
     const int64_t at = (first + v) * a.ldgw + cw;
 #pragma unroll
-    for (int j = 0; j < S::NB; ++j) store_block<kType>(acc[i][j], v < w.cols && cw + 32 * j < a.d, a.gw, at + 32 * j, h);
+    for (int j = 0; j < S::NB; j += 2)
+      store_pair<kType>(acc[i][j], acc[i][j + 1], v < w.cols && cw + 16 * j < a.d, a.gw, at + 16 * j, h);
   }
 }
 
@@ -417,7 +415,7 @@ __global__ __launch_bounds__(kThreads) void k_product(Args a) {
       w2 = where_is<S, kPass>(a, n_act, u + grid);
       t2 = tile_in<S, kPass>(a, n_act, w2);
     }
-    f32x16 acc[S::MB][S::NB];
+    f32x4 acc[S::MB][S::NB];
     const bool going = tiles.sums(acc, t, t2, more);
     if (kPass == kLogits) store_g<S>(a, n_act, w, acc);
     if (kPass == kHidden) store_hidden<S, kType>(a, n_act, w, acc);
