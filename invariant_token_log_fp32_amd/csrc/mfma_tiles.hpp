@@ -73,16 +73,18 @@ constexpr int at_slot(int t, int count, int first, int span) {
   return -1;
 }
 
-// Shape of a workgroup's tile: WM x WN waves; kRing LDS buffers of a slice.
-template <int BM_, int BN_, int WM_, int WN_, int kRing_>
+// Shape of a workgroup's tile: WM x WN waves; kRing LDS buffers of a slice; kPer
+// workgroups a compute unit.
+template <int BM_, int BN_, int WM_, int WN_, int kRing_, int kPer_>
 struct Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kRing = kRing_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kRing = kRing_, kPer = kPer_;
   static constexpr int MB = BM / WM / 16, NB = BN / WN / 16;  // blocks of a wave
   static constexpr int kLoadsA = BM / 64, kLoadsB = BN / 64;  // 1 KB loads a wave and slice
   static constexpr int kLoads = kLoadsA + kLoadsB;
   static constexpr int kBytesA = BM * kSlice * 2, kBytes = (BM + BN) * kSlice * 2;  // of a buffer
   static constexpr int kLds = kRing * kBytes;
   static_assert(WM * WN * 64 == kThreads && BM % 64 == 0 && BN % 64 == 0, "four waves, whole loads");
+  static_assert(NB % 2 == 0 && kLds * kPer <= 160 * 1024, "blocks are stored in pairs; the LDS of a compute unit");
   static_assert(kRing >= 3 && (kRing - 2) * kLoads < 64, "the wait counter has 6 bits");
 };
 
@@ -135,7 +137,7 @@ struct Stream {
     tail = (k_end % kSlice - 1) * ld * 2 + t.lim;  // looked at only where a row is left
   }
   // Goes on with another panel's slices, without a branch.
-  __device__ __forceinline__ void switch_to(const Stream& o, bool now) {
+  __device__ __forceinline__ void go_on(const Stream& o, bool now) {
     p = now ? o.p : p;
     rec = now ? o.rec : rec;
     if (kAcross) {
@@ -143,10 +145,11 @@ struct Stream {
       tail = now ? o.tail : tail;
     }
   }
-  __device__ __forceinline__ __amdgpu_buffer_rsrc_t next(int ld) {
-    const int now = kAcross ? (rest >= kSlice ? rec : (rest > 0 ? tail : 0)) : (rec > 0 ? rec : 0);
-    const __amdgpu_buffer_rsrc_t r =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, __builtin_amdgcn_readfirstlane(now), kRsrcWord3);
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t now() const {
+    const int n = kAcross ? (rest >= kSlice ? rec : (rest > 0 ? tail : 0)) : (rec > 0 ? rec : 0);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, __builtin_amdgcn_readfirstlane(n), kRsrcWord3);
+  }
+  __device__ __forceinline__ void advance(int ld) {
     if (kAcross) {
       p += static_cast<int64_t>(ld) * kSlice;
       rest -= kSlice;
@@ -154,7 +157,6 @@ struct Stream {
       p += kSlice;
       rec -= kSlice * 2;
     }
-    return r;
   }
 };
 
@@ -239,15 +241,18 @@ __device__ __forceinline__ void mma(f32x4& c, const bf16x8& b, const bf16x8& a) 
 
 // Between writes of the accumulators by ordinary instructions and mma (2 wait
 // states), and between mma and their reads (11 for this instruction): 32. The
-// accumulators pass through, so that nothing is done with them before.
+// accumulators pass through before and after, so that the one is done by then and
+// the other does not begin.
 template <int kM, int kN>
 __device__ __forceinline__ void settle(f32x4 (&acc)[kM][kN]) {
-  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < kM; ++i)
+  for (int turn = 0; turn < 2; ++turn) {
 #pragma unroll
-    for (int j = 0; j < kN; j += 4)
-      asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]), "+a"(acc[i][j + 2]), "+a"(acc[i][j + 3]));
+    for (int i = 0; i < kM; ++i)
+#pragma unroll
+      for (int j = 0; j < kN; j += 2) asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));
+    if (turn == 0) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  }
 }
 
 // A tile's product: panels and the end of K.
@@ -303,8 +308,10 @@ struct Tiles {
     streams(t);
 #pragma unroll
     for (int q = 0; q < S::kRing; ++q) {
-      const __amdgpu_buffer_rsrc_t ra = sa.next(lda);
-      const __amdgpu_buffer_rsrc_t rb = sb.next(ldb);
+      const __amdgpu_buffer_rsrc_t ra = sa.now();
+      const __amdgpu_buffer_rsrc_t rb = sb.now();
+      sa.advance(lda);
+      sb.advance(ldb);
 #pragma unroll
       for (int j = 0; j < S::kLoadsA; ++j) load_a(ra, ring + q * S::kBytes, j);
 #pragma unroll
@@ -319,17 +326,20 @@ struct Tiles {
     for (int i = 0; i < S::MB; ++i) fa[0][i] = read_frag<kTA, S::MB, S::BM>(pa, i);
 #pragma unroll
     for (int j = 0; j < S::NB; ++j) fb[0][j] = read_frag<kTB, S::NB, S::BN>(pb, j);
-    turn(S::kBytes);
+#pragma unroll
+    for (int n = 0; n < kAddresses; ++n) turn(n, S::kBytes);
   }
 
   __device__ __forceinline__ static int wave_m() { return (threadIdx.x >> 6) % S::WM; }
   __device__ __forceinline__ static int wave_n() { return (threadIdx.x >> 6) / S::WM; }
 
-  __device__ __forceinline__ void turn(int by) {
-#pragma unroll
-    for (int n = 0; n < pa.kCount; ++n) pa.at[n] += by;
-#pragma unroll
-    for (int n = 0; n < pb.kCount; ++n) pb.at[n] += by;
+  // Fragment address n (A's, then B's) goes to another buffer.
+  static constexpr int kAddresses = FragAt<kTA, S::MB>::kCount + FragAt<kTB, S::NB>::kCount;
+  __device__ __forceinline__ void turn(int n, int by) {
+    if (n < pa.kCount)
+      pa.at[n] += by;
+    else
+      pb.at[n - pa.kCount] += by;
   }
 
   // The wave's LDS reads, the loads of the slice after next, then the workgroup.
@@ -341,13 +351,17 @@ struct Tiles {
   // (in the first three quarters, so that none is waited for at the barrier) and a
   // slice's loads issued between them, into the buffer `to`. sched_barrier keeps
   // each group of instructions where it is written; without restrict every
-  // fragment read waits for all loads.
+  // fragment read waits for all loads. After the last slice of a tile's loads
+  // (`on`) the streams go on to na, nb.
   template <int kHalf>
-  __device__ __forceinline__ void slice(Acc& acc, uint8_t* __restrict__ to) {
+  __device__ __forceinline__ void slice(Acc& acc, uint8_t* __restrict__ to, const Stream<kTA>& na,
+                                        const Stream<kTB>& nb, bool on) {
     constexpr int kSlots = S::MB * S::NB, kReads = S::MB + S::NB, kLater = kSlots / 2;
-    constexpr int kTurnAt = (kReads - 1) * (kSlots * 3 / 4) / kReads + 1;
-    static_assert(kReads * 4 <= kSlots * 3 && S::kLoadsA < kLater && S::kLoadsB <= kSlots - kLater, "one of each a slot");
-    __amdgpu_buffer_rsrc_t ra, rb;
+    constexpr int kTurn = (kReads - 1) * (kSlots * 3 / 4) / kReads + 1;  // after the last read
+    static_assert(kReads * 4 <= kSlots * 3 && S::kLoadsA < kLater && kLater >= 4 && S::kLoadsB <= kSlots - kLater, "one of each a slot");
+    const __amdgpu_buffer_rsrc_t ra = sa.now();
+    __amdgpu_buffer_rsrc_t rb;
+    int by;
     each([&](auto slot) __attribute__((always_inline)) {
       constexpr int t = slot, i = t / S::NB, j = t % S::NB;
       mma(acc[i][j], fb[kHalf][j], fa[kHalf][i]);
@@ -356,17 +370,23 @@ struct Tiles {
         fa[kHalf ^ 1][read] = read_frag<kTA, S::MB, S::BM>(pa, read);
       else if constexpr (read >= 0)
         fb[kHalf ^ 1][read - S::MB] = read_frag<kTB, S::NB, S::BN>(pb, read - S::MB);
-      if constexpr (t == 0) ra = sa.next(lda);
       constexpr int la = at_slot(t, S::kLoadsA, 1, kLater - 1);
       if constexpr (la >= 0) load_a(ra, to, la);
-      if constexpr (t == kLater - 1) rb = sb.next(ldb);
+      if constexpr (t == kLater - 3) sa.advance(lda);
+      if constexpr (t == kLater - 2) sa.go_on(na, on);
+      if constexpr (t == kLater - 1) rb = sb.now();
       constexpr int lb = at_slot(t, S::kLoadsB, kLater, kSlots - kLater);
       if constexpr (lb >= 0) load_b(rb, to, lb);
-      if constexpr (t == kTurnAt) {
+      if constexpr (t == kTurn) {
         // the buffer that was read becomes the one at hand
         buf = buf + S::kBytes == S::kLds ? 0 : buf + S::kBytes;
-        turn(buf + S::kBytes == S::kLds ? S::kBytes - S::kLds : S::kBytes);
+        by = buf + S::kBytes == S::kLds ? S::kBytes - S::kLds : S::kBytes;
       }
+#pragma unroll
+      for (int n = 0; n < kAddresses; ++n)
+        if (kTurn + n * (kSlots - kTurn) / kAddresses == t) turn(n, by);
+      if constexpr (t == kSlots - 2) sb.advance(ldb);
+      if constexpr (t == kSlots - 1) sb.go_on(nb, on);
       __builtin_amdgcn_sched_barrier(0);
     }, std::make_integer_sequence<int, kSlots>());
     landed();
@@ -386,20 +406,17 @@ struct Tiles {
     settle(acc);
     const int n_slices = slices_of(t.k_end);
     const bool going = n_slices >= S::kRing;
-    int until = n_slices - S::kRing;  // slices until the loads go on to the next tile
+    const int until = n_slices - S::kRing;  // slices until the loads go on to the next tile
     Stream<kTA> na;
     Stream<kTB> nb;
     na.begin(tn.a, lda, next ? tn.k_end : 0);
     nb.begin(tn.b, ldb, next ? tn.k_end : 0);
+    sa.go_on(na, until == 0);
+    sb.go_on(nb, until == 0);
     int s = 0;
-    do {  // at least once
-      sa.switch_to(na, until == 0);
-      sb.switch_to(nb, until == 0);
-      slice<0>(acc, ring + buf);
-      sa.switch_to(na, until == 1);
-      sb.switch_to(nb, until == 1);
-      slice<1>(acc, ring + buf);
-      until -= 2;
+    do {  // one loop: accumulators that pass from loop to loop are moved between registers
+      slice<0>(acc, ring + buf, na, nb, s + 1 == until);
+      slice<1>(acc, ring + buf, na, nb, s + 2 == until);
       s += 2;
     } while (s < n_slices);
     settle(acc);

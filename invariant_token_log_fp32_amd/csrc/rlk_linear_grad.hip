@@ -157,7 +157,12 @@ __global__ __launch_bounds__(256) void k_gather(const uint16_t* __restrict__ h, 
 
 // One workgroup a compute unit: the largest wave part that the 512 registers
 // hold (the fewest LDS reads for a multiplication), five slices in 160 KB of LDS.
-using Large = Shape<256, 256, 2, 2, 5>;
+using Large = Shape<256, 256, 2, 2, 5, 1>;
+using Half = Shape<128, 256, 2, 2, 6, 1>;
+using Few = Shape<64, 256, 1, 4, 4, 2>;
+using FewHidden = Shape<64, 128, 2, 2, 12, 1>;
+using HalfHidden = Shape<128, 128, 2, 2, 9, 1>;
+using Short = Shape<128, 128, 2, 2, 3, 3>;
 
 constexpr int kTile = 256;  // rows of G are padded to whole tiles
 
@@ -205,7 +210,8 @@ __device__ __forceinline__ int tile_count(const Args& a, int n_act) {
   const int dt = (a.d + S::BN - 1) / S::BN;
   const int64_t full = a.cols / a.width;
   const int rest = static_cast<int>(a.cols - full * a.width);
-  const int per = (a.width + S::BN - 1) / S::BN, last = (rest + S::BN - 1) / S::BN;
+  constexpr int v = kPass == kWeight ? S::BM : S::BN;
+  const int per = (a.width + v - 1) / v, last = (rest + v - 1) / v;
   if (kPass == kLogits) return static_cast<int>(mt * (full * per + last));
   if (kPass == kWeight) return static_cast<int>(dt * (full * per + last));
   return mt * dt * a.shards;  // a shard without real columns has its (empty) sums all the same
@@ -215,14 +221,15 @@ template <class S, Pass kPass>
 __device__ __forceinline__ Where where_is(const Args& a, int n_act, int u) {
   const int mt = (n_act + S::BM - 1) / S::BM;
   const int dt = (a.d + S::BN - 1) / S::BN;
-  const int per = (a.width + S::BN - 1) / S::BN;
+  constexpr int cols = kPass == kWeight ? S::BM : S::BN;
+  const int per = (a.width + cols - 1) / cols;
   const int each = kPass == kHidden ? mt * dt : (kPass == kLogits ? mt : dt) * per;
   Where w;
   w.shard = u / each;
   const int64_t left = a.cols - static_cast<int64_t>(w.shard) * a.width;
   w.cols = static_cast<int>(left < 0 ? 0 : (left < a.width ? left : a.width));
   const int v = u - w.shard * each;
-  const int vt = (w.cols + S::BN - 1) / S::BN;
+  const int vt = (w.cols + cols - 1) / cols;
   if (kPass == kLogits) tile_at(v, mt, vt, w.m, w.n);
   if (kPass == kHidden) tile_at(v, mt, dt, w.m, w.n);
   if (kPass == kWeight) tile_at(v, vt, dt, w.m, w.n);
@@ -394,7 +401,7 @@ __device__ __forceinline__ void store_weight(const Args& a, const Where& w, cons
 }
 
 template <class S, Pass kPass, int kType>
-__global__ __launch_bounds__(kThreads) void k_product(Args a) {
+__global__ __launch_bounds__(kThreads, S::kPer) void k_product(Args a) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[S::kLds];
   const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
   const int n_tiles = tile_count<S, kPass>(a, n_act);
@@ -509,7 +516,7 @@ struct Plan {
   int64_t ldg;
   int64_t g_step;
   int64_t part_step;
-  int n_parts;      // partial sums of grad_hidden, and of earlier launches
+  int n_parts;      // partial sums of grad_hidden: of a launch's shards, and earlier ones that wait
   size_t n_act, coef, row_of, place, h, g, parts, bytes;
 };
 
@@ -525,9 +532,9 @@ static Plan plan_for(int64_t n_rows, int64_t d, const rlk_vocab_layout* L) {
   p.part_step = n_rows * d;
   p.at_once = p.local;
   while (p.at_once > 1 && p.at_once * p.g_step * 2 > kGBudget) p.at_once /= 2;
-  int levels = 0;  // sums of earlier launches that wait for their neighbours
+  int levels = 0;  // sums that wait for their neighbours
   for (int k = p.local / p.at_once; k > 1; k /= 2) ++levels;
-  p.n_parts = (p.at_once > 1 ? p.at_once : 0) + levels;
+  p.n_parts = (p.at_once > 1 ? p.at_once : 0) + levels;  // (shard by shard: at most as many)
   size_t at = 0;
   const auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -576,10 +583,58 @@ static int cu_count() {
   return n;
 }
 
-static unsigned grid_for(int64_t tiles) {
-  const int64_t cap = cu_count();
-  const int64_t want = (tiles + kXcds - 1) / kXcds * kXcds;
-  return static_cast<unsigned>(want < cap ? want : cap);
+// Tiles of a launch, at most (the rows with a gradient are counted on the device).
+template <class S, Pass kPass>
+static int64_t most_tiles(const Args& a, int64_t n_rows) {
+  const int64_t mt = (n_rows + S::BM - 1) / S::BM, dt = (a.d + S::BN - 1) / S::BN;
+  if (kPass == kHidden) return mt * dt * a.shards;
+  const int64_t v = kPass == kLogits ? S::BN : S::BM;
+  return (kPass == kLogits ? mt : dt) * ((a.width + v - 1) / v) * a.shards;
+}
+
+template <class S, Pass kPass, int kType>
+static int32_t product(const Args& a, int64_t n_rows, hipStream_t stream) {
+  const int64_t cap = static_cast<int64_t>(cu_count()) * S::kPer;
+  const int64_t want = (most_tiles<S, kPass>(a, n_rows) + kXcds - 1) / kXcds * kXcds;
+  k_product<S, kPass, kType><<<dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(kThreads), 0, stream>>>(a);
+  return launched();
+}
+
+// Whether tiles of 128 rows waste enough fewer than those of 256 to be worth their
+// more frequent LDS reads.
+static bool in_halves(int64_t n_rows) {
+  const int64_t halves = (n_rows + 127) / 128;
+  return halves % 2 == 1 && halves < 9;
+}
+
+// Whether grad_hidden's shards are summed one after another, each added to the
+// ones before as it ends: where that takes no more rounds of tiles over the compute
+// units than all at once, which writes and reads a partial sum for every shard.
+static bool alone(int64_t n_rows, int64_t d, int shards, bool by_halves) {
+  if (n_rows <= HalfHidden::BM) return shards == 1;
+  const int64_t rows = by_halves ? Half::BM : Large::BM;
+  const int64_t tiles = (n_rows + rows - 1) / rows * ((d + Large::BN - 1) / Large::BN);
+  constexpr int64_t kUnits = 256;
+  return (tiles + kUnits - 1) / kUnits * shards <= (tiles * shards + kUnits - 1) / kUnits;
+}
+
+template <int kType>
+static int32_t hidden_product_as(const Args& a, int64_t n_rows, bool by_halves, hipStream_t stream) {
+  if (n_rows <= FewHidden::BM) return product<FewHidden, kHidden, kType>(a, n_rows, stream);
+  if (n_rows <= HalfHidden::BM) return product<HalfHidden, kHidden, kType>(a, n_rows, stream);
+  if (by_halves) return product<Half, kHidden, kType>(a, n_rows, stream);
+  return product<Large, kHidden, kType>(a, n_rows, stream);
+}
+
+static int32_t hidden_product(const Args& a, int64_t n_rows, bool by_halves, hipStream_t stream) {
+  return a.hid.type == RLK_GRAD_BF16 ? hidden_product_as<RLK_GRAD_BF16>(a, n_rows, by_halves, stream)
+                                     : hidden_product_as<RLK_GRAD_F32>(a, n_rows, by_halves, stream);
+}
+
+template <int kType>
+static int32_t weight_product(const Args& a, int64_t n_rows, hipStream_t stream) {
+  if (n_rows <= 128) return product<Short, kWeight, kType>(a, n_rows, stream);
+  return product<Large, kWeight, kType>(a, n_rows, stream);
 }
 
 static unsigned vec_grid(int64_t vecs) {
@@ -654,9 +709,7 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
     if ((st = launched()) != RLK_OK) return st;
   }
 
-  const int64_t m_tiles = (n_rows + Large::BM - 1) / Large::BM;
-  const int64_t d_tiles = (d + Large::BN - 1) / Large::BN;
-  const int64_t v_tiles = (static_cast<int64_t>(p.width) + Large::BN - 1) / Large::BN * p.at_once;
+  const bool by_halves = in_halves(n_rows);
   const int64_t first = static_cast<int64_t>(rank) * p.local * p.width;  // the rank's first column
   Args a{};
   a.h = h;
@@ -670,7 +723,8 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
   a.shards = p.at_once;
   a.d = static_cast<int>(d);
   a.ldgw = grad_weight_stride;
-  float* waiting = parts + static_cast<int64_t>(p.at_once > 1 ? p.at_once : 0) * p.part_step;
+  const bool one_by_one = alone(n_rows, d, p.at_once, by_halves);
+  float* waiting = parts + static_cast<int64_t>(one_by_one || p.at_once == 1 ? 0 : p.at_once) * p.part_step;
   for (int s = 0; s < p.local; s += p.at_once) {
     const int64_t c0 = static_cast<int64_t>(s) * p.width;  // columns counted from the rank's first
     const int64_t left = layout->vocab_real - first - c0;
@@ -678,58 +732,63 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
     a.col0 = first + c0;
     a.cols = left < 0 ? 0 : (left < most ? left : most);
     a.w = n_rows > 0 && a.cols > 0 ? weight + c0 * weight_stride : weight;
-    if (m_tiles > 0 && a.cols > 0) {
-      k_product<Large, kLogits, RLK_GRAD_BF16><<<dim3(grid_for(m_tiles * v_tiles)), dim3(kThreads), 0, stream>>>(a);
-      if ((st = launched()) != RLK_OK) return st;
+    if (n_rows > 0 && a.cols > 0) {
+      if (n_rows <= Few::BM)
+        st = product<Few, kLogits, RLK_GRAD_BF16>(a, n_rows, stream);
+      else if (by_halves)
+        st = product<Half, kLogits, RLK_GRAD_BF16>(a, n_rows, stream);
+      else
+        st = product<Large, kLogits, RLK_GRAD_BF16>(a, n_rows, stream);
+      if (st != RLK_OK) return st;
     }
-    if (grad_hidden && m_tiles > 0) {
-      // sums of whole pairs, fours, eights of launches are added as they end
-      const int k = s / p.at_once;
-      HiddenOut o{};
-      int level = 0;
-      for (; (k >> level) & 1; ++level) o.add[level] = waiting + level * p.part_step;
-      o.n_add = level;
-      if (s + p.at_once == p.local) {
-        o.out = grad_hidden;
-        o.ldo = grad_hidden_stride;
-        o.type = grad_hidden_type;
-        o.row_of = row_of;
+    if (grad_hidden && n_rows > 0) {
+      // The k-th of the sums (of a shard, or of a launch's shards): those of whole
+      // pairs, fours and eights wait in `waiting` and are added as their neighbours end.
+      const auto sum_to = [&](int k, bool last) {
+        HiddenOut o{};
+        int level = 0;
+        for (; (k >> level) & 1; ++level) o.add[level] = waiting + level * p.part_step;
+        o.n_add = level;
+        o.out = last ? grad_hidden : waiting + level * p.part_step;
+        o.ldo = last ? grad_hidden_stride : d;
+        o.type = last ? grad_hidden_type : RLK_GRAD_F32;
+        o.row_of = last ? row_of : nullptr;
+        return o;
+      };
+      if (one_by_one) {
+        for (int k = 0; k < p.at_once; ++k) {
+          Args one = a;
+          const int64_t skip = static_cast<int64_t>(k) * p.width;
+          one.shards = 1;
+          one.cols = a.cols < skip ? 0 : (a.cols - skip < p.width ? a.cols - skip : p.width);
+          one.w = one.cols > 0 ? a.w + skip * weight_stride : a.w;
+          one.g = a.g + k * p.g_step;
+          one.hid = sum_to(s + k, s + k + 1 == p.local);
+          if ((st = hidden_product(one, n_rows, by_halves, stream)) != RLK_OK) return st;
+        }
       } else {
-        o.out = waiting + level * p.part_step;
-        o.ldo = d;
-        o.type = RLK_GRAD_F32;
-      }
-      a.hid = o;
-      if (p.at_once > 1) {
         a.hid = HiddenOut{};
         a.hid.out = parts;
         a.hid.ldo = d;
         a.hid.type = RLK_GRAD_F32;
         a.hid.shard_step = p.part_step;
-      }
-      const dim3 grid(grid_for(m_tiles * d_tiles * p.at_once));
-      if (a.hid.type == RLK_GRAD_BF16)
-        k_product<Large, kHidden, RLK_GRAD_BF16><<<grid, dim3(kThreads), 0, stream>>>(a);
-      else
-        k_product<Large, kHidden, RLK_GRAD_F32><<<grid, dim3(kThreads), 0, stream>>>(a);
-      if ((st = launched()) != RLK_OK) return st;
-      if (p.at_once > 1) {
-        k_combine<<<dim3(vec_grid(n_rows * (d / 4))), dim3(256), 0, stream>>>(parts, p.part_step, p.at_once, o, n_act,
-                                                                              static_cast<int>(d));
+        if ((st = hidden_product(a, n_rows, by_halves, stream)) != RLK_OK) return st;
+        k_combine<<<dim3(vec_grid(n_rows * (d / 4))), dim3(256), 0, stream>>>(
+            parts, p.part_step, p.at_once, sum_to(s / p.at_once, s + p.at_once == p.local), n_act,
+            static_cast<int>(d));
         if ((st = launched()) != RLK_OK) return st;
       }
     }
     if (grad_weight && a.cols > 0) {
       const int64_t size = grad_weight_type == RLK_GRAD_BF16 ? 2 : 4;
       a.gw = static_cast<uint8_t*>(grad_weight) + c0 * grad_weight_stride * size;
-      const dim3 grid(grid_for(v_tiles * d_tiles));
       if (grad_weight_type == RLK_GRAD_BF16)
-        k_product<Large, kWeight, RLK_GRAD_BF16><<<grid, dim3(kThreads), 0, stream>>>(a);
+        st = weight_product<RLK_GRAD_BF16>(a, n_rows, stream);
       else if (grad_weight_type == RLK_GRAD_F32)
-        k_product<Large, kWeight, RLK_GRAD_F32><<<grid, dim3(kThreads), 0, stream>>>(a);
+        st = weight_product<RLK_GRAD_F32>(a, n_rows, stream);
       else
-        k_product<Large, kWeight, RLK_GRAD_F32_ADD><<<grid, dim3(kThreads), 0, stream>>>(a);
-      if ((st = launched()) != RLK_OK) return st;
+        st = weight_product<RLK_GRAD_F32_ADD>(a, n_rows, stream);
+      if (st != RLK_OK) return st;
     }
   }
   return RLK_OK;

@@ -109,7 +109,9 @@ def close(got, want, mag, extra, n_terms, bf16, what):
 
 
 SIZES = [(1, 64, 300, 320), (2, 128, 1000, 1024), (5, 192, 64, 64), (37, 320, 2500, 2560), (257, 256, 1111, 1152),
-         (300, 1088, 700, 1024), (64, 64, 4096, 4096), (130, 576, 5000, 8192), (513, 128, 2049, 2112)]
+         (300, 1088, 700, 1024), (64, 64, 4096, 4096), (130, 576, 5000, 8192), (513, 128, 2049, 2112),
+         (64, 832, 3000, 3136), (65, 64, 1000, 1024), (128, 320, 2111, 2176), (129, 128, 600, 640), (640, 192, 900, 960),
+         (1025, 64, 500, 512)]
 
 
 @pytest.mark.parametrize("n,d,vr,vp", SIZES)
