@@ -25,7 +25,7 @@
 // slice, into the buffer that s came from (its fragments were read in s - 1, and
 // a barrier has passed). The barrier at the end of a slice waits until s + 2 has
 // landed and leaves the younger loads in flight, so a load has (kRing - 2) slices
-// to come. The ring runs on from tile to tile.
+// to come. The ring runs on from tile to tile, over several short ones.
 //
 // Order of a sum: increasing k, the accumulator carried from instruction to
 // instruction, whatever the tile's shape. 16x16x32 gives the bits of two
@@ -136,14 +136,9 @@ struct Stream {
     rest = k_end;
     tail = (k_end % kSlice - 1) * ld * 2 + t.lim;  // looked at only where a row is left
   }
-  // Goes on with another panel's slices, without a branch.
-  __device__ __forceinline__ void go_on(const Stream& o, bool now) {
-    p = now ? o.p : p;
-    rec = now ? o.rec : rec;
-    if (kAcross) {
-      rest = now ? o.rest : rest;
-      tail = now ? o.tail : tail;
-    }
+  __device__ __forceinline__ void none() {
+    rec = 0;
+    rest = 0;
   }
   __device__ __forceinline__ __amdgpu_buffer_rsrc_t now() const {
     const int n = kAcross ? (rest >= kSlice ? rec : (rest > 0 ? tail : 0)) : (rec > 0 ? rec : 0);
@@ -255,6 +250,17 @@ __device__ __forceinline__ void settle(f32x4 (&acc)[kM][kN]) {
   }
 }
 
+// An accumulator's values in ordinary registers, for good: copies that the compiler
+// may merge with the accumulator end in moves around mma.
+__device__ __forceinline__ f32x4 taken(const f32x4& c) {
+  f32x4 v;
+  asm("v_accvgpr_read_b32 %0, %1" : "=v"(v.x) : "a"(c.x));
+  asm("v_accvgpr_read_b32 %0, %1" : "=v"(v.y) : "a"(c.y));
+  asm("v_accvgpr_read_b32 %0, %1" : "=v"(v.z) : "a"(c.z));
+  asm("v_accvgpr_read_b32 %0, %1" : "=v"(v.w) : "a"(c.w));
+  return v;
+}
+
 // A tile's product: panels and the end of K.
 struct TileIn {
   Panel a, b;
@@ -267,10 +273,15 @@ __device__ __forceinline__ int slices_of(int k_end) {
 }
 
 // The pipeline of a workgroup: operands' strides, where loads and fragments lie,
-// the ring's position, and the fragments in registers.
-template <class S, bool kTA, bool kTB>
+// the ring's position, and the fragments in registers. The loads run kRing slices
+// ahead of the sums, over as many tiles as that is; `next(t)` gives them the
+// workgroup's next tile, or false.
+template <class S, bool kTA, bool kTB, class Next>
 struct Tiles {
   typedef f32x4 Acc[S::MB][S::NB];
+
+  Next next;
+  int left;       // slices of the loads' tile
 
   int lda, ldb;
   uint8_t* ring;
@@ -283,10 +294,8 @@ struct Tiles {
   FragAt<kTB, S::NB> pb;
   bf16x8 fa[2][S::MB], fb[2][S::NB];  // of the slice at hand and of the next, in turn
 
-  __device__ __forceinline__ void init(uint8_t* smem, int lda_, int ldb_) {
-    lda = lda_;
-    ldb = ldb_;
-    ring = smem;
+  __device__ __forceinline__ Tiles(const Next& n, uint8_t* smem, int lda_, int ldb_)
+      : next(n), lda(lda_), ldb(ldb_), ring(smem) {
     oa = offsets_for<kTA, S::BM>(lda);
     ob = offsets_for<kTB, S::BN>(ldb);
   }
@@ -298,16 +307,27 @@ struct Tiles {
     load_to_lds(r, ob.at[j], to + S::kBytesA + (wave_id() * S::kLoadsB + j) * 1024);
   }
 
-  __device__ __forceinline__ void streams(const TileIn& t) {
-    sa.begin(t.a, lda, t.k_end);
-    sb.begin(t.b, ldb, t.k_end);
+  // The loads go on to the next tile.
+  __device__ __forceinline__ void go_on() {
+    TileIn t;
+    if (next(t)) {
+      sa.begin(t.a, lda, t.k_end);
+      sb.begin(t.b, ldb, t.k_end);
+      left = slices_of(t.k_end);
+    } else {
+      sa.none();
+      sb.none();
+      left = 1 << 30;
+    }
   }
 
-  // Fills the ring with a tile's first slices and reads the first one's fragments.
-  __device__ __forceinline__ void start(const TileIn& t) {
-    streams(t);
+  // Fills the ring and reads the first slice's fragments.
+  __device__ __forceinline__ void start() {
+    left = 0;
 #pragma unroll
     for (int q = 0; q < S::kRing; ++q) {
+      if (left == 0) go_on();  // uniform
+      --left;
       const __amdgpu_buffer_rsrc_t ra = sa.now();
       const __amdgpu_buffer_rsrc_t rb = sb.now();
       sa.advance(lda);
@@ -317,6 +337,7 @@ struct Tiles {
 #pragma unroll
       for (int j = 0; j < S::kLoadsB; ++j) load_b(rb, ring + q * S::kBytes, j);
     }
+    if (left == 0) go_on();  // sums() finds at least a slice to load
     landed();
     buf = 0;
     const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((LdsPtr)(ring)));
@@ -351,11 +372,9 @@ struct Tiles {
   // (in the first three quarters, so that none is waited for at the barrier) and a
   // slice's loads issued between them, into the buffer `to`. sched_barrier keeps
   // each group of instructions where it is written; without restrict every
-  // fragment read waits for all loads. After the last slice of a tile's loads
-  // (`on`) the streams go on to na, nb.
+  // fragment read waits for all loads.
   template <int kHalf>
-  __device__ __forceinline__ void slice(Acc& acc, uint8_t* __restrict__ to, const Stream<kTA>& na,
-                                        const Stream<kTB>& nb, bool on) {
+  __device__ __forceinline__ void slice(Acc& acc, uint8_t* __restrict__ to) {
     constexpr int kSlots = S::MB * S::NB, kReads = S::MB + S::NB, kLater = kSlots / 2;
     constexpr int kTurn = (kReads - 1) * (kSlots * 3 / 4) / kReads + 1;  // after the last read
     static_assert(kReads * 4 <= kSlots * 3 && S::kLoadsA < kLater && kLater >= 4 && S::kLoadsB <= kSlots - kLater, "one of each a slot");
@@ -372,8 +391,7 @@ struct Tiles {
         fb[kHalf ^ 1][read - S::MB] = read_frag<kTB, S::NB, S::BN>(pb, read - S::MB);
       constexpr int la = at_slot(t, S::kLoadsA, 1, kLater - 1);
       if constexpr (la >= 0) load_a(ra, to, la);
-      if constexpr (t == kLater - 3) sa.advance(lda);
-      if constexpr (t == kLater - 2) sa.go_on(na, on);
+      if constexpr (t == kLater - 2) sa.advance(lda);
       if constexpr (t == kLater - 1) rb = sb.now();
       constexpr int lb = at_slot(t, S::kLoadsB, kLater, kSlots - kLater);
       if constexpr (lb >= 0) load_b(rb, to, lb);
@@ -385,18 +403,16 @@ struct Tiles {
 #pragma unroll
       for (int n = 0; n < kAddresses; ++n)
         if (kTurn + n * (kSlots - kTurn) / kAddresses == t) turn(n, by);
-      if constexpr (t == kSlots - 2) sb.advance(ldb);
-      if constexpr (t == kSlots - 1) sb.go_on(nb, on);
+      if constexpr (t == kSlots - 1) sb.advance(ldb);
       __builtin_amdgcn_sched_barrier(0);
     }, std::make_integer_sequence<int, kSlots>());
     landed();
   }
 
-  // The sums of tile t into acc; `tn` follows it in the ring when `next`. Element e
-  // of block (i, j) in lane l is row 16 i + l % 16, column 16 j + 4 (l / 16) + e of
-  // the wave's part (B's fragment is the first operand). Returns whether the ring holds the next
-  // tile's first slices (a tile shorter than the ring ends it: start again).
-  __device__ __forceinline__ bool sums(Acc& acc, const TileIn& t, const TileIn& tn, bool next) {
+  // The sums of the next tile, n_slices long, into acc. Element e of block (i, j) in
+  // lane l is row 16 i + l % 16, column 16 j + 4 (l / 16) + e of the wave's part (B's
+  // fragment is the first operand).
+  __device__ __forceinline__ void sums(Acc& acc, int n_slices) {
 #pragma unroll
     for (int i = 0; i < S::MB; ++i)
 #pragma unroll
@@ -404,23 +420,38 @@ struct Tiles {
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
     settle(acc);
-    const int n_slices = slices_of(t.k_end);
-    const bool going = n_slices >= S::kRing;
-    const int until = n_slices - S::kRing;  // slices until the loads go on to the next tile
-    Stream<kTA> na;
-    Stream<kTB> nb;
-    na.begin(tn.a, lda, next ? tn.k_end : 0);
-    nb.begin(tn.b, ldb, next ? tn.k_end : 0);
-    sa.go_on(na, until == 0);
-    sb.go_on(nb, until == 0);
+    // Pairs of slices up to the end of the sums or of the loads' tile, without a
+    // branch in between (one for each slice costs 3% of the large products); a ring
+    // of odd length ends the loads' tile inside a pair.
     int s = 0;
-    do {  // one loop: accumulators that pass from loop to loop are moved between registers
-      slice<0>(acc, ring + buf, na, nb, s + 1 == until);
-      slice<1>(acc, ring + buf, na, nb, s + 2 == until);
-      s += 2;
+    do {
+      const int even = left & ~1;
+      const int run = n_slices - s < even ? n_slices - s : even;
+      if constexpr (S::kRing % 2) {
+        for (int k = 0; k < run; k += 2) {
+          slice<0>(acc, ring + buf);
+          slice<1>(acc, ring + buf);
+        }
+      } else {
+        int k = 0;
+        do {  // at least once
+          slice<0>(acc, ring + buf);
+          slice<1>(acc, ring + buf);
+          k += 2;
+        } while (k < run);
+      }
+      s += run;
+      left -= run;
+      if (S::kRing % 2 && left == 1 && s < n_slices) {
+        slice<0>(acc, ring + buf);
+        go_on();
+        slice<1>(acc, ring + buf);
+        s += 2;
+        --left;
+      }
+      if (left == 0) go_on();
     } while (s < n_slices);
     settle(acc);
-    return going;
   }
 };
 

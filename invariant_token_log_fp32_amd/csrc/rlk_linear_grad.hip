@@ -159,7 +159,7 @@ __global__ __launch_bounds__(256) void k_gather(const uint16_t* __restrict__ h, 
 // hold (the fewest LDS reads for a multiplication), five slices in 160 KB of LDS.
 using Large = Shape<256, 256, 2, 2, 5, 1>;
 using Half = Shape<128, 256, 2, 2, 6, 1>;
-using Few = Shape<64, 256, 1, 4, 4, 2>;
+using Few = Shape<64, 128, 2, 2, 12, 1>;
 using FewHidden = Shape<64, 128, 2, 2, 12, 1>;
 using HalfHidden = Shape<128, 128, 2, 2, 9, 1>;
 using Short = Shape<128, 128, 2, 2, 3, 3>;
@@ -280,7 +280,7 @@ __device__ __forceinline__ int lane_here() {
 // G of the tile from its sums: BF16 logits (rounded to nearest even), the
 // gradient formula, BF16 again. Columns past the shard's real ones hold zeros.
 template <class S>
-__device__ __forceinline__ void store_g(const Args& a, int n_act, const Where& w, f32x4 (&acc)[S::MB][S::NB]) {
+__device__ __forceinline__ void store_g(const Args& a, int n_act, const Where& w, const f32x4 (&acc)[S::MB][S::NB]) {
   constexpr int kCols = S::NB * 16;       // of a wave
   const int lane = lane_here();
   const int h = lane >> 4;
@@ -296,38 +296,40 @@ __device__ __forceinline__ void store_g(const Args& a, int n_act, const Where& w
     const int gr = w.m * S::BM + (wm * S::MB + i) * 16 + (lane & 15);
     const RowCoef R = a.coef[gr < n_act ? gr : 0];
     const bool policy = __any(R.s_p != 0.0f);
+    f32x4 v[S::NB];
 #pragma unroll
-    for (int j = 0; j < S::NB; ++j)
+    for (int j = 0; j < S::NB; ++j) {
+      v[j] = taken(acc[i][j]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float x = __uint_as_float(static_cast<uint32_t>(__builtin_bit_cast(
-                                            uint16_t, static_cast<__bf16>(acc[i][j][e]))) << 16);
-        float v = R.s_r * __builtin_amdgcn_exp2f(fmaf(x, R.c, R.a_r));
+                                            uint16_t, static_cast<__bf16>(v[j][e]))) << 16);
+        float o = R.s_r * __builtin_amdgcn_exp2f(fmaf(x, R.c, R.a_r));
         if (policy) {  // uniform
           const float q = x >= R.thr ? __builtin_amdgcn_exp2f(fmaf(x, R.c, R.a_p)) : 0.0f;
-          v = v + R.s_p * q;
+          o = o + R.s_p * q;
         }
-        acc[i][j][e] = v;
+        v[j][e] = o;
       }
+    }
     const int64_t lc = R.target - col;
     const bool tin = R.target >= 0 && lc >= 0 && lc < kCols;
     if (__any(tin)) {
       const int lci = static_cast<int>(tin ? lc : 0);
       const int kt = tin && ((lci >> 2) & 3) == h ? (lci >> 4) * 4 + (lci & 3) : -1;
 #pragma unroll
-      for (int k = 0; k < 4 * S::NB; ++k) acc[i][k >> 2][k & 3] = k == kt ? R.g_t : acc[i][k >> 2][k & 3];
+      for (int k = 0; k < 4 * S::NB; ++k) v[k >> 2][k & 3] = k == kt ? R.g_t : v[k >> 2][k & 3];
     }
     if (!whole) {
       const int lim = w.cols - cw - 4 * h;  // this lane's column 16 j + e is real iff below lim
 #pragma unroll
-      for (int k = 0; k < 4 * S::NB; ++k)
-        acc[i][k >> 2][k & 3] = 16 * (k >> 2) + (k & 3) < lim ? acc[i][k >> 2][k & 3] : 0.0f;
+      for (int k = 0; k < 4 * S::NB; ++k) v[k >> 2][k & 3] = 16 * (k >> 2) + (k & 3) < lim ? v[k >> 2][k & 3] : 0.0f;
     }
     uint16_t* dst = g + static_cast<int64_t>(gr) * a.ldg + cw + pair_column(h);
 #pragma unroll
     for (int j = 0; j < S::NB; j += 2) {
-      const u32x4 v = pair_words(acc[i][j], acc[i][j + 1]);
-      if (gr < n_act) *reinterpret_cast<u32x4*>(dst + 16 * j) = v;  // ldg is a multiple of 256: the tile's columns exist
+      const u32x4 o = pair_words(v[j], v[j + 1]);
+      if (gr < n_act) *reinterpret_cast<u32x4*>(dst + 16 * j) = o;  // ldg is a multiple of 256: the tile's columns exist
     }
   }
 }
@@ -357,10 +359,9 @@ __device__ __forceinline__ void store_hidden(const Args& a, int n_act, const Whe
 #pragma unroll
   for (int i = 0; i < S::MB; ++i) {
     const int gr = w.m * S::BM + (wm * S::MB + i) * 16 + (lane & 15);
-    f32x4 v[S::NB];  // (sums added to here leave the accumulators in their registers)
+    f32x4 v[S::NB];
 #pragma unroll
-    for (int j = 0; j < S::NB; ++j) v[j] = acc[i][j];
-    __builtin_amdgcn_sched_barrier(0);
+    for (int j = 0; j < S::NB; ++j) v[j] = taken(acc[i][j]);
     for (int k = 0; k < a.hid.n_add; ++k) {
       const float* from = a.hid.add[k] + static_cast<int64_t>(gr) * a.d + cw + 4 * h;
       f32x4 o[S::NB];
@@ -372,7 +373,6 @@ __device__ __forceinline__ void store_hidden(const Args& a, int n_act, const Whe
 #pragma unroll
       for (int j = 0; j < S::NB; ++j) v[j] = o[j] + v[j];
     }
-    __builtin_amdgcn_sched_barrier(0);
     const int64_t row = a.hid.row_of && gr < n_act ? a.hid.row_of[gr] : gr;
     const int64_t at = row * a.hid.ldo + w.shard * a.hid.shard_step + cw;
 #pragma unroll
@@ -396,7 +396,7 @@ __device__ __forceinline__ void store_weight(const Args& a, const Where& w, cons
     const int64_t at = (first + v) * a.ldgw + cw;
 #pragma unroll
     for (int j = 0; j < S::NB; j += 2)
-      store_pair<kType>(acc[i][j], acc[i][j + 1], v < w.cols && cw + 16 * j < a.d, a.gw, at + 16 * j, h);
+      store_pair<kType>(taken(acc[i][j]), taken(acc[i][j + 1]), v < w.cols && cw + 16 * j < a.d, a.gw, at + 16 * j, h);
   }
 }
 
@@ -408,33 +408,25 @@ __global__ __launch_bounds__(kThreads, S::kPer) void k_product(Args a) {
   const int grid = static_cast<int>(gridDim.x);
   int u = first_tile();
   if (u >= n_tiles) return;  // uniform across the workgroup
-  Where w = where_is<S, kPass>(a, n_act, u);
-  TileIn t = tile_in<S, kPass>(a, n_act, w);
-  Tiles<S, kPass == kWeight, kPass != kLogits> tiles;
-  tiles.init(smem, kPass == kLogits ? a.d : static_cast<int>(a.ldg),
-             kPass == kWeight ? a.d : static_cast<int>(a.ldw));
-  tiles.start(t);
-  while (true) {
-    const bool more = u + grid < n_tiles;
-    Where w2 = w;
-    TileIn t2 = t;
-    if (more) {
-      w2 = where_is<S, kPass>(a, n_act, u + grid);
-      t2 = tile_in<S, kPass>(a, n_act, w2);
-    }
+  int loads = u;  // the tile that the loads come to next
+  const auto next = [&](TileIn& t) __attribute__((always_inline)) {
+    if (loads >= n_tiles) return false;
+    t = tile_in<S, kPass>(a, n_act, where_is<S, kPass>(a, n_act, loads));
+    loads += grid;
+    return true;
+  };
+  Tiles<S, kPass == kWeight, kPass != kLogits, decltype(next)> tiles(
+      next, smem, kPass == kLogits ? a.d : static_cast<int>(a.ldg), kPass == kWeight ? a.d : static_cast<int>(a.ldw));
+  tiles.start();
+  for (; u < n_tiles; u += grid) {
+    const Where w = where_is<S, kPass>(a, n_act, u);
     f32x4 acc[S::MB][S::NB];
-    const bool going = tiles.sums(acc, t, t2, more);
+    tiles.sums(acc, slices_of(kPass == kLogits ? a.d : (kPass == kHidden ? w.cols : n_act)));
     if (kPass == kLogits) store_g<S>(a, n_act, w, acc);
     if (kPass == kHidden) store_hidden<S, kType>(a, n_act, w, acc);
     if (kPass == kWeight) store_weight<S, kType>(a, w, acc);
-    if (!more) break;
-    u += grid;
-    w = w2;
-    t = t2;
-    if (!going) tiles.start(t);
   }
 }
-
 
 // The fixed sum of `count` (1, 2, 4 or 8) partial sums, neighbours first.
 template <typename F>
