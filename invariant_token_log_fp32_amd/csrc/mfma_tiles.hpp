@@ -108,7 +108,8 @@ __device__ __forceinline__ int swz_k(int k) {
 
 // One operand of one tile: where its first slice begins and what may be read.
 // K contiguous: lim = bytes from p to the end of the last row's K. K across rows:
-// lim = bytes of a row from p on, k_end rows.
+// lim = bytes of a row from p on, k_end rows. Both are multiples of a chunk: the
+// range check cuts whole words.
 struct Panel {
   const uint16_t* p;
   int lim;

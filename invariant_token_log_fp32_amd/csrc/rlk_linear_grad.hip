@@ -155,16 +155,20 @@ __global__ __launch_bounds__(256) void k_gather(const uint16_t* __restrict__ h, 
   }
 }
 
-// One workgroup a compute unit: the largest wave part that the 512 registers
-// hold (the fewest LDS reads for a multiplication), five slices in 160 KB of LDS.
+// Tiles, with LDS for one workgroup a compute unit (three of Short). Large has the
+// largest wave part that the 512 registers hold, so the fewest LDS reads for a
+// multiplication; the smaller ones are for products whose Large tiles would leave
+// compute units idle. kCost: time of a tile's slice in hundredths of Large's,
+// measured on full GPUs (1500 rows of the 151936 x 4096 head: Large 8 rounds of
+// logits 868 us, Half 14 in 1121, Quarter 28 in 1279; Few twice that).
 using Large = Shape<256, 256, 2, 2, 5, 1>;
 using Half = Shape<128, 256, 2, 2, 6, 1>;
+using Quarter = Shape<128, 128, 2, 2, 9, 1>;
 using Few = Shape<64, 128, 2, 2, 12, 1>;
-using FewHidden = Shape<64, 128, 2, 2, 12, 1>;
-using HalfHidden = Shape<128, 128, 2, 2, 9, 1>;
-using Short = Shape<128, 128, 2, 2, 3, 3>;
+using Short = Shape<128, 128, 2, 2, 3, 3>;  // sums over few rows: bound by their stores, three tiles at a time
+constexpr int kCost[4] = {100, 70, 44, 30};
 
-constexpr int kTile = 256;  // rows of G are padded to whole tiles
+constexpr int kTile = 256;  // columns of G are padded to whole tiles
 
 enum Pass { kLogits = 0, kHidden = 1, kWeight = 2 };
 
@@ -205,16 +209,16 @@ struct Where {
 };
 
 template <class S, Pass kPass>
-__device__ __forceinline__ int tile_count(const Args& a, int n_act) {
+__host__ __device__ __forceinline__ int64_t tile_count(const Args& a, int n_act) {
   const int mt = (n_act + S::BM - 1) / S::BM;
   const int dt = (a.d + S::BN - 1) / S::BN;
   const int64_t full = a.cols / a.width;
   const int rest = static_cast<int>(a.cols - full * a.width);
   constexpr int v = kPass == kWeight ? S::BM : S::BN;
   const int per = (a.width + v - 1) / v, last = (rest + v - 1) / v;
-  if (kPass == kLogits) return static_cast<int>(mt * (full * per + last));
-  if (kPass == kWeight) return static_cast<int>(dt * (full * per + last));
-  return mt * dt * a.shards;  // a shard without real columns has its (empty) sums all the same
+  if (kPass == kLogits) return mt * (full * per + last);
+  if (kPass == kWeight) return dt * (full * per + last);
+  return static_cast<int64_t>(mt) * dt * a.shards;  // a shard without real columns has its (empty) sums all the same
 }
 
 template <class S, Pass kPass>
@@ -249,7 +253,9 @@ __device__ __forceinline__ TileIn tile_in(const Args& a, int n_act, const Where&
     t.b = panel_rows(wp + static_cast<int64_t>(w.n) * S::BN * a.ldw, vr, static_cast<int>(a.ldw), a.d);
   } else if (kPass == kHidden) {
     t.k_end = w.cols;
-    t.a = panel_rows(gp + static_cast<int64_t>(w.m) * S::BM * a.ldg, rows, static_cast<int>(a.ldg), w.cols);
+    // G is zero up to whole slices (an odd end would cut the last row's last word off)
+    const int k = w.cols > 0 ? slices_of(w.cols) * kSlice : 0;
+    t.a = panel_rows(gp + static_cast<int64_t>(w.m) * S::BM * a.ldg, rows, static_cast<int>(a.ldg), k);
     t.b = panel_cols(wp + w.n * S::BN, a.d - w.n * S::BN, S::BN);
   } else {
     t.k_end = n_act;
@@ -404,7 +410,7 @@ template <class S, Pass kPass, int kType>
 __global__ __launch_bounds__(kThreads, S::kPer) void k_product(Args a) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[S::kLds];
   const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
-  const int n_tiles = tile_count<S, kPass>(a, n_act);
+  const int n_tiles = static_cast<int>(tile_count<S, kPass>(a, n_act));
   const int grid = static_cast<int>(gridDim.x);
   int u = first_tile();
   if (u >= n_tiles) return;  // uniform across the workgroup
@@ -575,54 +581,52 @@ static int cu_count() {
   return n;
 }
 
-// Tiles of a launch, at most (the rows with a gradient are counted on the device).
-template <class S, Pass kPass>
-static int64_t most_tiles(const Args& a, int64_t n_rows) {
-  const int64_t mt = (n_rows + S::BM - 1) / S::BM, dt = (a.d + S::BN - 1) / S::BN;
-  if (kPass == kHidden) return mt * dt * a.shards;
-  const int64_t v = kPass == kLogits ? S::BN : S::BM;
-  return (kPass == kLogits ? mt : dt) * ((a.width + v - 1) / v) * a.shards;
-}
-
+// (The rows with a gradient are counted on the device: n_rows is the most.)
 template <class S, Pass kPass, int kType>
 static int32_t product(const Args& a, int64_t n_rows, hipStream_t stream) {
   const int64_t cap = static_cast<int64_t>(cu_count()) * S::kPer;
-  const int64_t want = (most_tiles<S, kPass>(a, n_rows) + kXcds - 1) / kXcds * kXcds;
+  const int64_t want = (tile_count<S, kPass>(a, static_cast<int>(n_rows)) + kXcds - 1) / kXcds * kXcds;
   k_product<S, kPass, kType><<<dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(kThreads), 0, stream>>>(a);
   return launched();
 }
 
-// Whether tiles of 128 rows waste enough fewer than those of 256 to be worth their
-// more frequent LDS reads.
-static bool in_halves(int64_t n_rows) {
-  const int64_t halves = (n_rows + 127) / 128;
-  return halves % 2 == 1 && halves < 9;
-}
+// The tiles for a product: the least rounds over the compute units times a round's
+// cost; the larger ones where that is equal. Few rows read little of what a tile
+// multiplies: 1 row 0.80 ms, with Large tiles 1.12.
+struct Choice {
+  int kind;
+  int64_t cost;
+};
 
-// Whether grad_hidden's shards are summed one after another, each added to the
-// ones before as it ends: where that takes no more rounds of tiles over the compute
-// units than all at once, which writes and reads a partial sum for every shard.
-static bool alone(int64_t n_rows, int64_t d, int shards, bool by_halves) {
-  if (n_rows <= HalfHidden::BM) return shards == 1;
-  const int64_t rows = by_halves ? Half::BM : Large::BM;
-  const int64_t tiles = (n_rows + rows - 1) / rows * ((d + Large::BN - 1) / Large::BN);
+template <Pass kPass>
+static Choice tiles_for(const Args& a, int64_t n_rows) {
   constexpr int64_t kUnits = 256;
-  return (tiles + kUnits - 1) / kUnits * shards <= (tiles * shards + kUnits - 1) / kUnits;
+  const int n = static_cast<int>(n_rows);
+  const int64_t tiles[4] = {tile_count<Large, kPass>(a, n), tile_count<Half, kPass>(a, n),
+                            tile_count<Quarter, kPass>(a, n), tile_count<Few, kPass>(a, n)};
+  Choice best{0, 0};
+  for (int k = 0; k < 4; ++k) {
+    const int64_t cost = (tiles[k] + kUnits - 1) / kUnits * kCost[k];
+    if (k == 0 || cost < best.cost) best = Choice{k, cost};
+  }
+  return best;
 }
 
-template <int kType>
-static int32_t hidden_product_as(const Args& a, int64_t n_rows, bool by_halves, hipStream_t stream) {
-  if (n_rows <= FewHidden::BM) return product<FewHidden, kHidden, kType>(a, n_rows, stream);
-  if (n_rows <= HalfHidden::BM) return product<HalfHidden, kHidden, kType>(a, n_rows, stream);
-  if (by_halves) return product<Half, kHidden, kType>(a, n_rows, stream);
-  return product<Large, kHidden, kType>(a, n_rows, stream);
+template <Pass kPass, int kType>
+static int32_t product_of(int kind, const Args& a, int64_t n_rows, hipStream_t stream) {
+  if (kind == 0) return product<Large, kPass, kType>(a, n_rows, stream);
+  if (kind == 1) return product<Half, kPass, kType>(a, n_rows, stream);
+  if (kind == 2) return product<Quarter, kPass, kType>(a, n_rows, stream);
+  return product<Few, kPass, kType>(a, n_rows, stream);
 }
 
-static int32_t hidden_product(const Args& a, int64_t n_rows, bool by_halves, hipStream_t stream) {
-  return a.hid.type == RLK_GRAD_BF16 ? hidden_product_as<RLK_GRAD_BF16>(a, n_rows, by_halves, stream)
-                                     : hidden_product_as<RLK_GRAD_F32>(a, n_rows, by_halves, stream);
+static int32_t hidden_product(int kind, const Args& a, int64_t n_rows, hipStream_t stream) {
+  return a.hid.type == RLK_GRAD_BF16 ? product_of<kHidden, RLK_GRAD_BF16>(kind, a, n_rows, stream)
+                                     : product_of<kHidden, RLK_GRAD_F32>(kind, a, n_rows, stream);
 }
 
+// Short tiles up to 128 rows (128 rows of the 151936 x 4096 head 843 us with the
+// logits, as with Large; 256 rows 1092 and 930).
 template <int kType>
 static int32_t weight_product(const Args& a, int64_t n_rows, hipStream_t stream) {
   if (n_rows <= 128) return product<Short, kWeight, kType>(a, n_rows, stream);
@@ -701,7 +705,6 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
     if ((st = launched()) != RLK_OK) return st;
   }
 
-  const bool by_halves = in_halves(n_rows);
   const int64_t first = static_cast<int64_t>(rank) * p.local * p.width;  // the rank's first column
   Args a{};
   a.h = h;
@@ -715,7 +718,16 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
   a.shards = p.at_once;
   a.d = static_cast<int>(d);
   a.ldgw = grad_weight_stride;
-  const bool one_by_one = alone(n_rows, d, p.at_once, by_halves);
+  // Whether grad_hidden's shards are summed one after another, each added to the
+  // ones before as it ends: where that takes no longer than all at once, which
+  // writes and reads a partial sum for every shard (8192 rows: 25.1 and 23.4 ms).
+  a.shards = 1;
+  const bool one_by_one = tiles_for<kHidden>(a, n_rows).cost * p.at_once <= [&] {
+    Args b = a;
+    b.shards = p.at_once;
+    return tiles_for<kHidden>(b, n_rows).cost;
+  }();
+  a.shards = p.at_once;
   float* waiting = parts + static_cast<int64_t>(one_by_one || p.at_once == 1 ? 0 : p.at_once) * p.part_step;
   for (int s = 0; s < p.local; s += p.at_once) {
     const int64_t c0 = static_cast<int64_t>(s) * p.width;  // columns counted from the rank's first
@@ -725,12 +737,7 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
     a.cols = left < 0 ? 0 : (left < most ? left : most);
     a.w = n_rows > 0 && a.cols > 0 ? weight + c0 * weight_stride : weight;
     if (n_rows > 0 && a.cols > 0) {
-      if (n_rows <= Few::BM)
-        st = product<Few, kLogits, RLK_GRAD_BF16>(a, n_rows, stream);
-      else if (by_halves)
-        st = product<Half, kLogits, RLK_GRAD_BF16>(a, n_rows, stream);
-      else
-        st = product<Large, kLogits, RLK_GRAD_BF16>(a, n_rows, stream);
+      st = product_of<kLogits, RLK_GRAD_BF16>(tiles_for<kLogits>(a, n_rows).kind, a, n_rows, stream);
       if (st != RLK_OK) return st;
     }
     if (grad_hidden && n_rows > 0) {
@@ -756,7 +763,7 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
           one.w = one.cols > 0 ? a.w + skip * weight_stride : a.w;
           one.g = a.g + k * p.g_step;
           one.hid = sum_to(s + k, s + k + 1 == p.local);
-          if ((st = hidden_product(one, n_rows, by_halves, stream)) != RLK_OK) return st;
+          if ((st = hidden_product(tiles_for<kHidden>(one, n_rows).kind, one, n_rows, stream)) != RLK_OK) return st;
         }
       } else {
         a.hid = HiddenOut{};
@@ -764,7 +771,7 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
         a.hid.ldo = d;
         a.hid.type = RLK_GRAD_F32;
         a.hid.shard_step = p.part_step;
-        if ((st = hidden_product(a, n_rows, by_halves, stream)) != RLK_OK) return st;
+        if ((st = hidden_product(tiles_for<kHidden>(a, n_rows).kind, a, n_rows, stream)) != RLK_OK) return st;
         k_combine<<<dim3(vec_grid(n_rows * (d / 4))), dim3(256), 0, stream>>>(
             parts, p.part_step, p.at_once, sum_to(s / p.at_once, s + p.at_once == p.local), n_act,
             static_cast<int>(d));

@@ -126,6 +126,23 @@ def test_matches_the_oracle(n, d, vr, vp, terms):
     close(gw, want_w, mag_w, extra_w, n, True, "grad_weight")
 
 
+@pytest.mark.parametrize("n", [1, 64, 128, 200, 256, 513])
+@pytest.mark.parametrize("vr,vp", [(201, 256), (2049, 2112), (1, 64)])
+def test_the_last_column_of_an_odd_vocabulary(n, vr, vp):
+    """Every row's target is the last column, whose place in its shard is odd: the
+    largest part of G lies in half a word at the end of each row."""
+    import torch
+    say(f"case: {n} rows, last column of {vr}")
+    p = Problem(n, n, 128, vr, vp, temps=(1.0,), lean=0.0)
+    p.target[:] = vr - 1
+    p.tg = torch.from_numpy(p.target).to("cuda:0")
+    p.forward()
+    gh, gw = run_all(p)
+    want_h, want_w, mag_h, mag_w, extra_h, extra_w = p.want()
+    close(gh, want_h, mag_h, extra_h, vr, True, "grad_hidden")
+    close(gw, want_w, mag_w, extra_w, n, True, "grad_weight")
+
+
 def run_all(p, terms="ref", **more):
     a, kw = p.args(terms)
     kw.update(more)
