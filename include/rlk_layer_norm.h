@@ -13,12 +13,13 @@
  *   dx      = r * (g - c1 - xhat * mean(g * xhat)), c1 = mean(g) for
  *             RLK_NORM_LAYER, 0 for RLK_NORM_RMS
  *   dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy
- * A row whose dy holds only zeros has dx = 0 and adds nothing to dweight,
- * whatever x, m and r hold (padding).
+ * A row whose dy holds only zeros has dx = 0, and a dy of 0 adds nothing to
+ * dweight, whatever x, m and r hold there (padding).
  *
  * Order: y, the statistics and dx of a row depend on the row and d alone:
  * identical rows give identical bytes in any batch. dweight and dbias are
- * summed in an order that depends on n_rows and d alone (no atomics).
+ * summed in an order that depends on n_rows, d and whether dx takes the place of
+ * x or dy (no atomics).
  *
  * Types: x (and dx) BF16 or float32, weight and bias BF16 or float32 (both the
  * same), y and dy BF16, statistics, dweight and dbias float32.

@@ -200,6 +200,7 @@ def summary_bytes(n_rows: int, vocab_padded: int, vocab_real: int, groups: int =
 # torch marshalling
 # ---------------------------------------------------------------------------
 
+@functools.lru_cache(maxsize=None)
 def _torch():
     import torch
     return torch
@@ -1043,25 +1044,30 @@ def layer_norm_backward_workspace_bytes(n_rows: int, d: int) -> int:
     return _norm_need(int(n_rows), int(d))
 
 
-def _matrix(x, name, device=None, shape=None, f32_too=True):
-    """(row stride, RLK_TYPE_*) of a 2-D device tensor of BF16 (or float32) values with contiguous rows."""
+def _matrix(x, name, like=None, f32_too=True):
+    """(row stride, RLK_TYPE_*) of a 2-D device tensor of BF16 (or float32) values with contiguous rows, of the shape and
+    on the device of ``like``."""
     torch = _torch()
-    types = (torch.bfloat16, torch.float32) if f32_too else (torch.bfloat16,)
-    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in types or x.is_cpu or x.stride(1) != 1 or \
-            (device is not None and x.device != device) or (shape is not None and x.shape != shape):
-        raise ValueError(f"{name} must be a 2-D device tensor of {' or '.join(str(t) for t in types)} values with contiguous "
-                         f"rows" + (f", of shape {tuple(shape)} on {device}" if shape is not None else ""))
-    stride = x.stride(0) if x.shape[0] > 1 else max((x.stride(0) + 7) // 8 * 8, (x.shape[1] + 7) // 8 * 8)
-    return stride, TYPE_BF16 if x.dtype is torch.bfloat16 else TYPE_F32
+    if isinstance(x, torch.Tensor) and not x.is_cpu and (like is None or (x.shape == like.shape and x.device == like.device)):
+        kind = x.dtype
+        if kind is torch.bfloat16 or (f32_too and kind is torch.float32):
+            strides = x.stride()
+            if len(strides) == 2 and strides[1] == 1:
+                n, d = x.shape
+                return strides[0] if n > 1 else max((strides[0] + 7) // 8 * 8, (d + 7) // 8 * 8), \
+                    TYPE_BF16 if kind is torch.bfloat16 else TYPE_F32
+    raise ValueError(f"{name} must be a 2-D device tensor of bfloat16{' or float32' if f32_too else ''} values with contiguous rows"
+                     + (f", of shape {tuple(like.shape)} on {like.device}" if like is not None else ""))
 
 
 def _norm_weight(weight, bias, d, device):
     torch = _torch()
-    if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("weight must be a bfloat16 or float32 tensor")
-    _given(device, (weight, (d,), weight.dtype, "weight"))
-    if bias is not None:
-        _given(device, (bias, (d,), weight.dtype, "bias"))
+    for v, name in ((weight, "weight"), (bias, "bias")):
+        if v is None and name == "bias":
+            continue
+        if not (isinstance(v, torch.Tensor) and (v.dtype is torch.bfloat16 or v.dtype is torch.float32) and v.shape == (d,) and
+                v.device == device and v.is_contiguous() and v.dtype is weight.dtype):
+            raise ValueError(f"{name} must be a contiguous bfloat16 or float32 tensor of shape {(d,)} on {device}, bias of weight's type")
     return TYPE_BF16 if weight.dtype is torch.bfloat16 else TYPE_F32
 
 
@@ -1080,8 +1086,10 @@ def layer_norm(x, weight, bias=None, *, rms: bool = False, eps: float = 1e-6, re
     dev = x.device
     wt = _norm_weight(weight, bias, d, dev)
     if out is None:
-        out = torch.empty((n, d), dtype=torch.bfloat16, device=dev)
-    ldo = _matrix(out, "out", dev, x.shape, f32_too=False)[0]
+        out = torch.empty_like(x) if xt == TYPE_BF16 and ldx == d else torch.empty((n, d), dtype=torch.bfloat16, device=dev)
+        ldo = d
+    else:
+        ldo = _matrix(out, "out", x, f32_too=False)[0]
     if mean_out is not None or (return_stats and not rms):
         mean_out = _out(mean_out, (n,), torch.float32, dev, "mean_out")
     if rstd_out is not None or return_stats:
@@ -1106,7 +1114,7 @@ def layer_norm_backward(grad_out, x, weight, mean, rstd, *, rms: bool = False, x
     f32 = torch.float32
     lddy = _matrix(grad_out, "grad_out", f32_too=False)[0]
     dev = grad_out.device
-    ldx, xt = _matrix(x, "x", dev, grad_out.shape)
+    ldx, xt = _matrix(x, "x", grad_out)
     n, d = x.shape
     wt = _norm_weight(weight, None, d, dev)
     _given(dev, (rstd, (n,), f32, "rstd"))
@@ -1116,10 +1124,12 @@ def layer_norm_backward(grad_out, x, weight, mean, rstd, *, rms: bool = False, x
         raise ValueError("accumulate needs given gradients")
     dx, lddx = None, d
     if x_grad:
-        grad_x = torch.empty((n, d), dtype=x.dtype, device=dev) if grad_x is None else grad_x
-        lddx, gt = _matrix(grad_x, "grad_x", dev, x.shape)
-        if gt != xt:
-            raise ValueError("grad_x must have x's type")
+        if grad_x is None:
+            grad_x = torch.empty_like(x) if ldx == d else torch.empty((n, d), dtype=x.dtype, device=dev)
+        else:
+            lddx, gt = _matrix(grad_x, "grad_x", x)
+            if gt != xt:
+                raise ValueError("grad_x must have x's type")
         dx = grad_x.data_ptr()
     dw = db = None
     if weight_grad:

@@ -196,12 +196,15 @@ __global__ __launch_bounds__(kBound) void k_norm(const void* x, int64_t n_rows, 
   }
 }
 
+// A value's part of dweight: nothing where dy is 0, whatever stands there.
+__device__ __forceinline__ float weight_term(float dy, float hat) { return dy != 0.0f ? dy * hat : 0.0f; }
+
 // parts: per workgroup d sums of dy * xhat, then (kBias) d sums of dy.
-template <int kX, int kW, bool kBias, int kBound>
-__global__ __launch_bounds__(kBound) void k_norm_backward(
-    const uint16_t* dy, int64_t lddy, const void* x, int64_t n_rows, int d, int64_t ldx,
-    const void* __restrict__ weight, int rms, const float* __restrict__ mean, const float* __restrict__ rstd, void* dx,
-    int64_t lddx, float* __restrict__ parts) {
+template <int kX, int kW, bool kBias>
+__device__ __forceinline__ void backward_rows(const uint16_t* dy, int64_t lddy, const void* x, int64_t n_rows, int d,
+                                              int64_t ldx, const void* __restrict__ weight, int rms,
+                                              const float* __restrict__ mean, const float* __restrict__ rstd, void* dx,
+                                              int64_t lddx, float* __restrict__ parts, int step) {
   __shared__ float2 part[2][kMaxWaves];
   __shared__ int any[2];
   const int threads = static_cast<int>(blockDim.x);
@@ -230,7 +233,7 @@ __global__ __launch_bounds__(kBound) void k_norm_backward(
   if (threadIdx.x < 2) any[threadIdx.x] = 0;
   __syncthreads();
   int turn = 0;
-  for (; row < n_rows; row += gridDim.x) {  // uniform across the workgroup
+  for (; row < n_rows; row += step) {  // uniform across the workgroup
     float f[kVecs][8], g[kVecs][8];
     uint32_t some = 0;
 #pragma unroll
@@ -239,7 +242,7 @@ __global__ __launch_bounds__(kBound) void k_norm_backward(
       widen<RLK_TYPE_BF16>(up[v], g[v]);
       some |= (up[v].v.x | up[v].v.y | up[v].v.z | up[v].v.w) & 0x7FFF7FFFu;
     }
-    const int64_t next = row + gridDim.x;
+    const int64_t next = row + step;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v)
       if (in[v] && next < n_rows) {
@@ -265,7 +268,7 @@ __global__ __launch_bounds__(kBound) void k_norm_backward(
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float hat = live ? (f[v][e] - m) * r : 0.0f;
-        dw[v][e] = dw[v][e] + g[v][e] * hat;
+        dw[v][e] = dw[v][e] + weight_term(g[v][e], hat);
         if (kBias) db[v][e] = db[v][e] + g[v][e];
         f[v][e] = hat;
         g[v][e] = g[v][e] * wv[e];
@@ -298,10 +301,19 @@ __global__ __launch_bounds__(kBound) void k_norm_backward(
     }
 }
 
-// Column c of [count][ld] partial sums: 64 threads a column group of 16, each a
-// fixed share of the rows, joined in order.
+template <int kX, int kW, bool kBias, int kBound>
+__global__ __launch_bounds__(kBound) void k_norm_backward(
+    const uint16_t* dy, int64_t lddy, const void* x, int64_t n_rows, int d, int64_t ldx,
+    const void* __restrict__ weight, int rms, const float* __restrict__ mean, const float* __restrict__ rstd, void* dx,
+    int64_t lddx, float* __restrict__ parts) {
+  backward_rows<kX, kW, kBias>(dy, lddy, x, n_rows, d, ldx, weight, rms, mean, rstd, dx, lddx, parts,
+                               static_cast<int>(gridDim.x));
+}
+
+// Column c of [count][ld] partial sums: 32 threads a column, each a fixed share of
+// the rows in four sums, joined in order.
 constexpr int kSumThreads = 1024;
-constexpr int kSumCols = 16;
+constexpr int kSumCols = 32;
 constexpr int kSumRows = kSumThreads / kSumCols;
 
 __global__ __launch_bounds__(kSumThreads) void k_norm_sums(const float* __restrict__ parts, int count, int ld, int d,
@@ -311,10 +323,20 @@ __global__ __launch_bounds__(kSumThreads) void k_norm_sums(const float* __restri
   const int c = static_cast<int>(threadIdx.x) % kSumCols;
   const int k = static_cast<int>(threadIdx.x) / kSumCols;
   const int col = static_cast<int>(blockIdx.x) * kSumCols + c;
-  float a = 0.0f;
-  if (col < ld)
-    for (int r = k; r < count; r += kSumRows) a = a + parts[static_cast<int64_t>(r) * ld + col];
-  s[k][c] = a;
+  float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (col < ld) {
+    const float* __restrict__ p = parts + col;
+    int r = k;
+    for (; r + 7 * kSumRows < count; r += 8 * kSumRows) {  // eight loads in flight
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = p[static_cast<int64_t>(r + u * kSumRows) * ld];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) a[u & 3] = a[u & 3] + x[u];
+    }
+    for (; r < count; r += kSumRows) a[0] = a[0] + p[static_cast<int64_t>(r) * ld];
+  }
+  s[k][c] = (a[0] + a[1]) + (a[2] + a[3]);
   __syncthreads();
 #pragma unroll
   for (int o = kSumRows / 2; o >= 1; o >>= 1) {
@@ -325,6 +347,66 @@ __global__ __launch_bounds__(kSumThreads) void k_norm_sums(const float* __restri
     float* to = col < d ? dweight : dbias;
     const int at = col < d ? col : col - d;
     if (to) to[at] = accumulate ? to[at] + s[0][c] : s[0][c];
+  }
+}
+
+// Few rows: a workgroup a row for dx, and beside them workgroups that each sum 64
+// columns of dweight and dbias over all rows: one launch and no partial sums, for a
+// second read of x and dy (so dx may not take their place here).
+template <int kX, int kW, int kBound>
+__global__ __launch_bounds__(kBound) void k_norm_backward_few(
+    const uint16_t* __restrict__ dy, int64_t lddy, const void* __restrict__ x, int n_rows, int d, int64_t ldx,
+    const void* __restrict__ weight, int rms, const float* __restrict__ mean, const float* __restrict__ rstd,
+    void* __restrict__ dx, int64_t lddx, float* __restrict__ dweight, float* __restrict__ dbias, int accumulate,
+    int row_blocks) {
+  __shared__ float2 part[kMaxWaves][64];
+  const int threads = static_cast<int>(blockDim.x);
+  const int waves = threads >> 6;
+  const int wave = static_cast<int>(threadIdx.x) >> 6;
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  if (static_cast<int>(blockIdx.x) < row_blocks) {
+    backward_rows<kX, kW, false>(dy, lddy, x, n_rows, d, ldx, weight, rms, mean, rstd, dx, lddx, nullptr, row_blocks);
+    return;
+  }
+  const int first = (static_cast<int>(blockIdx.x) - row_blocks) * 64;
+  const int col = first + (lane & 7) * 8;  // 8 lanes a row
+  float dw[8], db[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) dw[e] = db[e] = 0.0f;
+  if (col < d)
+    for (int row = static_cast<int>(threadIdx.x) >> 3; row < n_rows; row += threads >> 3) {
+      float f[8], g[8];
+      widen<kX>(load8<kX>(x, row * ldx + col), f);
+      widen<RLK_TYPE_BF16>(load8<RLK_TYPE_BF16>(dy, row * lddy + col), g);
+      const float r = rstd[row];
+      const float m = rms ? 0.0f : mean[row];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dw[e] = dw[e] + weight_term(g[e], (f[e] - m) * r);
+        db[e] = db[e] + g[e];
+      }
+    }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+#pragma unroll
+    for (int o = 8; o <= 32; o *= 2) {
+      dw[e] = dw[e] + __shfl_xor(dw[e], o);
+      db[e] = db[e] + __shfl_xor(db[e], o);
+    }
+  if (lane < 8) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[wave][lane * 8 + e] = make_float2(dw[e], db[e]);
+  }
+  __syncthreads();
+  const int at = first + lane;
+  if (wave == 0 && at < d) {
+    float2 s = part[0][lane];
+    for (int k = 1; k < waves; ++k) {
+      s.x = s.x + part[k][lane].x;
+      s.y = s.y + part[k][lane].y;
+    }
+    if (dweight) dweight[at] = accumulate ? dweight[at] + s.x : s.x;
+    if (dbias) dbias[at] = accumulate ? dbias[at] + s.y : s.y;
   }
 }
 
@@ -342,7 +424,8 @@ static int threads_for(int64_t d) { return static_cast<int>((d / 8 + kVecs * 64 
 // Workgroups of a walk over the rows: `resident` threads a compute unit, all with
 // the same number of rows but the last.
 static int grid_for(int64_t n_rows, int64_t d, int resident) {
-  const int64_t most = static_cast<int64_t>(kUnits) * (resident / threads_for(d));
+  const int64_t fit = resident / threads_for(d);
+  const int64_t most = static_cast<int64_t>(kUnits) * (fit > 0 ? fit : 1);
   const int64_t rows = (n_rows + most - 1) / most;
   return rows > 0 ? static_cast<int>((n_rows + rows - 1) / rows) : 0;
 }
@@ -373,7 +456,9 @@ static void by_type(int x_type, int w_type, unsigned threads, const F& f) {
     typed(S());
 }
 
-constexpr int kBackwardThreads = 1024;
+constexpr int kBackwardThreads = 768;
+// Rows up to which dweight's columns are summed beside the rows in one launch.
+constexpr int kFewRows = 128;
 
 }  // namespace rlk_norm_layer
 
@@ -404,7 +489,8 @@ int32_t rlk_layer_norm(const void* x, int32_t x_type, int64_t n_rows, int64_t d,
 size_t rlk_layer_norm_backward_workspace_bytes(int64_t n_rows, int64_t d) {
   using namespace rlk_norm_layer;
   if (!sizes_ok(n_rows, d)) return 0;
-  const int64_t most = static_cast<int64_t>(kUnits) * (kBackwardThreads / threads_for(d));
+  const int64_t fit = kBackwardThreads / threads_for(d);
+  const int64_t most = static_cast<int64_t>(kUnits) * (fit > 0 ? fit : 1);
   return static_cast<size_t>(n_rows < most ? n_rows : most) * static_cast<size_t>(d) * 8 + 16;
 }
 
@@ -434,6 +520,16 @@ int32_t rlk_layer_norm_backward(const uint16_t* dy, int64_t dy_stride, const voi
   float* parts = sums ? static_cast<float*>(workspace) : nullptr;
   const int with_bias = dbias != nullptr;
   int32_t st;
+  if (sums && n_rows > 0 && n_rows <= kFewRows && dx != x && dx != static_cast<const void*>(dy)) {
+    const int rows = dx ? static_cast<int>(n_rows) : 0;
+    const dim3 grid(rows + static_cast<int>((d + 63) / 64)), block(threads_for(d));
+    by_type(x_type, weight_type, block.x, [&](auto xt, auto wt, auto bound) {
+      k_norm_backward_few<xt, wt, bound><<<grid, block, 0, stream>>>(
+          dy, dy_stride, x, static_cast<int>(n_rows), static_cast<int>(d), x_stride, weight, rms, mean, rstd, dx,
+          dx_stride, dweight, dbias, accumulate, rows);
+    });
+    return launched();
+  }
   if (n_rows > 0) {
     const dim3 grid(teams), block(threads_for(d));
     by_type(x_type, weight_type, block.x, [&](auto xt, auto wt, auto bound) {

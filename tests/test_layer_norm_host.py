@@ -94,11 +94,13 @@ def test_binding_checks_tensors():
     assert rlk._matrix(x, "x") == (64, rlk.TYPE_BF16)
     assert rlk._matrix(x[:1], "x") == (64, rlk.TYPE_BF16)
     assert rlk._norm_weight(w, None, 64, META) == rlk.TYPE_BF16
-    for bad in (torch.zeros((4, 64), dtype=torch.bfloat16), x.to(torch.float16), x[0], x[:, ::2], None):
+    for bad in (torch.zeros((4, 64), dtype=torch.bfloat16), x.to(torch.float16), x[0], x[:, ::2], None, x[None]):
         with pytest.raises(ValueError):
             rlk._matrix(bad, "x")
     with pytest.raises(ValueError):
         rlk._matrix(x.float(), "out", f32_too=False)
+    with pytest.raises(ValueError, match="of shape"):
+        rlk._matrix(x[:3], "grad_x", x)
     for weight, bias in ((None, None), (w.to(torch.float16), None), (w[:32], None), (w, w.float()), (torch.zeros(64), None)):
         with pytest.raises(ValueError):
             rlk._norm_weight(weight, bias, 64, META)
