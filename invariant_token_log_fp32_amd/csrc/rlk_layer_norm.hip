@@ -3,7 +3,7 @@
 //
 // Kernels:
 //   k_norm           a workgroup of just the waves that hold a row in registers
-//                    (16 values a thread) goes through rows, the next row's loads
+//                    (16 or 32 values a thread) goes through rows, the next row's loads
 //                    in flight while it reduces one; the weight stays in
 //                    registers. Mean and variance are two sums over the values
 //                    in registers, so the variance has no cancellation.
@@ -32,8 +32,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int64_t kMaxRows = int64_t(1) << 22;
 constexpr int64_t kMaxLd = int64_t(1) << 21;
 constexpr int kMaxD = 16384;
-constexpr int kVecs = 2;        // 8-value vectors a thread
-constexpr int kMaxThreads = kMaxD / (8 * kVecs);
+constexpr int kMaxThreads = 512;
 constexpr int kMaxWaves = kMaxThreads / 64;
 constexpr int kUnits = 256;     // compute units the walk is cut for (a fixed number: the order of the sums depends on it)
 
@@ -124,7 +123,7 @@ __device__ __forceinline__ float2 sum_over(float a, float b, int waves, float2 (
   return s;
 }
 
-template <int kX, int kW, int kBound>
+template <int kX, int kW, int kVecs, int kBound>
 __global__ __launch_bounds__(kBound) void k_norm(const void* x, int64_t n_rows, int d, int64_t ldx,
                                                  const void* __restrict__ weight, const void* __restrict__ bias,
                                                  int rms, float eps, uint16_t* y, int64_t ldy,
@@ -200,7 +199,7 @@ __global__ __launch_bounds__(kBound) void k_norm(const void* x, int64_t n_rows, 
 __device__ __forceinline__ float weight_term(float dy, float hat) { return dy != 0.0f ? dy * hat : 0.0f; }
 
 // parts: per workgroup d sums of dy * xhat, then (kBias) d sums of dy.
-template <int kX, int kW, bool kBias>
+template <int kX, int kW, int kVecs, bool kBias>
 __device__ __forceinline__ void backward_rows(const uint16_t* dy, int64_t lddy, const void* x, int64_t n_rows, int d,
                                               int64_t ldx, const void* __restrict__ weight, int rms,
                                               const float* __restrict__ mean, const float* __restrict__ rstd, void* dx,
@@ -301,12 +300,12 @@ __device__ __forceinline__ void backward_rows(const uint16_t* dy, int64_t lddy, 
     }
 }
 
-template <int kX, int kW, bool kBias, int kBound>
+template <int kX, int kW, int kVecs, bool kBias, int kBound>
 __global__ __launch_bounds__(kBound) void k_norm_backward(
     const uint16_t* dy, int64_t lddy, const void* x, int64_t n_rows, int d, int64_t ldx,
     const void* __restrict__ weight, int rms, const float* __restrict__ mean, const float* __restrict__ rstd, void* dx,
     int64_t lddx, float* __restrict__ parts) {
-  backward_rows<kX, kW, kBias>(dy, lddy, x, n_rows, d, ldx, weight, rms, mean, rstd, dx, lddx, parts,
+  backward_rows<kX, kW, kVecs, kBias>(dy, lddy, x, n_rows, d, ldx, weight, rms, mean, rstd, dx, lddx, parts,
                                static_cast<int>(gridDim.x));
 }
 
@@ -353,7 +352,7 @@ __global__ __launch_bounds__(kSumThreads) void k_norm_sums(const float* __restri
 // Few rows: a workgroup a row for dx, and beside them workgroups that each sum 64
 // columns of dweight and dbias over all rows: one launch and no partial sums, for a
 // second read of x and dy (so dx may not take their place here).
-template <int kX, int kW, int kBound>
+template <int kX, int kW, int kVecs, int kBound>
 __global__ __launch_bounds__(kBound) void k_norm_backward_few(
     const uint16_t* __restrict__ dy, int64_t lddy, const void* __restrict__ x, int n_rows, int d, int64_t ldx,
     const void* __restrict__ weight, int rms, const float* __restrict__ mean, const float* __restrict__ rstd,
@@ -365,7 +364,7 @@ __global__ __launch_bounds__(kBound) void k_norm_backward_few(
   const int wave = static_cast<int>(threadIdx.x) >> 6;
   const int lane = static_cast<int>(threadIdx.x) & 63;
   if (static_cast<int>(blockIdx.x) < row_blocks) {
-    backward_rows<kX, kW, false>(dy, lddy, x, n_rows, d, ldx, weight, rms, mean, rstd, dx, lddx, nullptr, row_blocks);
+    backward_rows<kX, kW, kVecs, false>(dy, lddy, x, n_rows, d, ldx, weight, rms, mean, rstd, dx, lddx, nullptr, row_blocks);
     return;
   }
   const int first = (static_cast<int>(blockIdx.x) - row_blocks) * 64;
@@ -419,7 +418,12 @@ static bool sizes_ok(int64_t n_rows, int64_t d) {
 }
 static bool stride_ok(int64_t ld, int64_t d) { return ld >= d && ld % 8 == 0 && ld <= kMaxLd; }
 
-static int threads_for(int64_t d) { return static_cast<int>((d / 8 + kVecs * 64 - 1) / (kVecs * 64)) * 64; }
+// 8-value vectors a thread: 2, and 4 where a row needs more than 512 threads of 2.
+static int vecs_for(int64_t d) { return d <= 16 * kMaxThreads ? 2 : 4; }
+static int threads_for(int64_t d) {
+  const int64_t a_wave = vecs_for(d) * 64;
+  return static_cast<int>((d / 8 + a_wave - 1) / a_wave) * 64;
+}
 
 // Workgroups of a walk over the rows: `resident` threads a compute unit, all with
 // the same number of rows but the last.
@@ -432,17 +436,20 @@ static int grid_for(int64_t n_rows, int64_t d, int resident) {
 
 constexpr int kForwardThreads = 2048;   // resident threads a compute unit
 
-// Calls f with the types, and the largest workgroup (registers: 128 a thread
-// where rows are longer than 4096 values), as constants.
+// Calls f with the types, the vectors a thread and the largest workgroup as
+// constants (a bound of 1024 threads leaves 128 registers: spills, and 403 us
+// instead of 285 for the backward of 32768 x 8192).
 template <typename F>
-static void by_type(int x_type, int w_type, unsigned threads, const F& f) {
+static void by_type(int x_type, int w_type, int64_t d, const F& f) {
   using B = std::integral_constant<int, RLK_TYPE_BF16>;
   using S = std::integral_constant<int, RLK_TYPE_F32>;
   const auto sized = [&](auto xt, auto wt) {
-    if (threads <= 256)
-      f(xt, wt, std::integral_constant<int, 256>());
+    if (threads_for(d) <= 256)
+      f(xt, wt, std::integral_constant<int, 2>(), std::integral_constant<int, 256>());
+    else if (vecs_for(d) == 2)
+      f(xt, wt, std::integral_constant<int, 2>(), std::integral_constant<int, kMaxThreads>());
     else
-      f(xt, wt, std::integral_constant<int, kMaxThreads>());
+      f(xt, wt, std::integral_constant<int, 4>(), std::integral_constant<int, kMaxThreads>());
   };
   const auto typed = [&](auto xt) {
     if (w_type == RLK_TYPE_BF16)
@@ -456,8 +463,17 @@ static void by_type(int x_type, int w_type, unsigned threads, const F& f) {
     typed(S());
 }
 
+// Resident threads a compute unit in the backward walk: 512 for large batches (65536
+// x 4096 281 us, with 768 326; 16384 x 4096 82 and 86), 768 for others (65536 x 512 54
+// us, with 512 61; 8192 x 4096 46 and 47).
 constexpr int kBackwardThreads = 768;
-// Rows up to which dweight's columns are summed beside the rows in one launch.
+constexpr int kBackwardThreadsLarge = 512;
+constexpr int64_t kLarge = int64_t(1) << 25;  // values
+static int backward_grid(int64_t n_rows, int64_t d) {
+  return grid_for(n_rows, d, n_rows * d > kLarge ? kBackwardThreadsLarge : kBackwardThreads);
+}
+// Rows up to which dweight's columns are summed beside the rows in one launch (37 x
+// 1000 16 us a call, in two launches 19; 128 x 4096 as long either way).
 constexpr int kFewRows = 128;
 
 }  // namespace rlk_norm_layer
@@ -479,8 +495,8 @@ int32_t rlk_layer_norm(const void* x, int32_t x_type, int64_t n_rows, int64_t d,
       !aligned(rstd_out, 4))
     return RLK_ERR_ALIGN;
   const dim3 grid(grid_for(n_rows, d, kForwardThreads)), block(threads_for(d));
-  by_type(x_type, weight_type, block.x, [&](auto xt, auto wt, auto bound) {
-    k_norm<xt, wt, bound><<<grid, block, 0, stream>>>(x, n_rows, static_cast<int>(d), x_stride, weight, bias,
+  by_type(x_type, weight_type, d, [&](auto xt, auto wt, auto vecs, auto bound) {
+    k_norm<xt, wt, vecs, bound><<<grid, block, 0, stream>>>(x, n_rows, static_cast<int>(d), x_stride, weight, bias,
                                                       kind == RLK_NORM_RMS, eps, y, y_stride, mean_out, rstd_out);
   });
   return launched();
@@ -516,15 +532,15 @@ int32_t rlk_layer_norm_backward(const uint16_t* dy, int64_t dy_stride, const voi
     return RLK_ERR_ALIGN;
   if (sums && workspace_bytes < rlk_layer_norm_backward_workspace_bytes(n_rows, d)) return RLK_ERR_WORKSPACE;
   if (n_rows == 0 && (!sums || accumulate)) return RLK_OK;
-  const int teams = grid_for(n_rows, d, kBackwardThreads);
+  const int teams = backward_grid(n_rows, d);
   float* parts = sums ? static_cast<float*>(workspace) : nullptr;
   const int with_bias = dbias != nullptr;
   int32_t st;
   if (sums && n_rows > 0 && n_rows <= kFewRows && dx != x && dx != static_cast<const void*>(dy)) {
     const int rows = dx ? static_cast<int>(n_rows) : 0;
     const dim3 grid(rows + static_cast<int>((d + 63) / 64)), block(threads_for(d));
-    by_type(x_type, weight_type, block.x, [&](auto xt, auto wt, auto bound) {
-      k_norm_backward_few<xt, wt, bound><<<grid, block, 0, stream>>>(
+    by_type(x_type, weight_type, d, [&](auto xt, auto wt, auto vecs, auto bound) {
+      k_norm_backward_few<xt, wt, vecs, bound><<<grid, block, 0, stream>>>(
           dy, dy_stride, x, static_cast<int>(n_rows), static_cast<int>(d), x_stride, weight, rms, mean, rstd, dx,
           dx_stride, dweight, dbias, accumulate, rows);
     });
@@ -532,9 +548,9 @@ int32_t rlk_layer_norm_backward(const uint16_t* dy, int64_t dy_stride, const voi
   }
   if (n_rows > 0) {
     const dim3 grid(teams), block(threads_for(d));
-    by_type(x_type, weight_type, block.x, [&](auto xt, auto wt, auto bound) {
+    by_type(x_type, weight_type, d, [&](auto xt, auto wt, auto vecs, auto bound) {
       const auto go = [&](auto with) {
-        k_norm_backward<xt, wt, with, bound><<<grid, block, 0, stream>>>(
+        k_norm_backward<xt, wt, vecs, with, bound><<<grid, block, 0, stream>>>(
             dy, dy_stride, x, n_rows, static_cast<int>(d), x_stride, weight, rms, mean, rstd, dx, dx_stride, parts);
       };
       if (with_bias)
