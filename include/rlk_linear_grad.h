@@ -30,7 +30,7 @@
  * ((s0+s1)+(s2+s3))+((s4+s5)+(s6+s7)). It depends on the row and the column
  * geometry alone: identical rows give identical bytes in any batch, and the
  * vocabulary-parallel form below gives the bytes of the whole. grad_weight is
- * summed over the rows that have a gradient, in row order, 16 rows a matrix
+ * summed over the rows that have a gradient, in row order, 32 rows a matrix
  * instruction: rows without one do not change its bytes.
  *
  * Shapes: as rlk_linear.h, and vocab_padded at most 2^22.
@@ -96,10 +96,10 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
                                  int32_t grad_weight_type, void* workspace, size_t workspace_bytes,
                                  hipStream_t stream);
 
-/* Bytes of workspace for any types and either output: the rows' hidden states,
- * BF16 gradients of at least one and at most two canonical shards of logits (all of
- * them for few rows), and float32 partial sums of grad_hidden. 0 for arguments that the
- * call refuses. */
+/* Bytes of workspace for any types and either output: the rows' hidden states, the
+ * BF16 gradients of 1, 2, 4 or 8 canonical shards of logits (the most that take no
+ * more than 640 MiB together; one takes what it needs), and float32 partial sums of
+ * grad_hidden. Never less for more rows. 0 for arguments that the call refuses. */
 size_t rlk_linear_logp_backward_workspace_bytes(int64_t n_rows, int64_t d_model, const rlk_vocab_layout* layout);
 
 /* grad_hidden of the whole vocabulary from the ranks' float32 parts, rank r's

@@ -220,11 +220,11 @@ __device__ __forceinline__ FragAt<kAcross, kBlocks> frag_at(uint32_t base, int w
 template <bool kAcross, int kBlocks, int kWidth>
 __device__ __forceinline__ bf16x8 read_frag(const FragAt<kAcross, kBlocks>& f, int n) {
   if constexpr (kAcross) {
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(f.at[n]));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(f.at[n] + 4 * kWidth * 2));
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(static_cast<uintptr_t>(f.at[n])));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(static_cast<uintptr_t>(f.at[n] + 4 * kWidth * 2)));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   } else {
-    return *(LdsFrag)(f.at[0] + n * 16 * kSlice * 2);
+    return *(LdsFrag)(static_cast<uintptr_t>(f.at[0] + n * 16 * kSlice * 2));
   }
 }
 

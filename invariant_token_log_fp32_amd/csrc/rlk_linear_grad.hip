@@ -158,9 +158,9 @@ __global__ __launch_bounds__(256) void k_gather(const uint16_t* __restrict__ h, 
 // Tiles, with LDS for one workgroup a compute unit (three of Short). Large has the
 // largest wave part that the 512 registers hold, so the fewest LDS reads for a
 // multiplication; the smaller ones are for products whose Large tiles would leave
-// compute units idle. kCost: time of a tile's slice in hundredths of Large's,
-// measured on full GPUs (1500 rows of the 151936 x 4096 head: Large 8 rounds of
-// logits 868 us, Half 14 in 1121, Quarter 28 in 1279; Few twice that).
+// compute units idle. kCost: time of a tile's slice in hundredths of Large's, from
+// the logits of 1500 rows and 76000 columns at 4096 (Large 868 us for 1800 tiles, 8
+// rounds over the compute units; Half 1121 for 3600, 15; Quarter 1279 for 7152, 28).
 using Large = Shape<256, 256, 2, 2, 5, 1>;
 using Half = Shape<128, 256, 2, 2, 6, 1>;
 using Quarter = Shape<128, 128, 2, 2, 9, 1>;
@@ -591,8 +591,9 @@ static int32_t product(const Args& a, int64_t n_rows, hipStream_t stream) {
 }
 
 // The tiles for a product: the least rounds over the compute units times a round's
-// cost; the larger ones where that is equal. Few rows read little of what a tile
-// multiplies: 1 row 0.80 ms, with Large tiles 1.12.
+// cost; the larger ones where that is equal (64 rows of the 151936 x 4096 head: logits
+// and grad_hidden 527 us, with Large logits 604; 128 rows 675 and 705; 640 rows 1635,
+// with Few 2527).
 struct Choice {
   int kind;
   int64_t cost;
@@ -625,11 +626,14 @@ static int32_t hidden_product(int kind, const Args& a, int64_t n_rows, hipStream
                                      : product_of<kHidden, RLK_GRAD_F32>(kind, a, n_rows, stream);
 }
 
-// Short tiles up to 128 rows (128 rows of the 151936 x 4096 head 843 us with the
-// logits, as with Large; 256 rows 1092 and 930).
+// Short tiles for few rows and few tiles (64 rows of an 8000 x 512 head 33 us a call,
+// with Large 37; 77 of 50021 x 1088, 1000 Large tiles, 103 and 106), Large ones
+// otherwise (64 rows of 151936 x 4096, 9500 tiles: 630 us with the logits, with Short
+// 682; 128 rows 737 and 829; 256 rows 930 and 1065).
 template <int kType>
 static int32_t weight_product(const Args& a, int64_t n_rows, hipStream_t stream) {
-  if (n_rows <= 128) return product<Short, kWeight, kType>(a, n_rows, stream);
+  if (n_rows <= 128 && tile_count<Large, kWeight>(a, static_cast<int>(n_rows)) <= 1024)
+    return product<Short, kWeight, kType>(a, n_rows, stream);
   return product<Large, kWeight, kType>(a, n_rows, stream);
 }
 
@@ -720,7 +724,8 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
   a.ldgw = grad_weight_stride;
   // Whether grad_hidden's shards are summed one after another, each added to the
   // ones before as it ends: where that takes no longer than all at once, which
-  // writes and reads a partial sum for every shard (8192 rows: 25.1 and 23.4 ms).
+  // writes and reads a partial sum for every shard (8192 rows of the 151936 x 4096
+  // head: 15.5 ms with the logits, all at once 15.9).
   a.shards = 1;
   const bool one_by_one = tiles_for<kHidden>(a, n_rows).cost * p.at_once <= [&] {
     Args b = a;
