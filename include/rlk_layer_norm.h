@@ -54,7 +54,7 @@ enum { RLK_TYPE_BF16 = 0, RLK_TYPE_F32 = 1 };
  *   weight    [d] of weight_type; bias [d] of weight_type, or NULL
  *   eps       finite, >= 0
  *   y         BF16 [n_rows x d], row stride y_stride; it may be x itself (BF16,
- *             the same stride) and must not overlap it otherwise
+ *             the same stride; else RLK_ERR_SHAPE) and must not overlap it otherwise
  *   mean_out  [n_rows] float32, or NULL (RLK_NORM_RMS writes zeros)
  *   rstd_out  [n_rows] float32, or NULL
  * n_rows == 0 enqueues nothing. */
@@ -68,8 +68,8 @@ int32_t rlk_layer_norm(const void* x, int32_t x_type, int64_t n_rows, int64_t d,
  *   mean      [n_rows] float32, the forward's (RLK_NORM_RMS: not read, may be NULL)
  *   rstd      [n_rows] float32, the forward's
  *   dx        [n_rows x d] of x_type, row stride dx_stride, or NULL; it may be x
- *             itself (the same stride), or dy itself (BF16, the same stride), and
- *             must not overlap them otherwise
+ *             itself (the same stride), or dy itself (BF16, the same stride; else
+ *             RLK_ERR_SHAPE), and must not overlap them otherwise
  *   dweight, dbias
  *             [d] float32, 16-byte aligned, or NULL; at least one of the three
  *             outputs must be given (else RLK_ERR_NULL)

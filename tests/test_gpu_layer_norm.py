@@ -210,6 +210,26 @@ def test_bytes_do_not_depend_on_the_batch():
             assert torch.equal(rlk.layer_norm_backward(dy[rows], x[rows], w, m2, r2)[0], dx[rows])
 
 
+def test_strides_whose_offsets_pass_32_bits():
+    import torch
+    n, d, ld = 1100, 264, 1 << 21
+    say(f"case: {n} rows {ld} elements apart")
+    g = torch.Generator(device="cuda:0").manual_seed(9)
+    x = torch.randn((n, d), device="cuda:0", generator=g)
+    w = torch.randn(d, device="cuda:0", generator=g)
+    dy = torch.randn((n, d), device="cuda:0", generator=g).bfloat16()
+    far = [torch.empty((n, ld), dtype=t, device="cuda:0")[:, ld - d:] for t in
+           (torch.float32, torch.bfloat16, torch.bfloat16, torch.float32)]
+    far[0].copy_(x)
+    far[1].copy_(dy)
+    y, m, r = rlk.layer_norm(x, w, return_stats=True)
+    dx, dw, db = rlk.layer_norm_backward(dy, x, w, m, r, bias_grad=True)
+    fy, fm, fr = rlk.layer_norm(far[0], w, return_stats=True, out=far[2])
+    fx, fw, fb = rlk.layer_norm_backward(far[1], far[0], w, fm, fr, bias_grad=True, grad_x=far[3])
+    for a, b in ((fy, y), (fm, m), (fr, r), (fx, dx), (fw, dw), (fb, db)):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("n", [700, 40])
 def test_in_place_and_accumulated(n):
     import torch

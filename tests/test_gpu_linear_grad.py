@@ -292,6 +292,82 @@ def test_bytes_do_not_depend_on_the_batch(n, vr, vp):
         assert np.array_equal(bits(got), bits(gh)[pick])
 
 
+def first_rows(p, k, n):
+    """Arguments of a call with p's first n rows, of which the first k have a gradient."""
+    import torch
+    a, kw = p.args(rows=torch.arange(n, device="cuda:0"))
+    up = kw["grad_ref"].clone()
+    up[k:] = 0.0
+    return a, dict(kw, grad_ref=up)
+
+
+# Heads and row counts whose products take tiles of every size (64 and 128 x 128, 128 and
+# 256 x 256), sum grad_hidden's shards all at once and one after another, and have odd
+# ends of rows, columns and K in each.
+@pytest.mark.parametrize("d,vr,vp,rows", [(1024, 20000, 20032, (3, 100, 201, 300, 520, 1101)),
+                                          (1088, 13999, 14336, (129, 190, 700)), (2048, 19999, 20032, (130, 385, 641)),
+                                          (4096, 1000, 1024, (2, 300, 4096))])
+def test_bytes_do_not_depend_on_the_tiles(d, vr, vp, rows):
+    n = max(rows)
+    say(f"case: rows {rows} of a {vr} x {d} head")
+    p = Problem(21, n, d, vr, vp)
+    a, kw = first_rows(p, n, n)
+    whole, _ = rlk.linear_logp_backward(*a, **kw)
+    whole = bits(whole)
+    for k in rows:
+        say(f"  {k} rows")
+        a, kw = first_rows(p, k, k)
+        gh, gw = rlk.linear_logp_backward(*a, **kw)
+        assert np.array_equal(bits(gh), whole[:k])
+        if k < n:
+            a, kw = first_rows(p, k, n)
+            mh, mw = rlk.linear_logp_backward(*a, **kw)
+            assert np.array_equal(bits(mh)[:k], whole[:k]) and not bits(mh)[k:].any()
+            assert np.array_equal(bits(mw), bits(gw))
+
+
+def test_a_long_head_against_the_oracle():
+    say("case: 201 rows of a 20000 x 1024 head")
+    p = Problem(21, 201, 1024, 20000, 20032)
+    gh, gw = run_all(p)
+    want_h, want_w, mag_h, mag_w, extra_h, extra_w = p.want()
+    close(gh, want_h, mag_h, extra_h, 20000, True, "grad_hidden")
+    close(gw, want_w, mag_w, extra_w, 201, True, "grad_weight")
+
+
+def test_bytes_do_not_depend_on_how_many_shards_a_launch_takes():
+    """8, 4, 2 and 1 shards of logits in the workspace at a time."""
+    say("case: 9000 rows of a 151936 x 64 head")
+    p = Problem(22, 9000, 64, 151936, 152576)
+    a, kw = first_rows(p, 9000, 9000)
+    whole = bits(rlk.linear_logp_backward(*a, **kw)[0])
+    a, kw = first_rows(p, 500, 500)
+    gh, gw = rlk.linear_logp_backward(*a, **kw)
+    assert np.array_equal(bits(gh), whole[:500])
+    for n in (2600, 5000, 9000):
+        say(f"  {n} rows")
+        a, kw = first_rows(p, 500, n)
+        mh, mw = rlk.linear_logp_backward(*a, **kw)
+        assert np.array_equal(bits(mh)[:500], whole[:500]) and not bits(mh)[500:].any()
+        assert np.array_equal(bits(mw), bits(gw))
+
+
+def test_strides_whose_offsets_pass_32_bits():
+    import torch
+    n, d, vr, vp, ld = 1100, 64, 1090, 1152, 1 << 21
+    say(f"case: {n} rows {ld} elements apart")
+    p = Problem(23, n, d, vr, vp)
+    want = run_all(p)
+    a, kw = p.args()
+    far = [torch.empty((k, ld), dtype=t, device="cuda:0")[:, ld - d:] for k, t in
+           ((n, torch.bfloat16), (vr, torch.bfloat16), (n, torch.float32), (vr, torch.float32))]
+    far[0].copy_(p.h)
+    far[1].copy_(p.w)
+    gh, gw = rlk.linear_logp_backward(far[0], far[1], *a[2:], **kw, grad_hidden=far[2], grad_weight=far[3])
+    assert np.array_equal(bits(gh.to(torch.bfloat16)), bits(want[0]))
+    assert np.array_equal(bits(gw.to(torch.bfloat16)), bits(want[1]))
+
+
 @pytest.mark.parametrize("vr,vp", [(2000, 2048), (500, 2048), (1000, 1088), (60, 64)])
 def test_vocabulary_parallel_parts_give_the_bytes_of_the_whole(vr, vp):
     import torch

@@ -65,6 +65,7 @@ SIZES = [(dict(n=-1), SHAPE), (dict(n=(1 << 22) + 1), SHAPE), (dict(d=0), SHAPE)
     (dict(x=None), NULL), (dict(w=None), NULL), (dict(y=None), NULL),
     (dict(x=P + 8), ALIGN), (dict(w=P + 8), ALIGN), (dict(b=P + 8), ALIGN), (dict(y=P + 8), ALIGN), (dict(mean=P + 2), ALIGN),
     (dict(rstd=P + 2), ALIGN), (dict(n=0, x=None, w=None, y=None), OK),
+    (dict(y=P, ldy=128), SHAPE), (dict(y=P, ldx=128), SHAPE), (dict(y=P, xt=1), SHAPE),
 ])
 def test_forward_refuses(kw, code):
     assert fwd(**kw) == code
@@ -77,6 +78,7 @@ def bwd(dy=P, lddy=64, x=2 * P, xt=0, n=4, d=64, ldx=64, w=3 * P, wt=0, kind=0, 
 
 
 @pytest.mark.parametrize("kw,code", SIZES + [
+    (dict(dx=2 * P, lddx=128), SHAPE), (dict(dx=P, lddx=128), SHAPE), (dict(dx=P, xt=1), SHAPE), (dict(dx=2 * P, ldx=128), SHAPE),
     (dict(lddy=56), SHAPE), (dict(lddy=66), SHAPE), (dict(lddx=56), SHAPE), (dict(lddx=66), SHAPE), (dict(acc=2), SHAPE),
     (dict(dy=None), NULL), (dict(x=None), NULL), (dict(w=None), NULL), (dict(mean=None), NULL), (dict(rstd=None), NULL),
     (dict(dx=None, dw=None, db=None), NULL), (dict(ws=None), NULL),
