@@ -348,6 +348,8 @@ struct Tiles {
     for (int i = 0; i < S::MB; ++i) fa[0][i] = read_frag<kTA, S::MB, S::BM>(pa, i);
 #pragma unroll
     for (int j = 0; j < S::NB; ++j) fb[0][j] = read_frag<kTB, S::NB, S::BN>(pb, j);
+    // every wave has read its part before the first slice's loads go into that buffer
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
     for (int n = 0; n < kAddresses; ++n) turn(n, S::kBytes);
   }

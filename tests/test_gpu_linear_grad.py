@@ -352,6 +352,21 @@ def test_bytes_do_not_depend_on_how_many_shards_a_launch_takes():
         assert np.array_equal(bits(mw), bits(gw))
 
 
+@pytest.mark.parametrize("n", [2150, 4250, 8400, 9000])
+def test_the_same_bytes_every_time(n):
+    """A narrow head, whose loads come from the caches: they are soon there, also where a
+    wave of the workgroup is late (its code is read for the first time)."""
+    say(f"case: {n} rows of a 151936 x 64 head, again and again")
+    p = Problem(24, n, 64, 151936, 152576)
+    a, kw = first_rows(p, n, n)
+    gh, gw = rlk.linear_logp_backward(*a, **kw)
+    for _ in range(10):
+        mh, mw = rlk.linear_logp_backward(*a, **kw)
+        assert np.array_equal(bits(mh), bits(gh)) and np.array_equal(bits(mw), bits(gw))
+    a, kw = first_rows(p, 64, 64)
+    assert np.array_equal(bits(rlk.linear_logp_backward(*a, **kw)[0]), bits(gh)[:64])
+
+
 def test_strides_whose_offsets_pass_32_bits():
     import torch
     n, d, vr, vp, ld = 1100, 64, 1090, 1152, 1 << 21
