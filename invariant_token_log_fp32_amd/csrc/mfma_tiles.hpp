@@ -473,11 +473,11 @@ __device__ __forceinline__ void tile_at(int u, int m_tiles, int n_tiles, int& m,
   n = band * kGN + l / bm;
 }
 
-// First tile index of workgroup b, which runs on XCD b % 8: the XCD's
-// workgroups take neighbouring tiles (grid: a multiple of 8).
-__device__ __forceinline__ int first_tile() {
+// First tile index of workgroup b of `grid` (a multiple of 8), which runs on XCD b %
+// 8: the XCD's workgroups take neighbouring tiles.
+__device__ __forceinline__ int first_tile(int grid) {
   const int b = static_cast<int>(blockIdx.x);
-  return (b % kXcds) * (static_cast<int>(gridDim.x) / kXcds) + b / kXcds;
+  return (b % kXcds) * (grid / kXcds) + b / kXcds;
 }
 
 }  // namespace rlk_tiles

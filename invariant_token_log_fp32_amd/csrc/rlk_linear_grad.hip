@@ -158,29 +158,26 @@ __global__ __launch_bounds__(256) void k_gather(const uint16_t* __restrict__ h, 
 // Tiles, with LDS for one workgroup a compute unit (three of Short). Large has the
 // largest wave part that the 512 registers hold, so the fewest LDS reads for a
 // multiplication; the smaller ones are for products whose Large tiles would leave
-// compute units idle. kCost: time of a tile's slice in hundredths of Large's, from
-// the logits of 1500 rows and 76000 columns at 4096 (Large 868 us for 1800 tiles, 8
-// rounds over the compute units; Half 1121 for 3600, 15; Quarter 1279 for 7152, 28).
+// compute units idle.
 using Large = Shape<256, 256, 2, 2, 5, 1>;
 using Half = Shape<128, 256, 2, 2, 6, 1>;
 using Quarter = Shape<128, 128, 2, 2, 9, 1>;
 using Few = Shape<64, 128, 2, 2, 12, 1>;
 using Short = Shape<128, 128, 2, 2, 3, 3>;  // sums over few rows: bound by their stores, three tiles at a time
-constexpr int kCost[4] = {100, 70, 44, 30};
 
 constexpr int kTile = 256;  // columns of G are padded to whole tiles
 
 enum Pass { kLogits = 0, kHidden = 1, kWeight = 2 };
 
-// Where sums of grad_hidden go: the buffers `add` in order in front of them, then
-// float32 sums of the rows with a gradient, or (row_of given) the output's rows.
+// Where the sums of grad_hidden go that are made one shard after another: the buffers
+// `add` in order in front of them, then float32 sums of the rows with a gradient, or
+// (row_of given) the output's rows.
 struct HiddenOut {
   const float* add[3];  // [rows with a gradient x d]
   int n_add;
   int type;
   void* out;
   int64_t ldo;
-  int64_t shard_step;   // values between the shards of a launch
   const int32_t* row_of;
 };
 
@@ -195,44 +192,82 @@ struct Args {
   const RowCoef* coef;
   int64_t col0;        // first (global) column of the launch
   int64_t cols;        // its real columns
+  int full, rest;      // whole shards of them, columns of the next
   int width;           // columns of a shard
   int shards;          // shards of the launch
   int d;
-  HiddenOut hid;
+  int in_turn;         // grad_hidden may be summed one shard after another:
+  int turn;            //   then this launch is for shard `turn`
+  HiddenOut hid;       //   and its sums go here; else all shards' go to
+  float* parts;        // [shard of the launch][part_step]
+  int64_t part_step;
   void* gw;            // grad_weight at the launch's first column
   int64_t ldgw;
 };
 
 // Shard, tile and sizes of tile u of a launch.
+// (kHidden one by one: every tile is of shard `first`.)
 struct Where {
   int shard, m, n, cols;
 };
 
+// Tiles of a product over n rows with a gradient (`shards` of them in kHidden, a
+// shard without real columns among them: it has its empty sums all the same).
 template <class S, Pass kPass>
-__host__ __device__ __forceinline__ int64_t tile_count(const Args& a, int n_act) {
-  const int mt = (n_act + S::BM - 1) / S::BM;
+__host__ __device__ __forceinline__ int tile_count(const Args& a, int n, int shards) {
+  const int mt = (n + S::BM - 1) / S::BM;
   const int dt = (a.d + S::BN - 1) / S::BN;
-  const int64_t full = a.cols / a.width;
-  const int rest = static_cast<int>(a.cols - full * a.width);
+  if (kPass == kHidden) return mt * dt * shards;
   constexpr int v = kPass == kWeight ? S::BM : S::BN;
-  const int per = (a.width + v - 1) / v, last = (rest + v - 1) / v;
-  if (kPass == kLogits) return mt * (full * per + last);
-  if (kPass == kWeight) return dt * (full * per + last);
-  return static_cast<int64_t>(mt) * dt * a.shards;  // a shard without real columns has its (empty) sums all the same
+  return (kPass == kLogits ? mt : dt) * (a.full * ((a.width + v - 1) / v) + (a.rest + v - 1) / v);
+}
+
+// The kind of tile for a product, 0 .. 3 for Large, Half, Quarter, Few: the least
+// rounds over the compute units times a round's cost; the larger one where that is
+// equal (64 rows of the 151936 x 4096 head: logits and grad_hidden 527 us, with
+// Large logits 604; 128 rows 675 and 705; 640 rows 1635, with Few 2527). It is taken
+// on the device, for the rows that have a gradient.
+// Costs: of a tile's slice in hundredths of Large's, from the logits of 1500 rows and
+// 76000 columns at 4096 (Large 868 us for 1800 tiles, 8 rounds; Half 1121 for 3600,
+// 15; Quarter 1279 for 7152, 28).
+struct Choice {
+  int kind, cost;
+};
+
+template <Pass kPass>
+__host__ __device__ __forceinline__ Choice tiles_for(const Args& a, int n, int shards) {
+  constexpr int kUnits = 256;
+  const auto rounds = [](int tiles) { return (tiles + kUnits - 1) / kUnits; };
+  Choice best{0, rounds(tile_count<Large, kPass>(a, n, shards)) * 100};
+  const int half = rounds(tile_count<Half, kPass>(a, n, shards)) * 70;
+  if (half < best.cost) best = Choice{1, half};
+  const int quarter = rounds(tile_count<Quarter, kPass>(a, n, shards)) * 44;
+  if (quarter < best.cost) best = Choice{2, quarter};
+  const int few = rounds(tile_count<Few, kPass>(a, n, shards)) * 30;
+  if (few < best.cost) best = Choice{3, few};
+  return best;
+}
+
+// Whether grad_hidden's shards are summed one after another, each added to the ones
+// before as it ends: where that takes no longer than all at once, which writes and
+// reads a partial sum for every shard (8192 rows of the 151936 x 4096 head: 15.5 ms
+// with the logits, all at once 15.9).
+__host__ __device__ __forceinline__ bool one_by_one(const Args& a, int n) {
+  return tiles_for<kHidden>(a, n, 1).cost * a.shards <= tiles_for<kHidden>(a, n, a.shards).cost;
 }
 
 template <class S, Pass kPass>
-__device__ __forceinline__ Where where_is(const Args& a, int n_act, int u) {
+__device__ __forceinline__ Where where_is(const Args& a, int n_act, int first, int u) {
   const int mt = (n_act + S::BM - 1) / S::BM;
   const int dt = (a.d + S::BN - 1) / S::BN;
   constexpr int cols = kPass == kWeight ? S::BM : S::BN;
   const int per = (a.width + cols - 1) / cols;
   const int each = kPass == kHidden ? mt * dt : (kPass == kLogits ? mt : dt) * per;
   Where w;
-  w.shard = u / each;
+  w.shard = u / each + first;
   const int64_t left = a.cols - static_cast<int64_t>(w.shard) * a.width;
   w.cols = static_cast<int>(left < 0 ? 0 : (left < a.width ? left : a.width));
-  const int v = u - w.shard * each;
+  const int v = u % each;
   const int vt = (w.cols + cols - 1) / cols;
   if (kPass == kLogits) tile_at(v, mt, vt, w.m, w.n);
   if (kPass == kHidden) tile_at(v, mt, dt, w.m, w.n);
@@ -355,20 +390,25 @@ __device__ __forceinline__ void store_pair(const f32x4& x, const f32x4& y, bool 
 }
 
 template <class S, int kType>
-__device__ __forceinline__ void store_hidden(const Args& a, int n_act, const Where& w, const f32x4 (&acc)[S::MB][S::NB]) {
+__device__ __forceinline__ void store_hidden(const Args& a, int n_act, bool in_turn, const Where& w,
+                                             const f32x4 (&acc)[S::MB][S::NB]) {
   const int lane = lane_here();
   const int h = lane >> 4;
   const int wave = threadIdx.x >> 6;
   const int wm = wave % S::WM;
   const int wn = wave / S::WM;
   const int cw = w.n * S::BN + wn * S::NB * 16;
+  const int n_add = in_turn ? a.hid.n_add : 0;
+  const int32_t* row_of = in_turn ? a.hid.row_of : nullptr;
+  const int64_t ldo = in_turn ? a.hid.ldo : a.d;
+  void* out = in_turn ? a.hid.out : a.parts + w.shard * a.part_step;
 #pragma unroll
   for (int i = 0; i < S::MB; ++i) {
     const int gr = w.m * S::BM + (wm * S::MB + i) * 16 + (lane & 15);
     f32x4 v[S::NB];
 #pragma unroll
     for (int j = 0; j < S::NB; ++j) v[j] = taken(acc[i][j]);
-    for (int k = 0; k < a.hid.n_add; ++k) {
+    for (int k = 0; k < n_add; ++k) {
       const float* from = a.hid.add[k] + static_cast<int64_t>(gr) * a.d + cw + 4 * h;
       f32x4 o[S::NB];
 #pragma unroll
@@ -379,11 +419,11 @@ __device__ __forceinline__ void store_hidden(const Args& a, int n_act, const Whe
 #pragma unroll
       for (int j = 0; j < S::NB; ++j) v[j] = o[j] + v[j];
     }
-    const int64_t row = a.hid.row_of && gr < n_act ? a.hid.row_of[gr] : gr;
-    const int64_t at = row * a.hid.ldo + w.shard * a.hid.shard_step + cw;
+    const int64_t row = row_of && gr < n_act ? row_of[gr] : gr;
+    const int64_t at = row * ldo + cw;
 #pragma unroll
     for (int j = 0; j < S::NB; j += 2)
-      store_pair<kType>(v[j], v[j + 1], gr < n_act && cw + 16 * j < a.d, a.hid.out, at + 16 * j, h);
+      store_pair<kType>(v[j], v[j + 1], gr < n_act && cw + 16 * j < a.d, out, at + 16 * j, h);
   }
 }
 
@@ -407,17 +447,18 @@ __device__ __forceinline__ void store_weight(const Args& a, const Where& w, cons
 }
 
 template <class S, Pass kPass, int kType>
-__global__ __launch_bounds__(kThreads, S::kPer) void k_product(Args a) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[S::kLds];
-  const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
-  const int n_tiles = static_cast<int>(tile_count<S, kPass>(a, n_act));
-  const int grid = static_cast<int>(gridDim.x);
-  int u = first_tile();
+__device__ __forceinline__ void product_tiles(const Args& a, int n_act, bool in_turn, uint8_t* smem) {
+  const int n_tiles = tile_count<S, kPass>(a, n_act, in_turn ? 1 : a.shards);
+  const int first = in_turn ? a.turn : 0;
+  const int most = (n_tiles + kXcds - 1) / kXcds * kXcds;
+  const int grid = static_cast<int>(gridDim.x) < most ? static_cast<int>(gridDim.x) : most;
+  if (static_cast<int>(blockIdx.x) >= grid) return;
+  int u = first_tile(grid);
   if (u >= n_tiles) return;  // uniform across the workgroup
   int loads = u;  // the tile that the loads come to next
   const auto next = [&](TileIn& t) __attribute__((always_inline)) {
     if (loads >= n_tiles) return false;
-    t = tile_in<S, kPass>(a, n_act, where_is<S, kPass>(a, n_act, loads));
+    t = tile_in<S, kPass>(a, n_act, where_is<S, kPass>(a, n_act, first, loads));
     loads += grid;
     return true;
   };
@@ -425,13 +466,34 @@ __global__ __launch_bounds__(kThreads, S::kPer) void k_product(Args a) {
       next, smem, kPass == kLogits ? a.d : static_cast<int>(a.ldg), kPass == kWeight ? a.d : static_cast<int>(a.ldw));
   tiles.start();
   for (; u < n_tiles; u += grid) {
-    const Where w = where_is<S, kPass>(a, n_act, u);
+    const Where w = where_is<S, kPass>(a, n_act, first, u);
     f32x4 acc[S::MB][S::NB];
     tiles.sums(acc, slices_of(kPass == kLogits ? a.d : (kPass == kHidden ? w.cols : n_act)));
     if (kPass == kLogits) store_g<S>(a, n_act, w, acc);
-    if (kPass == kHidden) store_hidden<S, kType>(a, n_act, w, acc);
+    if (kPass == kHidden) store_hidden<S, kType>(a, n_act, in_turn, w, acc);
     if (kPass == kWeight) store_weight<S, kType>(a, w, acc);
   }
+}
+
+// kLogits and kHidden, on the tiles that suit the rows with a gradient.
+template <Pass kPass, int kType>
+__global__ __launch_bounds__(kThreads, 1) void k_product(Args a) {
+  static_assert(Large::kLds >= Half::kLds && Large::kLds >= Quarter::kLds && Large::kLds >= Few::kLds, "LDS of each kind");
+  __shared__ __attribute__((aligned(16))) uint8_t smem[Large::kLds];
+  const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
+  const bool in_turn = kPass == kHidden && a.in_turn && one_by_one(a, n_act);
+  if (kPass == kHidden && !in_turn && a.turn > 0) return;  // the first launch has summed all shards
+  const int kind = tiles_for<kPass>(a, n_act, in_turn ? 1 : a.shards).kind;
+  if (kind == 0) product_tiles<Large, kPass, kType>(a, n_act, in_turn, smem);
+  if (kind == 1) product_tiles<Half, kPass, kType>(a, n_act, in_turn, smem);
+  if (kind == 2) product_tiles<Quarter, kPass, kType>(a, n_act, in_turn, smem);
+  if (kind == 3) product_tiles<Few, kPass, kType>(a, n_act, in_turn, smem);
+}
+
+template <class S, int kType>
+__global__ __launch_bounds__(kThreads, S::kPer) void k_weight(Args a) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[S::kLds];
+  product_tiles<S, kWeight, kType>(a, __builtin_amdgcn_readfirstlane(*a.n_act), false, smem);
 }
 
 // The fixed sum of `count` (1, 2, 4 or 8) partial sums, neighbours first.
@@ -457,18 +519,18 @@ __device__ __forceinline__ void store4(void* out, int type, int64_t at, const f3
     *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) = v;
 }
 
-// Row r of the rows with a gradient: `count` partial sums of this launch, then
-// the earlier ones.
-__global__ __launch_bounds__(256) void k_combine(const float* __restrict__ parts, int64_t step, int count,
-                                                 HiddenOut o, const int32_t* __restrict__ n_act, int d) {
-  const int n = *n_act;
-  const int64_t vecs = static_cast<int64_t>(n) * (d / 4);
+// Row r of the rows with a gradient: the partial sums of a launch's shards, then the
+// earlier ones.
+__global__ __launch_bounds__(256) void k_combine(Args a, HiddenOut o) {
+  const int n = *a.n_act;
+  if (a.in_turn && one_by_one(a, n)) return;  // done already
+  const int64_t vecs = static_cast<int64_t>(n) * (a.d / 4);
   for (int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; v < vecs;
        v += static_cast<int64_t>(gridDim.x) * 256) {
-    f32x4 s = tree(count, [&](int k) { return *reinterpret_cast<const f32x4*>(parts + k * step + v * 4); });
+    f32x4 s = tree(a.shards, [&](int k) { return *reinterpret_cast<const f32x4*>(a.parts + k * a.part_step + v * 4); });
     for (int k = 0; k < o.n_add; ++k) s = *reinterpret_cast<const f32x4*>(o.add[k] + v * 4) + s;
-    const int64_t r = v / (d / 4);
-    const int64_t c = (v - r * (d / 4)) * 4;
+    const int64_t r = v / (a.d / 4);
+    const int64_t c = (v - r * (a.d / 4)) * 4;
     store4(o.out, o.type, (o.row_of ? o.row_of[r] : r) * o.ldo + c, s);
   }
 }
@@ -582,48 +644,17 @@ static int cu_count() {
 }
 
 // (The rows with a gradient are counted on the device: n_rows is the most.)
-template <class S, Pass kPass, int kType>
-static int32_t product(const Args& a, int64_t n_rows, hipStream_t stream) {
-  const int64_t cap = static_cast<int64_t>(cu_count()) * S::kPer;
-  const int64_t want = (tile_count<S, kPass>(a, static_cast<int>(n_rows)) + kXcds - 1) / kXcds * kXcds;
-  k_product<S, kPass, kType><<<dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(kThreads), 0, stream>>>(a);
-  return launched();
-}
-
-// The tiles for a product: the least rounds over the compute units times a round's
-// cost; the larger ones where that is equal (64 rows of the 151936 x 4096 head: logits
-// and grad_hidden 527 us, with Large logits 604; 128 rows 675 and 705; 640 rows 1635,
-// with Few 2527).
-struct Choice {
-  int kind;
-  int64_t cost;
-};
-
-template <Pass kPass>
-static Choice tiles_for(const Args& a, int64_t n_rows) {
-  constexpr int64_t kUnits = 256;
-  const int n = static_cast<int>(n_rows);
-  const int64_t tiles[4] = {tile_count<Large, kPass>(a, n), tile_count<Half, kPass>(a, n),
-                            tile_count<Quarter, kPass>(a, n), tile_count<Few, kPass>(a, n)};
-  Choice best{0, 0};
-  for (int k = 0; k < 4; ++k) {
-    const int64_t cost = (tiles[k] + kUnits - 1) / kUnits * kCost[k];
-    if (k == 0 || cost < best.cost) best = Choice{k, cost};
-  }
-  return best;
+static dim3 grid_for(int tiles, int per) {
+  const int most = cu_count() * per;
+  const int want = (tiles + kXcds - 1) / kXcds * kXcds;
+  return dim3(static_cast<unsigned>(want < most ? want : most));
 }
 
 template <Pass kPass, int kType>
-static int32_t product_of(int kind, const Args& a, int64_t n_rows, hipStream_t stream) {
-  if (kind == 0) return product<Large, kPass, kType>(a, n_rows, stream);
-  if (kind == 1) return product<Half, kPass, kType>(a, n_rows, stream);
-  if (kind == 2) return product<Quarter, kPass, kType>(a, n_rows, stream);
-  return product<Few, kPass, kType>(a, n_rows, stream);
-}
-
-static int32_t hidden_product(int kind, const Args& a, int64_t n_rows, hipStream_t stream) {
-  return a.hid.type == RLK_GRAD_BF16 ? product_of<kHidden, RLK_GRAD_BF16>(kind, a, n_rows, stream)
-                                     : product_of<kHidden, RLK_GRAD_F32>(kind, a, n_rows, stream);
+static int32_t product(const Args& a, int64_t n_rows, hipStream_t stream) {
+  const int n = static_cast<int>(n_rows);  // Few has the most tiles
+  k_product<kPass, kType><<<grid_for(tile_count<Few, kPass>(a, n, a.shards), 1), dim3(kThreads), 0, stream>>>(a);
+  return launched();
 }
 
 // Short tiles for few rows and few tiles (64 rows of an 8000 x 512 head 33 us a call,
@@ -632,9 +663,13 @@ static int32_t hidden_product(int kind, const Args& a, int64_t n_rows, hipStream
 // 682; 128 rows 737 and 829; 256 rows 930 and 1065).
 template <int kType>
 static int32_t weight_product(const Args& a, int64_t n_rows, hipStream_t stream) {
-  if (n_rows <= 128 && tile_count<Large, kWeight>(a, static_cast<int>(n_rows)) <= 1024)
-    return product<Short, kWeight, kType>(a, n_rows, stream);
-  return product<Large, kWeight, kType>(a, n_rows, stream);
+  const int n = static_cast<int>(n_rows);
+  const int tiles = tile_count<Large, kWeight>(a, n, a.shards);
+  if (n <= 128 && tiles <= 1024)
+    k_weight<Short, kType><<<grid_for(tile_count<Short, kWeight>(a, n, a.shards), Short::kPer), dim3(kThreads), 0, stream>>>(a);
+  else
+    k_weight<Large, kType><<<grid_for(tiles, 1), dim3(kThreads), 0, stream>>>(a);
+  return launched();
 }
 
 static unsigned vec_grid(int64_t vecs) {
@@ -719,36 +754,29 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
   a.n_act = n_act;
   a.coef = coef;
   a.width = p.width;
-  a.shards = p.at_once;
   a.d = static_cast<int>(d);
   a.ldgw = grad_weight_stride;
-  // Whether grad_hidden's shards are summed one after another, each added to the
-  // ones before as it ends: where that takes no longer than all at once, which
-  // writes and reads a partial sum for every shard (8192 rows of the 151936 x 4096
-  // head: 15.5 ms with the logits, all at once 15.9).
-  a.shards = 1;
-  const bool one_by_one = tiles_for<kHidden>(a, n_rows).cost * p.at_once <= [&] {
-    Args b = a;
-    b.shards = p.at_once;
-    return tiles_for<kHidden>(b, n_rows).cost;
-  }();
   a.shards = p.at_once;
-  float* waiting = parts + static_cast<int64_t>(one_by_one || p.at_once == 1 ? 0 : p.at_once) * p.part_step;
+  a.parts = parts;
+  a.part_step = p.part_step;
+  a.in_turn = one_by_one(a, static_cast<int>(n_rows));
   for (int s = 0; s < p.local; s += p.at_once) {
     const int64_t c0 = static_cast<int64_t>(s) * p.width;  // columns counted from the rank's first
     const int64_t left = layout->vocab_real - first - c0;
     const int64_t most = static_cast<int64_t>(p.at_once) * p.width;
     a.col0 = first + c0;
     a.cols = left < 0 ? 0 : (left < most ? left : most);
+    a.full = static_cast<int>(a.cols / p.width);
+    a.rest = static_cast<int>(a.cols % p.width);
     a.w = n_rows > 0 && a.cols > 0 ? weight + c0 * weight_stride : weight;
     if (n_rows > 0 && a.cols > 0) {
-      st = product_of<kLogits, RLK_GRAD_BF16>(tiles_for<kLogits>(a, n_rows).kind, a, n_rows, stream);
-      if (st != RLK_OK) return st;
+      if ((st = product<kLogits, RLK_GRAD_BF16>(a, n_rows, stream)) != RLK_OK) return st;
     }
     if (grad_hidden && n_rows > 0) {
       // The k-th of the sums (of a shard, or of a launch's shards): those of whole
-      // pairs, fours and eights wait in `waiting` and are added as their neighbours end.
-      const auto sum_to = [&](int k, bool last) {
+      // pairs, fours and eights wait and are added as their neighbours end. Only one of
+      // the two ways is gone, on the device, so both may use the same buffers.
+      const auto sum_to = [&](float* waiting, int k, bool last) {
         HiddenOut o{};
         int level = 0;
         for (; (k >> level) & 1; ++level) o.add[level] = waiting + level * p.part_step;
@@ -759,27 +787,18 @@ int32_t rlk_linear_logp_backward(const uint16_t* hidden, int64_t n_rows, int64_t
         o.row_of = last ? row_of : nullptr;
         return o;
       };
-      if (one_by_one) {
-        for (int k = 0; k < p.at_once; ++k) {
-          Args one = a;
-          const int64_t skip = static_cast<int64_t>(k) * p.width;
-          one.shards = 1;
-          one.cols = a.cols < skip ? 0 : (a.cols - skip < p.width ? a.cols - skip : p.width);
-          one.w = one.cols > 0 ? a.w + skip * weight_stride : a.w;
-          one.g = a.g + k * p.g_step;
-          one.hid = sum_to(s + k, s + k + 1 == p.local);
-          if ((st = hidden_product(tiles_for<kHidden>(one, n_rows).kind, one, n_rows, stream)) != RLK_OK) return st;
-        }
-      } else {
-        a.hid = HiddenOut{};
-        a.hid.out = parts;
-        a.hid.ldo = d;
-        a.hid.type = RLK_GRAD_F32;
-        a.hid.shard_step = p.part_step;
-        if ((st = hidden_product(tiles_for<kHidden>(a, n_rows).kind, a, n_rows, stream)) != RLK_OK) return st;
+      for (a.turn = 0; a.turn < (a.in_turn ? p.at_once : 1); ++a.turn) {
+        const int k = s + a.turn;
+        a.hid = sum_to(parts, k, k + 1 == p.local);
+        // (BF16 is the last shard's, whose launch sums no others unless it is the only one)
+        st = a.in_turn && a.hid.type == RLK_GRAD_BF16 ? product<kHidden, RLK_GRAD_BF16>(a, n_rows, stream)
+                                                      : product<kHidden, RLK_GRAD_F32>(a, n_rows, stream);
+        if (st != RLK_OK) return st;
+      }
+      a.turn = 0;
+      if (p.at_once > 1) {
         k_combine<<<dim3(vec_grid(n_rows * (d / 4))), dim3(256), 0, stream>>>(
-            parts, p.part_step, p.at_once, sum_to(s / p.at_once, s + p.at_once == p.local), n_act,
-            static_cast<int>(d));
+            a, sum_to(parts + p.at_once * p.part_step, s / p.at_once, s + p.at_once == p.local));
         if ((st = launched()) != RLK_OK) return st;
       }
     }

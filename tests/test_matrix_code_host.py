@@ -2,7 +2,7 @@
 
 Their matrix instructions are inline assembly, of which the compiler does not know
 the waits that they need. What mfma_tiles.hpp relies on is checked in the assembly
-of every k_product kernel:
+of every kernel of theirs:
   - an accumulator is a matrix instruction's source and destination at once
   - they all stand between the two waits of a sum, and nothing else there touches an
     accumulator register or memory of its own
@@ -39,7 +39,7 @@ def kernels(tmp_path_factory):
     assert res.returncode == 0, res.stderr[-2000:]
     found, name, text = {}, None, open(out).read()
     for line in text.splitlines():
-        m = re.match(r"(_ZN\S*k_product\S*):", line)
+        m = re.match(r"(_ZN\S*(?:k_product|k_weight)\S*):", line)
         if m:
             name = m.group(1)
             found[name] = []
@@ -47,19 +47,24 @@ def kernels(tmp_path_factory):
             op, _, rest = line.split(";")[0].strip().partition(" ")
             op, _, more = op.partition("\t")
             found[name].append((op, [a.strip() for a in (more + " " + rest).split(",")]))
-            if op == "s_endpgm":
-                name = None
+        elif line.startswith(".Lfunc_end"):
+            name = None
     return found, text
 
 
 def test_products_have_their_waits(kernels):
     found, _ = kernels
-    assert len(found) >= 15
+    assert len(found) >= 9
     for name, code in found.items():
         waits = [k for k, (op, a) in enumerate(code) if op == "s_nop" and a == ["15"]]
         products = [k for k, (op, _) in enumerate(code) if op.startswith("v_mfma")]
-        assert len(waits) == 4 and waits[1] == waits[0] + 1 and waits[3] == waits[2] + 1, (name, waits)
-        assert products and waits[1] < products[0] and products[-1] < waits[2], name
+        assert len(waits) == (16 if "k_product" in name else 4), (name, waits)  # one sum for each kind of tile
+        inside = []
+        for k in range(0, len(waits), 4):
+            before, last, after, end = waits[k:k + 4]
+            assert last == before + 1 and end == after + 1, (name, waits)
+            inside += range(last + 1, after)
+        assert products and set(products) <= set(inside), name
         for k in products:
             op, a = code[k]
             assert a[0] == a[3] and a[0].startswith("a["), (name, a)
@@ -67,7 +72,8 @@ def test_products_have_their_waits(kernels):
             for near, b in code[k - 2:k]:
                 if near.startswith("v_") and not near.startswith("v_mfma"):
                     assert not registers(b[0]) & needed, (name, near, b, a)
-        for op, a in code[waits[1] + 1:waits[2]]:
+        for k in inside:
+            op, a = code[k]
             if not op.startswith("v_mfma"):
                 assert not any(r[0] == "a" for x in a for r in registers(x)), (name, op, a)
                 assert not op.startswith("scratch_"), (name, op, a)
@@ -78,7 +84,7 @@ def test_products_do_not_spill(kernels):
     blocks = re.split(r"\n  - \.", text[text.index("amdhsa.kernels:"):])
     seen = 0
     for b in blocks:
-        if "k_product" in b:
+        if "k_product" in b or "k_weight" in b:
             seen += 1
             for what in ("private_segment_fixed_size", "vgpr_spill_count"):
                 assert re.search(rf"\.{what}:\s+0\b", b), (what, b[:300])
