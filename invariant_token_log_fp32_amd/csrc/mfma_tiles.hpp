@@ -120,7 +120,7 @@ __device__ __forceinline__ Panel panel_rows(const uint16_t* p, int rows, int ld,
 }
 
 __device__ __forceinline__ Panel panel_cols(const uint16_t* p, int64_t cols, int most) {
-  return Panel{p, static_cast<int>(cols < most ? cols : most) * 2};
+  return Panel{p, cols > 0 ? static_cast<int>(cols < most ? cols : most) * 2 : 0};
 }
 
 // The slices of a panel one after another, as buffer resources whose range check
@@ -134,7 +134,7 @@ struct Stream {
   __device__ __forceinline__ void begin(const Panel& t, int ld, int k_end) {
     p = t.p;
     rec = kAcross ? (kSlice - 1) * ld * 2 + t.lim : (k_end > 0 ? t.lim : 0);
-    rest = k_end;
+    rest = !kAcross || t.lim > 0 ? k_end : 0;
     tail = (k_end % kSlice - 1) * ld * 2 + t.lim;  // looked at only where a row is left
   }
   __device__ __forceinline__ void none() {
@@ -325,8 +325,8 @@ struct Tiles {
   // Fills the ring and reads the first slice's fragments.
   __device__ __forceinline__ void start() {
     left = 0;
-#pragma unroll
-    for (int q = 0; q < S::kRing; ++q) {
+#pragma unroll 1
+    for (int q = 0; q < S::kRing; ++q) {  // (written out it is kilobytes of code, read for the first time)
       if (left == 0) go_on();  // uniform
       --left;
       const __amdgpu_buffer_rsrc_t ra = sa.now();

@@ -23,7 +23,12 @@
 //              shard; <kWeight> G^T times the hidden states
 //   k_combine  a row's partial sums added in the fixed order
 // The products run on the tiles of mfma_tiles.hpp, one workgroup a compute unit
-// looping over its tiles. Both operands of kWeight and the projection in kHidden
+// looping over its tiles. What bounds them, at 4096 columns of hidden states and a
+// vocabulary of 151936: one row reads the projection twice and writes its gradient at
+// 4.7 TB/s (0.80 ms; a large copy reaches 4.9); 8192 rows take 22.7 ms (1.35 PFLOP/s)
+// or, on a warm GPU, 24.6, as long as the three library products alone in the same loop
+// (1.24): the power limit; in between, rounds of tiles that the compute units share
+// unevenly (640 rows, grad_hidden alone, 1.53 ms: 1.05 PFLOP/s). Both operands of kWeight and the projection in kHidden
 // run across K in memory; they are transposed on the way from LDS to registers,
 // so no transposed copy is written.
 #include <hip/hip_runtime.h>
@@ -206,7 +211,6 @@ struct Args {
 };
 
 // Shard, tile and sizes of tile u of a launch.
-// (kHidden one by one: every tile is of shard `first`.)
 struct Where {
   int shard, m, n, cols;
 };
@@ -222,29 +226,35 @@ __host__ __device__ __forceinline__ int tile_count(const Args& a, int n, int sha
   return (kPass == kLogits ? mt : dt) * (a.full * ((a.width + v - 1) / v) + (a.rest + v - 1) / v);
 }
 
-// The kind of tile for a product, 0 .. 3 for Large, Half, Quarter, Few: the least
-// rounds over the compute units times a round's cost; the larger one where that is
-// equal (64 rows of the 151936 x 4096 head: logits and grad_hidden 527 us, with
-// Large logits 604; 128 rows 675 and 705; 640 rows 1635, with Few 2527). It is taken
-// on the device, for the rows that have a gradient.
+// The tiles of a product, taken on the device for the rows that have a gradient: of
+// one kind (0 .. 3: Large, Half, Quarter, Few), or whole rounds of Large tiles and what
+// is left of them cut into smaller ones. Whichever has the least rounds over the compute
+// units times a round's cost; the larger kind where that is equal (64 rows of the 151936
+// x 4096 head: logits and grad_hidden 527 us, with Large logits 604; 128 rows 675 and
+// 705; 640 rows with Large 1635, with Few 2527, with Large's last rounds cut 1520).
 // Costs: of a tile's slice in hundredths of Large's, from the logits of 1500 rows and
 // 76000 columns at 4096 (Large 868 us for 1800 tiles, 8 rounds; Half 1121 for 3600,
 // 15; Quarter 1279 for 7152, 28).
 struct Choice {
   int kind, cost;
+  int whole;  // Large tiles that come first
 };
 
 template <Pass kPass>
 __host__ __device__ __forceinline__ Choice tiles_for(const Args& a, int n, int shards) {
   constexpr int kUnits = 256;
   const auto rounds = [](int tiles) { return (tiles + kUnits - 1) / kUnits; };
-  Choice best{0, rounds(tile_count<Large, kPass>(a, n, shards)) * 100};
-  const int half = rounds(tile_count<Half, kPass>(a, n, shards)) * 70;
-  if (half < best.cost) best = Choice{1, half};
-  const int quarter = rounds(tile_count<Quarter, kPass>(a, n, shards)) * 44;
-  if (quarter < best.cost) best = Choice{2, quarter};
-  const int few = rounds(tile_count<Few, kPass>(a, n, shards)) * 30;
-  if (few < best.cost) best = Choice{3, few};
+  const int large = tile_count<Large, kPass>(a, n, shards);
+  const int whole = large / kUnits, rest = large % kUnits;
+  Choice best{0, rounds(large) * 100, 0};
+  const auto look = [&](int kind, int cost, int tiles, int parts) {
+    if (rounds(tiles) * cost < best.cost) best = Choice{kind, rounds(tiles) * cost, 0};
+    const int mixed = whole * 100 + rounds(rest * parts) * cost;
+    if (whole > 0 && mixed < best.cost) best = Choice{kind, mixed, whole * kUnits};
+  };
+  look(1, 70, tile_count<Half, kPass>(a, n, shards), 2);
+  look(2, 44, tile_count<Quarter, kPass>(a, n, shards), 4);
+  look(3, 30, tile_count<Few, kPass>(a, n, shards), 8);
   return best;
 }
 
@@ -275,6 +285,27 @@ __device__ __forceinline__ Where where_is(const Args& a, int n_act, int first, i
   return w;
 }
 
+// Which tiles a walk goes through: those of its kind, or with `cut` its kind's parts of
+// the Large tiles from `from` on (a part may lie past the last row or column: it is a
+// sum of zeros, and is not stored).
+struct Walk {
+  bool cut;
+  int from;   // Large tile of the first part
+  int shard;  // kHidden one by one: every tile is of this shard
+  int count;
+};
+
+template <class S, Pass kPass>
+__device__ __forceinline__ Where where_is(const Args& a, int n_act, const Walk& walk, int u) {
+  constexpr int kM = Large::BM / S::BM, kN = Large::BN / S::BN;
+  if (kM * kN == 1 || !walk.cut) return where_is<S, kPass>(a, n_act, walk.shard, u);  // uniform
+  Where w = where_is<Large, kPass>(a, n_act, walk.shard, walk.from + u / (kM * kN));
+  const int part = u % (kM * kN);
+  w.m = w.m * kM + part % kM;
+  w.n = w.n * kN + part / kM;
+  return w;
+}
+
 template <class S, Pass kPass>
 __device__ __forceinline__ TileIn tile_in(const Args& a, int n_act, const Where& w) {
   TileIn t;
@@ -282,7 +313,7 @@ __device__ __forceinline__ TileIn tile_in(const Args& a, int n_act, const Where&
   const uint16_t* gp = a.g + w.shard * a.g_step;
   const int rows = n_act - w.m * S::BM < S::BM ? n_act - w.m * S::BM : S::BM;
   if (kPass == kLogits) {
-    const int vr = w.cols - w.n * S::BN < S::BN ? w.cols - w.n * S::BN : S::BN;
+    const int vr = w.cols - w.n * S::BN < S::BN ? w.cols - w.n * S::BN : S::BN;  // (below 1: none)
     t.k_end = a.d;
     t.a = panel_rows(a.h + static_cast<int64_t>(w.m) * S::BM * a.d, rows, a.d, a.d);
     t.b = panel_rows(wp + static_cast<int64_t>(w.n) * S::BN * a.ldw, vr, static_cast<int>(a.ldw), a.d);
@@ -447,9 +478,8 @@ __device__ __forceinline__ void store_weight(const Args& a, const Where& w, cons
 }
 
 template <class S, Pass kPass, int kType>
-__device__ __forceinline__ void product_tiles(const Args& a, int n_act, bool in_turn, uint8_t* smem) {
-  const int n_tiles = tile_count<S, kPass>(a, n_act, in_turn ? 1 : a.shards);
-  const int first = in_turn ? a.turn : 0;
+__device__ __forceinline__ void product_tiles(const Args& a, int n_act, bool in_turn, const Walk& walk, uint8_t* smem) {
+  const int n_tiles = walk.count;
   const int most = (n_tiles + kXcds - 1) / kXcds * kXcds;
   const int grid = static_cast<int>(gridDim.x) < most ? static_cast<int>(gridDim.x) : most;
   if (static_cast<int>(blockIdx.x) >= grid) return;
@@ -458,7 +488,7 @@ __device__ __forceinline__ void product_tiles(const Args& a, int n_act, bool in_
   int loads = u;  // the tile that the loads come to next
   const auto next = [&](TileIn& t) __attribute__((always_inline)) {
     if (loads >= n_tiles) return false;
-    t = tile_in<S, kPass>(a, n_act, where_is<S, kPass>(a, n_act, first, loads));
+    t = tile_in<S, kPass>(a, n_act, where_is<S, kPass>(a, n_act, walk, loads));
     loads += grid;
     return true;
   };
@@ -466,7 +496,7 @@ __device__ __forceinline__ void product_tiles(const Args& a, int n_act, bool in_
       next, smem, kPass == kLogits ? a.d : static_cast<int>(a.ldg), kPass == kWeight ? a.d : static_cast<int>(a.ldw));
   tiles.start();
   for (; u < n_tiles; u += grid) {
-    const Where w = where_is<S, kPass>(a, n_act, first, u);
+    const Where w = where_is<S, kPass>(a, n_act, walk, u);
     f32x4 acc[S::MB][S::NB];
     tiles.sums(acc, slices_of(kPass == kLogits ? a.d : (kPass == kHidden ? w.cols : n_act)));
     if (kPass == kLogits) store_g<S>(a, n_act, w, acc);
@@ -483,17 +513,42 @@ __global__ __launch_bounds__(kThreads, 1) void k_product(Args a) {
   const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
   const bool in_turn = kPass == kHidden && a.in_turn && one_by_one(a, n_act);
   if (kPass == kHidden && !in_turn && a.turn > 0) return;  // the first launch has summed all shards
-  const int kind = tiles_for<kPass>(a, n_act, in_turn ? 1 : a.shards).kind;
-  if (kind == 0) product_tiles<Large, kPass, kType>(a, n_act, in_turn, smem);
-  if (kind == 1) product_tiles<Half, kPass, kType>(a, n_act, in_turn, smem);
-  if (kind == 2) product_tiles<Quarter, kPass, kType>(a, n_act, in_turn, smem);
-  if (kind == 3) product_tiles<Few, kPass, kType>(a, n_act, in_turn, smem);
+  const int shards = in_turn ? 1 : a.shards;
+  const Choice best = tiles_for<kPass>(a, n_act, shards);
+  int kind = best.whole > 0 ? 0 : best.kind;
+  int done = 0;  // Large tiles before the walk at hand
+#pragma unroll 1
+  for (;;) {
+    Walk walk{done > 0, done, in_turn ? a.turn : 0, 0};
+    if (kind == 0) {
+      walk.count = best.whole > 0 ? best.whole : tile_count<Large, kPass>(a, n_act, shards);
+      product_tiles<Large, kPass, kType>(a, n_act, in_turn, walk, smem);
+    } else {
+      const int rest = tile_count<Large, kPass>(a, n_act, shards) - done;
+      if (kind == 1) {
+        walk.count = walk.cut ? rest * 2 : tile_count<Half, kPass>(a, n_act, shards);
+        product_tiles<Half, kPass, kType>(a, n_act, in_turn, walk, smem);
+      } else if (kind == 2) {
+        walk.count = walk.cut ? rest * 4 : tile_count<Quarter, kPass>(a, n_act, shards);
+        product_tiles<Quarter, kPass, kType>(a, n_act, in_turn, walk, smem);
+      } else {
+        walk.count = walk.cut ? rest * 8 : tile_count<Few, kPass>(a, n_act, shards);
+        product_tiles<Few, kPass, kType>(a, n_act, in_turn, walk, smem);
+      }
+    }
+    if (done == best.whole) return;  // uniform: there is no second walk, or it is over
+    done = best.whole;
+    kind = best.kind;
+    // no load of the first walk (of zeros, past its last tile) comes after this
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
 }
 
 template <class S, int kType>
 __global__ __launch_bounds__(kThreads, S::kPer) void k_weight(Args a) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[S::kLds];
-  product_tiles<S, kWeight, kType>(a, __builtin_amdgcn_readfirstlane(*a.n_act), false, smem);
+  const int n_act = __builtin_amdgcn_readfirstlane(*a.n_act);
+  product_tiles<S, kWeight, kType>(a, n_act, false, Walk{false, 0, 0, tile_count<S, kWeight>(a, n_act, a.shards)}, smem);
 }
 
 // The fixed sum of `count` (1, 2, 4 or 8) partial sums, neighbours first.
@@ -674,7 +729,7 @@ static int32_t weight_product(const Args& a, int64_t n_rows, hipStream_t stream)
 
 static unsigned vec_grid(int64_t vecs) {
   const int64_t blocks = (vecs + 255) / 256;
-  return static_cast<unsigned>(blocks < 1 ? 1 : (blocks < 16384 ? blocks : 16384));
+  return static_cast<unsigned>(blocks < 1 ? 1 : (blocks < 4096 ? blocks : 4096));
 }
 
 }  // namespace rlk_lin_grad

@@ -302,11 +302,13 @@ def first_rows(p, k, n):
 
 
 # Heads and row counts whose products take tiles of every size (64 and 128 x 128, 128 and
-# 256 x 256), sum grad_hidden's shards all at once and one after another, and have odd
-# ends of rows, columns and K in each.
+# 256 x 256) and whole rounds of the largest with the rest cut into each smaller one, sum
+# grad_hidden's shards all at once and one after another, and have odd ends of rows,
+# columns and K in each.
 @pytest.mark.parametrize("d,vr,vp,rows", [(1024, 20000, 20032, (3, 100, 201, 300, 520, 1101)),
                                           (1088, 13999, 14336, (129, 190, 700)), (2048, 19999, 20032, (130, 385, 641)),
-                                          (4096, 1000, 1024, (2, 300, 4096))])
+                                          (4096, 1000, 1024, (2, 300, 4096)), (1088, 20000, 20032, (200, 801, 1601)),
+                                          (1088, 13999, 14336, (128, 1101, 1401)), (2048, 20000, 20032, (150, 1101, 1401))])
 def test_bytes_do_not_depend_on_the_tiles(d, vr, vp, rows):
     n = max(rows)
     say(f"case: rows {rows} of a {vr} x {d} head")
