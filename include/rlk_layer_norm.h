@@ -28,7 +28,9 @@
  * at most 2^21; matrices, weight and bias 16-byte aligned.
  *
  * Memory: every pointer is caller-owned DEVICE memory; nothing is allocated,
- * freed or synchronised, and calls can be captured into a hipGraph. Argument
+ * freed or synchronised, and calls can be captured into a hipGraph. But for what
+ * is said of y and dx below, outputs must not overlap each other, the inputs
+ * (weight and statistics among them) or the workspace. Argument
  * errors detectable on the host return a negative status (codes of rlk_logp.h)
  * before any HIP call; n_rows is at most 2^22.
  */

@@ -1017,7 +1017,7 @@ def linear_logp_backward_merge(parts, *, out=None):
     linear_logp_backward's on the whole projection, byte for byte. BF16, or what a
     given ``out`` holds."""
     torch = _torch()
-    if parts.dim() != 3 or parts.dtype != torch.float32 or not parts.is_cuda or not parts[0].is_contiguous():
+    if parts.dim() != 3 or parts.dtype != torch.float32 or not parts.is_cuda or not len(parts) or not parts[0].is_contiguous():
         raise ValueError("parts must be a float32 device tensor [groups, n_rows, d_model] with contiguous parts")
     groups, n, d = parts.shape
     out = _grad_out(out, (n, d), torch.bfloat16, parts.device, "out")

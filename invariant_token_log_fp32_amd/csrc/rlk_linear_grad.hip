@@ -14,13 +14,15 @@
 // Kernels, in order:
 //   k_rows     per row the coefficients of G (those of rlk_logp_backward); rows
 //              without a gradient are left out, the others numbered in order
-//              (one workgroup: a running count over 1024 rows at a time)
+//              (one workgroup: a running count over 1024 rows at a time; 4 us up to
+//              640 rows, 23 for 8192)
 //   k_gather   the hidden states of the rows that remain, side by side; zeros
 //              into grad_hidden of the others
 //   k_product  <kLogits> x of some shards (bit for bit rlk_linear's), turned
 //              into G in the accumulators and stored in BF16
 //              <kHidden> G times the projection's rows, a partial sum for each
-//              shard; <kWeight> G^T times the hidden states
+//              shard
+//   k_weight   G^T times the hidden states
 //   k_combine  a row's partial sums added in the fixed order
 // The products run on the tiles of mfma_tiles.hpp, one workgroup a compute unit
 // looping over its tiles. What bounds them, at 4096 columns of hidden states and a

@@ -6,8 +6,9 @@ of every kernel of theirs:
   - an accumulator is a matrix instruction's source and destination at once
   - they all stand between the two waits of a sum, and nothing else there touches an
     accumulator register or memory of its own
-  - none of the two instructions in front of one is a vector instruction that writes
-    one of its operands (2 wait states; LDS reads are waited for by the counters)
+  - none of the two instructions in front of one, on any way to it, is a vector
+    instruction that writes one of its operands (2 wait states; LDS reads are waited for
+    by the counters)
   - nothing spills
 """
 import os
@@ -37,23 +38,36 @@ def kernels(tmp_path_factory):
     res = subprocess.run([build.hipcc(), *flags, "-I", build.INCLUDE, "-I", os.path.dirname(src), "-S",
                           "--cuda-device-only", "-o", out, src], capture_output=True, text=True, timeout=600)
     assert res.returncode == 0, res.stderr[-2000:]
-    found, name, text = {}, None, open(out).read()
+    found, labels, name, text = {}, {}, None, open(out).read()
     for line in text.splitlines():
         m = re.match(r"(_ZN\S*(?:k_product|k_weight)\S*):", line)
         if m:
             name = m.group(1)
-            found[name] = []
+            found[name], labels[name] = [], {}
+        elif name and re.match(r"\.LBB\S+:", line):
+            labels[name][line.split(":")[0]] = len(found[name])
         elif name and line.startswith("\t") and not line.strip().startswith((";", ".")):
             op, _, rest = line.split(";")[0].strip().partition(" ")
             op, _, more = op.partition("\t")
             found[name].append((op, [a.strip() for a in (more + " " + rest).split(",")]))
         elif line.startswith(".Lfunc_end"):
             name = None
-    return found, text
+    return found, labels, text
+
+
+def ways_to(code, labels):
+    """For each instruction those that may run just before it."""
+    before = [[] for _ in code]
+    for k, (op, a) in enumerate(code):
+        if op.startswith(("s_cbranch", "s_branch")):
+            before[labels[a[0]]].append(k)
+        if op not in ("s_branch", "s_endpgm") and k + 1 < len(code):
+            before[k + 1].append(k)
+    return before
 
 
 def test_products_have_their_waits(kernels):
-    found, _ = kernels
+    found, labels, _ = kernels
     assert len(found) >= 9
     for name, code in found.items():
         waits = [k for k, (op, a) in enumerate(code) if op == "s_nop" and a == ["15"]]
@@ -61,17 +75,19 @@ def test_products_have_their_waits(kernels):
         assert len(waits) == (16 if "k_product" in name else 4), (name, waits)  # one sum for each kind of tile
         inside = []
         for k in range(0, len(waits), 4):
-            before, last, after, end = waits[k:k + 4]
-            assert last == before + 1 and end == after + 1, (name, waits)
+            first, last, after, end = waits[k:k + 4]
+            assert last == first + 1 and end == after + 1, (name, waits)
             inside += range(last + 1, after)
         assert products and set(products) <= set(inside), name
+        before = ways_to(code, labels[name])
         for k in products:
             op, a = code[k]
             assert a[0] == a[3] and a[0].startswith("a["), (name, a)
             needed = registers(a[1]) | registers(a[2])
-            for near, b in code[k - 2:k]:
-                if near.startswith("v_") and not near.startswith("v_mfma"):
-                    assert not registers(b[0]) & needed, (name, near, b, a)
+            for near in set(before[k]) | {q for p in before[k] for q in before[p]}:
+                what, b = code[near]
+                if what.startswith("v_") and not what.startswith("v_mfma"):
+                    assert not registers(b[0]) & needed, (name, what, b, a)
         for k in inside:
             op, a = code[k]
             if not op.startswith("v_mfma"):
@@ -80,7 +96,7 @@ def test_products_have_their_waits(kernels):
 
 
 def test_products_do_not_spill(kernels):
-    found, text = kernels
+    found, _, text = kernels
     blocks = re.split(r"\n  - \.", text[text.index("amdhsa.kernels:"):])
     seen = 0
     for b in blocks:
