@@ -50,7 +50,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 
 struct BwdRow {
   float c;      // fl32(log2(e) / T)
-  float a_r;    // -lse * log2(e)
+  float a_r;    // -lse * log2(e) (-inf when the reference term is absent)
   float s_r;    // -g_r / T
   float a_p;    // -lse_S * log2(e)
   float s_p;    // -g_p / T (0 when the policy term is absent)

@@ -246,7 +246,8 @@ __device__ __forceinline__ int backward_row(int64_t row, int64_t vocab_real, con
   if (t == 0.0f) return 1;
   if (gp != 0.0f && status == -1) return 2;
   R.c = kLog2e / t;
-  R.a_r = grad_ref ? static_cast<float>(-static_cast<double>(lse[row]) * 1.4426950408889634) : 0.0f;
+  // without a reference term its power is 0 (2^(x c) alone overflows from x / T = 89 on: 0 * inf)
+  R.a_r = gr != 0.0f ? static_cast<float>(-static_cast<double>(lse[row]) * 1.4426950408889634) : -INFINITY;
   R.s_r = -gr / t;
   const float gpe = (status == 1) ? gp : 0.0f;
   R.s_p = -gpe / t;
