@@ -556,11 +556,17 @@ def l2norm(xs, *, workspace=None, sumsq_out=None, norm_out=None, stream=None):
 # LM-head linear and fused linear + logprob (include/rlk_linear.h)
 # ---------------------------------------------------------------------------
 
+def _row_stride(stride, n, d):
+    """The row stride to pass on of n rows of d values: with one row or none it has no meaning
+    (hidden[:, -1] of [1, length, d] has length * d, beyond what the library takes)."""
+    return stride if n > 1 else (d + 7) // 8 * 8
+
+
 def _bf16_matrix(x, name):
     torch = _torch()
     if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.int16, torch.uint16) or not x.is_cuda or x.stride(1) != 1:
         raise ValueError(f"{name} must be a 2-D device tensor of BF16 bits with contiguous rows")
-    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1])
+    return _row_stride(x.stride(0), *x.shape)
 
 
 def linear_logp_workspace_bytes(n_rows: int, vocab_padded: int, vocab_real: int) -> int:
@@ -921,7 +927,8 @@ def _grad_out(value, shape, dtype, device, name, f32_only=False):
     if value is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(value, torch.Tensor) or value.dtype not in ((torch.float32,) if f32_only else (torch.bfloat16, torch.float32)) \
-            or value.device != device or tuple(value.shape) != tuple(shape) or value.stride(1) != 1 or value.stride(0) % 8:
+            or value.device != device or tuple(value.shape) != tuple(shape) or value.stride(1) != 1 or \
+            _row_stride(value.stride(0), *shape) % 8:
         what = "float32" if f32_only else "bfloat16 or float32"
         raise ValueError(f"{name} must be a {what} tensor of shape {tuple(shape)} on {device} with contiguous rows, row "
                          f"stride a multiple of 8")
@@ -993,7 +1000,7 @@ def linear_logp_backward(hidden, weight, temperature, target, *, vocab_padded: i
         if not wanted:
             return None, 0, 0
         kind = GRAD_BF16 if t.dtype == torch.bfloat16 else GRAD_F32_ADD if add else GRAD_F32
-        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), d), kind
+        return t.data_ptr(), _row_stride(t.stride(0), *t.shape), kind
 
     spare = workspace.data_ptr() if workspace is not None else None
     gh = out(grad_hidden, hidden_grad)
@@ -1022,8 +1029,8 @@ def linear_logp_backward_merge(parts, *, out=None):
     groups, n, d = parts.shape
     out = _grad_out(out, (n, d), torch.bfloat16, parts.device, "out")
     _run("rlk_linear_logp_backward_merge", parts.device, parts.data_ptr(),
-         parts.stride(0) if groups > 1 else max(parts.stride(0), n * d), groups, n, d, out.data_ptr(),
-         out.stride(0) if n > 1 else max(out.stride(0), d), GRAD_BF16 if out.dtype == torch.bfloat16 else GRAD_F32)
+         parts.stride(0) if groups > 1 else n * d, groups, n, d, out.data_ptr(),
+         _row_stride(out.stride(0), n, d), GRAD_BF16 if out.dtype == torch.bfloat16 else GRAD_F32)
     return out
 
 
@@ -1054,8 +1061,7 @@ def _matrix(x, name, like=None, f32_too=True):
             strides = x.stride()
             if len(strides) == 2 and strides[1] == 1:
                 n, d = x.shape
-                return strides[0] if n > 1 else max((strides[0] + 7) // 8 * 8, (d + 7) // 8 * 8), \
-                    TYPE_BF16 if kind is torch.bfloat16 else TYPE_F32
+                return _row_stride(strides[0], n, d), TYPE_BF16 if kind is torch.bfloat16 else TYPE_F32
     raise ValueError(f"{name} must be a 2-D device tensor of bfloat16{' or float32' if f32_too else ''} values with contiguous rows"
                      + (f", of shape {tuple(like.shape)} on {like.device}" if like is not None else ""))
 
