@@ -13,8 +13,8 @@
  *   dx      = r * (g - c1 - xhat * mean(g * xhat)), c1 = mean(g) for
  *             RLK_NORM_LAYER, 0 for RLK_NORM_RMS
  *   dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy
- * A row whose dy holds only zeros has dx = 0, and a dy of 0 adds nothing to
- * dweight, whatever x, m and r hold there (padding).
+ * A row whose dy holds only zeros has dx = 0, whatever x, m, r and weight hold,
+ * and a dy of 0 adds nothing to dweight, whatever x, m and r hold there (padding).
  *
  * Order: y, the statistics and dx of a row depend on the row and d alone:
  * identical rows give identical bytes in any batch. dweight and dbias are

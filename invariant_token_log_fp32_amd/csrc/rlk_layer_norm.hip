@@ -274,7 +274,7 @@ __device__ __forceinline__ void backward_rows(const uint16_t* dy, int64_t lddy, 
         dw[v][e] = dw[v][e] + weight_term(g[v][e], hat);
         if (kBias) db[v][e] = db[v][e] + g[v][e];
         f[v][e] = hat;
-        g[v][e] = g[v][e] * wv[e];
+        g[v][e] = live ? g[v][e] * wv[e] : 0.0f;  // (0 times a weight that is no number would not be 0)
         q1[e] = g[v][e];
         q2[e] = g[v][e] * hat;
       }

@@ -28,7 +28,7 @@ def backward(dy, x, weight, mean, rstd, rms: bool):
     if not rms:
         c = c - np.where(live, np.asarray(mean, np.float64)[:, None], 0.0)
     hat = c * r
-    g = dy * np.asarray(weight, np.float64)
+    g = np.where(live, dy * np.asarray(weight, np.float64), 0.0)
     dx = g - hat * (g * hat).mean(1, keepdims=True)
     if not rms:
         dx = dx - g.mean(1, keepdims=True)
