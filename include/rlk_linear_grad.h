@@ -13,7 +13,7 @@
  * x_ij = bf16(sum_k h_ik * w_jk) the BF16 logits of rlk_linear (bit for bit):
  *   G_ij  = d/dx_ij of sum_i (grad_ref[i] * ref_i + grad_policy[i] * policy_i)
  *           as rlk_logp_backward defines it (both terms, the target column,
- *           the row rules), rounded to BF16 as there
+ *           the row rules), rounded to BF16 as there, whatever the outputs' types
  *   grad_hidden[i][k] = sum_j G_ij * w_jk
  *   grad_weight[j][k] = sum_i G_ij * h_ik
  * with float32 sums on the matrix cores, rounded once where the output is BF16.

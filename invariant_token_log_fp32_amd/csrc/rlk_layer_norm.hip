@@ -438,11 +438,17 @@ static int grid_for(int64_t n_rows, int64_t d, int resident) {
   return rows > 0 ? static_cast<int>((n_rows + rows - 1) / rows) : 0;
 }
 
-constexpr int kForwardThreads = 2048;   // resident threads a compute unit
+// Threads a compute unit that the forward walk is cut for. Fewer are resident: k_norm's
+// 80 to 90 registers leave 6 or 5 waves a SIMD (1536 or 1280 threads), 142 to 156 beyond d =
+// 8192 leave 3, so the last workgroups start when others end (4999 x 2080: 2500 workgroups, 2048
+// resident, 12.2 us on the GPU for 42 MB; 8192 x 4096 in float32 31 us at 6.4 TB/s).
+constexpr int kForwardThreads = 2048;
 
 // Calls f with the types, the vectors a thread and the largest workgroup as
 // constants (a bound of 1024 threads leaves 128 registers: spills, and 403 us
-// instead of 285 for the backward of 32768 x 8192).
+// instead of 285 for the backward of 32768 x 8192). The backward of float32 x beyond d =
+// 8192 with both sums still spills 14 registers (float32 weight: 32): 8192 x 16384 372 us, without
+// dbias, which spills nothing, 267.
 template <typename F>
 static void by_type(int x_type, int w_type, int64_t d, const F& f) {
   using B = std::integral_constant<int, RLK_TYPE_BF16>;

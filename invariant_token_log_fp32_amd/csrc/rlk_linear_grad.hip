@@ -26,11 +26,13 @@
 //   k_combine  a row's partial sums added in the fixed order
 // The products run on the tiles of mfma_tiles.hpp, one workgroup a compute unit
 // looping over its tiles. What bounds them, at 4096 columns of hidden states and a
-// vocabulary of 151936: one row reads the projection twice and writes its gradient at
-// 4.7 TB/s (0.80 ms; a large copy reaches 4.9); 8192 rows take 22.7 ms (1.35 PFLOP/s)
+// vocabulary of 151936: one row reads the projection twice and writes its gradient in
+// 0.78 ms (4.8 TB/s; a bare read and a fill reach 6.9, which would be 0.54): the logits pass takes
+// 256 to 316 us where grad_hidden takes 211 for the same bytes, of which a slice of the
+// logits has 64 in a row and one of grad_hidden 256. 8192 rows take 22.7 ms (1.35 PFLOP/s)
 // or, on a warm GPU, 24.6, as long as the three library products alone in the same loop
 // (1.24): the power limit; in between, rounds of tiles that the compute units share
-// unevenly (640 rows, grad_hidden alone, 1.53 ms: 1.05 PFLOP/s). Both operands of kWeight and the projection in kHidden
+// unevenly (640 rows, grad_hidden alone, 1.50 ms: 1.06 PFLOP/s). Both operands of kWeight and the projection in kHidden
 // run across K in memory; they are transposed on the way from LDS to registers,
 // so no transposed copy is written.
 #include <hip/hip_runtime.h>
@@ -352,7 +354,11 @@ __device__ __forceinline__ int lane_here() {
 }
 
 // G of the tile from its sums: BF16 logits (rounded to nearest even), the
-// gradient formula, BF16 again. Columns past the shard's real ones hold zeros.
+// gradient formula, BF16 again: the matrix cores' operand in both products that follow
+// (two BF16 parts would double them), of the type and bits of rlk_logp_backward. Each G is off
+// by at most 2^-8 of itself and 1.7e-3 as a root mean square, BF16 outputs by 2.0e-3 to 2.4e-3 of their norm
+// in batches (up to 3.4e-3 where few entries of G are large), of which 1.7e-3 is their own rounding.
+// Columns past the shard's real ones hold zeros.
 template <class S>
 __device__ __forceinline__ void store_g(const Args& a, int n_act, const Where& w, const f32x4 (&acc)[S::MB][S::NB]) {
   constexpr int kCols = S::NB * 16;       // of a wave
@@ -717,7 +723,9 @@ static int32_t product(const Args& a, int64_t n_rows, hipStream_t stream) {
 // Short tiles for few rows and few tiles (64 rows of an 8000 x 512 head 33 us a call,
 // with Large 37; 77 of 50021 x 1088, 1000 Large tiles, 103 and 106), Large ones
 // otherwise (64 rows of 151936 x 4096, 9500 tiles: 630 us with the logits, with Short
-// 682; 128 rows 737 and 829; 256 rows 930 and 1065).
+// 682; 128 rows 737 and 829; 256 rows 930 and 1065). The host chooses, by all rows; a small
+// head with many rows gets few Large tiles (8000 x 512: 64 for 256 compute units), which the
+// other products' choice by rounds would cut.
 template <int kType>
 static int32_t weight_product(const Args& a, int64_t n_rows, hipStream_t stream) {
   const int n = static_cast<int>(n_rows);
