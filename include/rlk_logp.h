@@ -207,7 +207,8 @@ int32_t rlk_logp_nucleus_noalloc(const uint16_t* logits, int64_t n_rows, const r
  *   ref_logp, lse [n_rows] float32: logp_out and lse_out of rlk_logp_full
  *                 (or ref_out and lse_out of rlk_logp_nucleus) on these rows
  *   grad_ref      [n_rows] float32 upstream gradient of ref_i, or NULL (no
- *                 reference term; ref_logp and lse may then be NULL)
+ *                 reference term; ref_logp and lse may then be NULL). Where it
+ *                 is 0 the row has no reference term and lse is not read
  *   policy_logp, support  [n_rows] policy_out and support_out of
  *                 rlk_logp_nucleus on these rows
  *   grad_policy   [n_rows] float32 upstream gradient of policy_i, or NULL (no
